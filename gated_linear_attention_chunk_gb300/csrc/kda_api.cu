@@ -473,6 +473,8 @@ kda_status kda_device_status(const void *workspace, void *stream) {
     if (word & kda::DEV_ERR_SLOT) return KDA_ERR_BAD_SLOT;
     if (word & kda::DEV_ERR_GATE) return KDA_ERR_GATE_RANGE;
     if (word & kda::DEV_ERR_TIMEOUT) return KDA_ERR_TIMEOUT;
+    if (word & kda::DEV_ERR_PAGE) return KDA_ERR_BAD_PAGE;
+    if (word & kda::DEV_ERR_TREE) return KDA_ERR_BAD_TREE;
     return KDA_OK;
 }
 
@@ -492,6 +494,8 @@ const char *kda_status_string(kda_status status) {
         case KDA_ERR_TIMEOUT: return "KDA_ERR_TIMEOUT";
         case KDA_ERR_BAD_SEQLENS: return "KDA_ERR_BAD_SEQLENS";
         case KDA_ERR_BAD_SLOT: return "KDA_ERR_BAD_SLOT";
+        case KDA_ERR_BAD_PAGE: return "KDA_ERR_BAD_PAGE";
+        case KDA_ERR_BAD_TREE: return "KDA_ERR_BAD_TREE";
     }
     return "KDA_ERR_UNKNOWN";
 }

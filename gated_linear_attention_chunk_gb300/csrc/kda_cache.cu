@@ -1,0 +1,138 @@
+// Append of new rows to a paged cache: the keys and values of a prompt, or of the accepted nodes of a
+// drafted tree (through their row indices), to the rows after each sequence's context.
+//
+// A pure copy, bounded by its bytes (each row read and written once).  One warp per token, found
+// among the sequences by a 32-way search; its lanes take 16 bytes of the token's heads at a time, all
+// loads of a batch before the first store.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_spec.cuh"
+
+namespace kda {
+namespace {
+
+using namespace spec;
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendUnroll = 4;  // 16-byte loads in flight per lane
+
+struct AppendParams {
+    const char *k, *v;
+    Pages c;
+    const int32_t *cu, *rows;
+    int32_t *new_len;
+    int64_t A_total, T_src, ks, vs;  // token strides in 16-byte units
+    int N, Hkv;
+    int kshift, vshift;              // log2 of a head's 16-byte units
+    uint32_t *status;
+};
+
+// A sequence's place in the packed rows and its context, checked.
+struct AppendSeq {
+    int64_t first, last, ctx;
+    uint32_t err;
+};
+__device__ __forceinline__ AppendSeq append_seq(const AppendParams &p, int n) {
+    AppendSeq s{p.cu[n], p.cu[n + 1], p.c.ctx_len[n], 0u};
+    if (s.first < 0 || s.first > s.last || s.last > p.A_total || (n == 0 && s.first != 0)) s.err = DEV_ERR_SEQLENS;
+    else if (s.ctx < 0 || s.ctx + (s.last - s.first) > static_cast<int64_t>(p.c.max_pages) * p.c.page_size)
+        s.err = DEV_ERR_PAGE;
+    return s;
+}
+
+// `units` 16-byte units from a packed row to the heads of one cache row.
+__device__ __forceinline__ void copy_row(const char *src, char *dst, int64_t head_bytes, int units, int shift) {
+    const int lane = threadIdx.x & 31;
+    for (int u0 = lane; u0 < units; u0 += 32 * kAppendUnroll) {
+        uint4 x[kAppendUnroll];
+#pragma unroll
+        for (int i = 0; i < kAppendUnroll; ++i)
+            if (u0 + 32 * i < units) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + u0 + 32 * i);
+#pragma unroll
+        for (int i = 0; i < kAppendUnroll; ++i) {
+            const int u = u0 + 32 * i;
+            if (u < units)
+                *reinterpret_cast<uint4 *>(dst + (u >> shift) * head_bytes + ((u & ((1 << shift) - 1)) << 4)) = x[i];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int64_t es) {
+    // new lengths, one thread per sequence
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
+    for (int64_t n = gid; n < p.N; n += static_cast<int64_t>(gridDim.x) * kAppendThreads) {
+        const AppendSeq s = append_seq(p, static_cast<int>(n));
+        if (s.err) atomicOr(p.status, s.err);
+        if (p.new_len) p.new_len[n] = static_cast<int32_t>(s.err ? s.ctx : s.ctx + s.last - s.first);
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t most = p.cu[p.N];
+    const int64_t total = most < p.A_total ? most : p.A_total;
+    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5); j < total;
+         j += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
+        const int n = warp_find([&](int i) { return p.cu[i]; }, p.N, j);
+        const AppendSeq s = append_seq(p, n);
+        if (s.err || j < s.first || j >= s.last) {
+            if (!s.err && lane == 0) atomicOr(p.status, DEV_ERR_SEQLENS);
+            continue;
+        }
+        const int64_t row = p.rows ? static_cast<int64_t>(p.rows[j]) : j;
+        const int64_t at = s.ctx + j - s.first;
+        const int64_t page = p.c.table[static_cast<int64_t>(n) * p.c.table_stride + at / p.c.page_size];
+        const int64_t slot = at % p.c.page_size;
+        const bool row_ok = row >= 0 && row < p.T_src, page_ok = page >= 0 && page < p.c.num_pages;
+        if (!row_ok || !page_ok) {
+            if (lane == 0) atomicOr(p.status, row_ok ? DEV_ERR_PAGE : DEV_ERR_SLOT);
+            continue;
+        }
+        copy_row(p.k + row * p.ks * 16, p.c.k + (page * p.c.kp + slot * p.c.kr) * es, p.c.kh * es, p.Hkv << p.kshift, p.kshift);
+        copy_row(p.v + row * p.vs * 16, p.c.v + (page * p.c.vp + slot * p.c.vr) * es, p.c.vh * es, p.Hkv << p.vshift, p.vshift);
+    }
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
+                            const int32_t *cu, const int32_t *rows, int N, int64_t A_total, int64_t T_src, int Hkv,
+                            int dk, int dv, int64_t k_stride, int64_t v_stride, int32_t *new_len, void *workspace,
+                            size_t ws_bytes, void *stream) {
+    using namespace kda::spec;
+    if (!dtype_ok(dtype) || !dim_ok(dk) || !dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
+    if (N < 0 || A_total < 0 || T_src < 0 || Hkv <= 0 || Hkv > 4096) return KDA_ERR_INVALID_ARGUMENT;
+    if (!workspace || !aligned_to(workspace, 16) || ws_bytes < KDA_WS_HEADER_BYTES) return KDA_ERR_WORKSPACE;
+    Pages c;
+    kda_status st = check_pages(cache, dtype, N, &c);
+    if (st != KDA_OK) return st;
+    const int es = static_cast<int>(elem_size(dtype)), vec = 16 / es;
+    if (!k_stride) k_stride = static_cast<int64_t>(Hkv) * dk;
+    if (!v_stride) v_stride = static_cast<int64_t>(Hkv) * dv;
+    if (k_stride < static_cast<int64_t>(Hkv) * dk || v_stride < static_cast<int64_t>(Hkv) * dv || k_stride % vec ||
+        v_stride % vec)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (N > 0 && (!cu || !aligned_to(cu, 4))) return KDA_ERR_INVALID_ARGUMENT;
+    if (A_total > 0 && T_src > 0 && (!k || !v)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!rows && A_total > T_src) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(rows, 4) || !aligned_to(new_len, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (new_len && new_len == cache->ctx_len) return KDA_ERR_INVALID_ARGUMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (N == 0) return KDA_OK;
+    auto shift = [&](int d) { int b = 0; for (int u = d / vec; u > 1; u >>= 1) ++b; return b; };
+    kda::AppendParams p{static_cast<const char *>(k), static_cast<const char *>(v), c, cu, rows, new_len, A_total, T_src,
+                        k_stride / vec, v_stride / vec, N, Hkv, shift(dk), shift(dv), static_cast<uint32_t *>(workspace)};
+    const int64_t work = A_total > N ? A_total : N;
+    const int64_t want = (work + kda::kAppendWarps - 1) / kda::kAppendWarps;
+    const int64_t most = static_cast<int64_t>(sm_count()) * 8;
+    if (most <= 0) return KDA_ERR_CUDA;
+    kda::append_kernel<<<static_cast<unsigned>(want < most ? want : most), kda::kAppendThreads, 0, s>>>(p, es);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -12,6 +12,8 @@ enum DeviceError : uint32_t {
     DEV_ERR_SLOT = 2u,     // slot outside [0, num_slots)
     DEV_ERR_GATE = 4u,     // a chunk's cumulative decay left the supported range
     DEV_ERR_TIMEOUT = 8u,  // a bounded wait gave up
+    DEV_ERR_PAGE = 16u,    // page outside the pool, or a context longer than its block table
+    DEV_ERR_TREE = 32u,    // a drafted node's parent or token is not valid
 };
 
 enum SeqMode : int {

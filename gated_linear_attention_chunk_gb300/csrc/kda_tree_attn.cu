@@ -1,0 +1,928 @@
+// Attention of drafted trees over a paged cache.
+//
+// Node i of a sequence attends to the sequence's context rows in the cache, to its ancestors among the
+// drafted nodes and to itself: o = sum_j softmax_j(scale q.k_j) v_j.  The G = Hq / Hkv query heads of a KV head and
+// the sequence's nodes form the R = m G rows of one matrix product per KV head, so that a
+// key or value is read once for all of them.
+//
+// One pass over the keys with a running maximum and sum per row (base-2 exponentials of
+// scale log2(e) q.k).  A sequence's context is cut into parts of `chunk` keys (split_of below); a unit
+// of work is (sequence, KV head, row tile, part), the last part taking the drafted nodes' own keys as one more
+// tile with the ancestor masks.  The units are numbered sequence by sequence; a persistent grid takes a
+// contiguous run of them per CTA and streams their key tiles through one ring of stages filled by 16-byte asynchronous
+// copies, across unit borders.  Parts leave their unnormalised sums, maximum and weight sum in the workspace and
+// combine_kernel joins them in part order.  Everything a unit does depends on its own sequence alone,
+// so a sequence's bits do not depend on the batch.
+//
+// plan_kernel, one launch before: checks the lengths, lists the sequences with their first unit, and
+// turns the parents into ancestor masks (one 64-bit word per node, by pointer doubling).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_spec.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+namespace {
+
+using namespace spec;
+
+constexpr int kTileRows = 64;    // query rows of a unit
+constexpr int kAttnThreads = 128;
+
+// One sequence as the plan leaves it.
+struct __align__(16) SeqInfo {
+    int ctx, nodes, t0, unit0;   // context, nodes, first packed node, first unit
+    int nsplit, chunk, tiles, pad;
+};
+
+struct AttnParams {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    Pages c;
+    const int32_t *cu, *parent;
+    int64_t T, qs, ks, vs;       // token strides in elements
+    int N, Hq, Hkv, G, max_nodes, max_splits;
+    float scale;
+    uint32_t *status;
+    SeqInfo *info;               // [N + 1]; entry N holds the number of units in unit0
+    uint32_t *bad;               // [N] a page or a parent of the sequence is not valid
+    int32_t *seq_of;             // [T] sequence of a packed node
+    uint64_t *sees;              // [T] ancestors of a packed node, itself included
+    float *part_o;               // [T, Hq, max_splits, dv]
+    float2 *part_ml;             // [T, Hq, max_splits] maximum (base 2) and sum
+};
+
+// How a sequence is cut: parts of at least 256 keys (more for many rows, whose partial results would outweigh the
+// keys they save), as many as give the sequence alone about one unit per SM, whatever else is in the batch.
+constexpr int kFillUnits = 152;
+__host__ __device__ inline int most_splits(int Hkv, int tiles) {
+    const int per = Hkv * tiles;
+    return per >= kFillUnits ? 1 : (kFillUnits + per - 1) / per;
+}
+__host__ __device__ inline int least_chunk(int rows) { return rows <= 16 ? 256 : rows <= 64 ? 16 * rows : 1024; }
+__host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, int *nsplit, int *chunk) {
+    const int least = least_chunk(rows);
+    int s = (ctx + least - 1) / least;
+    const int most = most_splits(Hkv, tiles);
+    s = s < 1 ? 1 : s > most ? most : s;
+    int c = (ctx + s - 1) / s;
+    c = (c + 63) / 64 * 64;
+    if (c < 64) c = 64;
+    *chunk = c;
+    *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
+}
+__host__ __device__ inline int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
+
+__device__ __forceinline__ uint32_t seq_check(const AttnParams &p, int n, int *t0, int *m, int *ctx) {
+    const int64_t a = p.cu[n], b = p.cu[n + 1], c = p.c.ctx_len[n];
+    *t0 = static_cast<int>(a);
+    *m = static_cast<int>(b - a);
+    *ctx = static_cast<int>(c);
+    if (a < 0 || a > b || b > p.T || b - a > p.max_nodes || (n == 0 && a != 0)) return DEV_ERR_SEQLENS;
+    if (c < 0 || c > static_cast<int64_t>(p.c.max_pages) * p.c.page_size) return DEV_ERR_PAGE;
+    return 0;
+}
+
+constexpr int kPlanThreads = 256;
+
+// CTA 0: the list of sequences and units, and the status word.  The others, a warp per sequence: masks.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) {
+        __shared__ int warp_tot[kPlanThreads / 32];
+        __shared__ int base_units;
+        __shared__ uint32_t errors;
+        if (threadIdx.x == 0) {
+            base_units = 0;
+            errors = 0;
+        }
+        __syncthreads();
+        for (int base = 0; base < p.N; base += kPlanThreads) {
+            const int n = base + threadIdx.x;
+            SeqInfo s{};
+            int units = 0;
+            if (n < p.N) {
+                const uint32_t err = seq_check(p, n, &s.t0, &s.nodes, &s.ctx);
+                if (err) atomicOr(&errors, err);
+                if (!err && s.nodes > 0) {
+                    const int rows = s.nodes * p.G;
+                    s.tiles = tiles_of(rows);
+                    split_of(s.ctx, rows, p.Hkv, s.tiles, &s.nsplit, &s.chunk);
+                    units = s.nsplit * s.tiles * p.Hkv;
+                }
+            }
+            int upto = units;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (lane == 31) warp_tot[warp] = upto;
+            __syncthreads();
+            int off = base_units;
+            for (int w = 0; w < warp; ++w) off += warp_tot[w];
+            s.unit0 = off + upto - units;
+            if (n < p.N) p.info[n] = s;
+            __syncthreads();
+            if (threadIdx.x == kPlanThreads - 1) base_units = off + upto;
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) {
+            SeqInfo s{};
+            s.unit0 = base_units;
+            p.info[p.N] = s;
+            *p.status = errors;
+        }
+        return;
+    }
+    const int n = (blockIdx.x - 1) * (kPlanThreads / 32) + warp;
+    if (n >= p.N) return;
+    int t0, m, ctx;
+    const bool ok = seq_check(p, n, &t0, &m, &ctx) == 0;
+    if (!ok) m = 0;
+    uint64_t mask[2];
+    int up[2];
+    bool wrong = false;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int i = lane + 32 * w;
+        up[w] = i < m && i > 0 ? (p.parent ? p.parent[t0 + i] : i - 1) : -1;
+        if (i > 0 && i < m && (up[w] < 0 || up[w] >= i)) {
+            wrong = true;
+            up[w] = -1;
+        }
+        mask[w] = i < 64 ? 1ull << i : 0ull;
+    }
+    // after round r a mask holds 2^r generations and `up` the next one
+#pragma unroll
+    for (int r = 0; r < 6; ++r) {
+        uint64_t grown[2];
+        int next[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int a = up[w] < 0 ? 0 : up[w];
+            const uint64_t m0 = __shfl_sync(0xffffffffu, mask[0], a & 31), m1 = __shfl_sync(0xffffffffu, mask[1], a & 31);
+            const int u0 = __shfl_sync(0xffffffffu, up[0], a & 31), u1 = __shfl_sync(0xffffffffu, up[1], a & 31);
+            grown[w] = up[w] < 0 ? mask[w] : mask[w] | (a < 32 ? m0 : m1);
+            next[w] = up[w] < 0 ? -1 : (a < 32 ? u0 : u1);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            mask[w] = grown[w];
+            up[w] = next[w];
+        }
+    }
+    wrong = __any_sync(0xffffffffu, wrong);
+    if (lane == 0) p.bad[n] = wrong ? DEV_ERR_TREE : 0u;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int i = lane + 32 * w;
+        if (i < m) {
+            p.sees[t0 + i] = mask[w];
+            p.seq_of[t0 + i] = n;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// The walk over a CTA's units and key tiles (one instance fills the ring, one consumes it)
+// ---------------------------------------------------------------------------------------------------------------
+struct Walk {
+    int unit, end;                      // units left: [unit, end)
+    int n, head, tile, split;           // of the unit
+    int ctx, nodes, t0, nsplit, chunk, tiles, next0;  // of the sequence; next0: the first unit after it
+    int key, key_end;                   // context keys left in the unit
+    int node, node_end;                 // drafted keys left in the unit
+
+    __device__ __forceinline__ void begin_unit() {
+        key = split * chunk;
+        key_end = key + chunk < ctx ? key + chunk : ctx;
+        node = 0;
+        node_end = split == nsplit - 1 ? nodes : 0;
+    }
+    __device__ __forceinline__ bool unit_done() const { return key >= key_end && node >= node_end; }
+    __device__ __forceinline__ void enter_seq(const AttnParams &p) {
+        // sequences without units (empty or bad) have the unit0 of the next one
+        int next = __ldg(&p.info[n + 1].unit0);
+        while (unit >= next && n + 1 < p.N) {
+            ++n;
+            next = __ldg(&p.info[n + 1].unit0);
+        }
+        const int4 a = __ldg(reinterpret_cast<const int4 *>(p.info + n));
+        const int4 b = __ldg(reinterpret_cast<const int4 *>(p.info + n) + 1);
+        ctx = a.x; nodes = a.y; t0 = a.z; nsplit = b.x; chunk = b.y; tiles = b.z;
+        next0 = next;
+        const int u = unit - a.w, ht = u / nsplit;
+        split = u - ht * nsplit;
+        head = ht / tiles;
+        tile = ht - head * tiles;
+        begin_unit();
+    }
+    // Every lane of a converged warp.
+    __device__ __forceinline__ void start(const AttnParams &p, int first, int last) {
+        unit = first;
+        end = last;
+        if (unit >= end) return;
+        n = warp_find([&](int i) { return __ldg(&p.info[i].unit0); }, p.N, unit);
+        enter_seq(p);
+    }
+    __device__ __forceinline__ void next_unit(const AttnParams &p) {
+        if (++unit >= end) return;
+        if (unit >= next0) {
+            ++n;
+            enter_seq(p);
+            return;
+        }
+        if (++split == nsplit) {
+            split = 0;
+            if (++tile == tiles) {
+                tile = 0;
+                ++head;
+            }
+        }
+        begin_unit();
+    }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+    const int n = there ? 16 : 0;  // 0: nothing is read and the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A key row of a tile: page and slot in the pools, or page kDrafted and the packed node; kNoRow: zeros.
+struct TileRow {
+    int page, slot;
+};
+constexpr int kNoRow = -1, kDrafted = -2;
+
+// The ring of key / value tiles.  A tile is kKeys rows of K, then kKeys rows of V; the 16-byte
+// units of a row are permuted by its low three row bits, so that both a column of eight rows and a row are read
+// without bank conflicts.
+template <typename T, int DK, int DV>
+struct Ring {
+    static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kStages = 3;
+    static constexpr int kUnitsK = DK * static_cast<int>(sizeof(T)) / 16, kUnitsV = DV * static_cast<int>(sizeof(T)) / 16;
+    static constexpr int kBytesK = kKeys * kUnitsK * 16, kBytesV = kKeys * kUnitsV * 16;
+    static constexpr int kStage = kBytesK + kBytesV;
+
+    char *smem;                  // kStages * kStage bytes
+    TileRow (*rows)[kKeys];      // [2]: rows of the next tile to be issued, by tile parity
+    int *bad_seen;               // a page of this CTA's units was out of range
+    Walk w;                      // the tile after the one whose rows were looked up last
+    int tile;                    // tiles consumed so far
+    int head;                    // head of the looked-up tile
+    bool any;                    // there is one
+
+    // Rows of the walk's tile; moves the walk past it.  Every thread takes part, threads < kKeys have a row.
+    __device__ __forceinline__ TileRow look(const AttnParams &p) {
+        TileRow r{kNoRow, 0};
+        if (w.unit >= w.end) {
+            any = false;
+            return r;
+        }
+        const int j = threadIdx.x;
+        head = w.head;
+        any = true;
+        if (w.key < w.key_end) {
+            if (j < kKeys && w.key + j < w.key_end) {
+                const int at = w.key + j, pg = at / p.c.page_size;
+                r.slot = at - pg * p.c.page_size;
+                r.page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
+                if (r.page < 0 || r.page >= p.c.num_pages) {
+                    r.page = kNoRow;
+                    atomicOr(p.bad + w.n, static_cast<uint32_t>(DEV_ERR_PAGE));
+                    atomicOr(p.status, static_cast<uint32_t>(DEV_ERR_PAGE));
+                    *bad_seen = 1;
+                }
+            }
+            w.key += kKeys;
+        } else {
+            if (j < kKeys && w.node + j < w.node_end) r = TileRow{kDrafted, w.t0 + w.node + j};
+            w.node += kKeys;
+        }
+        if (w.unit_done()) w.next_unit(p);
+        return r;
+    }
+    __device__ __forceinline__ void put(TileRow r, int parity) {
+        if (threadIdx.x < kKeys) rows[parity][threadIdx.x] = r;
+    }
+    template <int kUnits>
+    __device__ __forceinline__ void copy(uint32_t dst, const TileRow *tr, const char *pages, int64_t ps, int64_t rs,
+                                         const char *fresh, int64_t ts) {
+        constexpr int kRowsPer = kAttnThreads / kUnits;  // rows side by side
+        const int u = threadIdx.x % kUnits;
+#pragma unroll
+        for (int i = 0; i < kKeys / kRowsPer; ++i) {
+            const int r = threadIdx.x / kUnits + i * kRowsPer;
+            const TileRow x = tr[r];
+            const char *src = x.page == kDrafted ? fresh + x.slot * ts : pages + (x.page == kNoRow ? 0 : x.page * ps + x.slot * rs);
+            cp16(dst + r * (kUnits * 16) + ((u ^ (r & 7)) << 4), src + u * 16, x.page != kNoRow);
+        }
+    }
+    // Starts the copies of the looked-up tile of the given number.
+    __device__ __forceinline__ void issue(const AttnParams &p, int number) {
+        const int parity = number & 1;
+        if (any) {
+            constexpr int64_t es = sizeof(T);
+            const int64_t h = head;
+            const uint32_t dst = ptx::smem_u32(smem) + static_cast<uint32_t>(number % kStages) * kStage;
+            copy<kUnitsK>(dst, rows[parity], p.c.k + h * p.c.kh * es, p.c.kp * es, p.c.kr * es,
+                          static_cast<const char *>(p.k) + h * DK * es, p.ks * es);
+            copy<kUnitsV>(dst + kBytesK, rows[parity], p.c.v + h * p.c.vh * es, p.c.vp * es, p.c.vr * es,
+                          static_cast<const char *>(p.v) + h * DV * es, p.vs * es);
+        }
+        cp_commit();
+    }
+    __device__ __forceinline__ void start(const AttnParams &p, int first, int last) {
+        tile = 0;
+        w.start(p, first, last);
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) {
+            put(look(p), i & 1);
+            __syncthreads();
+            if (i < kStages - 1) issue(p, i);
+        }
+    }
+    // Waits for the next tile, refills the stage freed before it, and looks one tile further; returns the
+    // looked-up row, to be stored by end_tile after the tile's work (its latency is covered by it).
+    __device__ __forceinline__ TileRow begin_tile(const AttnParams &p) {
+        cp_wait<kStages - 2>();
+        __syncthreads();
+        issue(p, tile + kStages - 1);
+        return look(p);
+    }
+    __device__ __forceinline__ void end_tile(TileRow r) {
+        put(r, (tile + kStages) & 1);
+        ++tile;
+    }
+    __device__ __forceinline__ const char *stage() const { return smem + (tile % kStages) * kStage; }
+    // The stage of the last consumed tile: free from a barrier after end_tile up to the next begin_tile.
+    __device__ __forceinline__ char *scratch() const { return smem + ((tile + kStages - 1) % kStages) * kStage; }
+};
+
+// Whether a unit of the walk's sequence may write: `flag` is what the plan left (a bad parent); a bad
+// page can only have been met by this CTA itself if it matters here (a unit that writes o has seen all pages).
+__device__ __forceinline__ bool may_write(const AttnParams &p, int n, uint32_t flag, int *bad_seen) {
+    if (*reinterpret_cast<volatile int *>(bad_seen)) flag |= __ldcg(p.bad + n);
+    return flag == 0;
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// bf16: 16-row fragments of mma.sync, RW of the four warps on different rows and the rest on different keys
+// ---------------------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DK, int DV, int RW>
+__device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat16, DK, DV> &ring, Walk &cw, float2 (*ml)[16]) {
+    using R = Ring<__nv_bfloat16, DK, DV>;
+    constexpr int KW = 4 / RW, NT = 8 / KW;  // warps along the keys; 8-key columns of a warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rg = warp % RW, kg = warp / RW, key0 = kg * (64 / KW);
+    const int quad = lane >> 2, two = (lane & 3) * 2;
+    const int n = cw.n, t0 = cw.t0, split = cw.split, nsplit = cw.nsplit, rows = cw.nodes * p.G;
+    const uint32_t flag = __ldcg(p.bad + n);
+    const float c = p.scale * kLog2e;
+
+    // this thread's two rows: node and query head
+    int node[2], hq[2];
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = cw.tile * kTileRows + rg * 16 + quad + 8 * i;
+        live[i] = r < rows;
+        node[i] = live[i] ? r / p.G : 0;
+        hq[i] = cw.head * p.G + (live[i] ? r - node[i] * p.G : 0);
+    }
+    uint32_t qf[DK / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) + (t0 + node[i]) * p.qs + static_cast<int64_t>(hq[i]) * DK + two;
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+            qf[k][i] = live[i] ? *reinterpret_cast<const uint32_t *>(src + k * 16) : 0u;
+            qf[k][2 + i] = live[i] ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8) : 0u;
+        }
+    }
+    float o[DV / 8][4];
+#pragma unroll
+    for (int j = 0; j < DV / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+
+    while (!cw.unit_done()) {
+        const bool drafted = cw.key >= cw.key_end;
+        const int first = drafted ? cw.node : 0;
+        const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;  // keys from here on
+        if (drafted) cw.node += R::kKeys; else cw.key += R::kKeys;
+        const TileRow ahead = ring.begin_tile(p);
+        const uint32_t ks = ptx::smem_u32(ring.stage()), vs = ks + R::kBytesK;
+        // scores of 16 rows x NT * 8 keys
+        float s[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+                const int row = key0 + (j + (lane >> 4)) * 8 + (lane & 7), u = 2 * k + ((lane >> 3) & 1);
+                uint32_t b[4];
+                ldm4(b, ks + row * (R::kUnitsK * 16) + ((u ^ (row & 7)) << 4));
+                mma16816(s[j], qf[k], b[0], b[1]);
+                mma16816(s[j + 1], qf[k], b[2], b[3]);
+            }
+        uint64_t sees[2] = {~0ull, ~0ull};
+        if (drafted) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sees[i] = __ldg(p.sees + t0 + node[i]) >> first;
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = key0 + j * 8 + two + (e & 1);
+                float t = s[j][e] * c;
+                if (key >= count || !((sees[e >> 1] >> key) & 1)) t = -INFINITY;
+                s[j][e] = t;
+                top[e >> 1] = fmaxf(top[e >> 1], t);
+            }
+        float old[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+            const float now = fmaxf(mx[i], top[i]);
+            const float base = now == -INFINITY ? 0.f : now;
+            old[i] = ex2(mx[i] - base);
+            mx[i] = now;
+            top[i] = base;
+            sum[i] *= old[i];
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                e[x] = ex2(s[j][x] - top[x >> 1]);
+                sum[x >> 1] += e[x];
+            }
+            pf[j][0] = ptx::pack_bf16x2(e[0], e[1]);
+            pf[j][1] = ptx::pack_bf16x2(e[2], e[3]);
+        }
+        if (__any_sync(0xffffffffu, old[0] != 1.f || old[1] != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < DV / 8; ++j) {
+                o[j][0] *= old[0];
+                o[j][1] *= old[0];
+                o[j][2] *= old[1];
+                o[j][3] *= old[1];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NT / 2; ++k) {
+            const uint32_t a[4] = {pf[2 * k][0], pf[2 * k][1], pf[2 * k + 1][0], pf[2 * k + 1][1]};
+#pragma unroll
+            for (int j = 0; j < DV / 8; j += 2) {
+                const int row = key0 + k * 16 + (lane & 15), u = j + (lane >> 4);
+                uint32_t b[4];
+                ldm4t(b, vs + row * (R::kUnitsV * 16) + ((u ^ (row & 7)) << 4));
+                mma16816(o[j], a, b[0], b[1]);
+                mma16816(o[j + 1], a, b[2], b[3]);
+            }
+        }
+        ring.end_tile(ahead);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    }
+    if constexpr (KW > 1) {
+        // the warps along the keys are joined in order by the first of them
+        float *buf = reinterpret_cast<float *>(ring.scratch());
+        __syncthreads();  // the last tile's readers are done with the stage
+        if ((lane & 3) == 0) {
+            ml[warp][quad] = make_float2(mx[0], sum[0]);
+            ml[warp][quad + 8] = make_float2(mx[1], sum[1]);
+        }
+        if (kg > 0) {
+            float *to = buf + ((kg - 1) * RW + rg) * (16 * DV) + lane;
+#pragma unroll
+            for (int j = 0; j < DV / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) to[(j * 4 + e) * 32] = o[j][e];
+        }
+        __syncthreads();
+        if (kg == 0) {
+            float f[KW][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float m = mx[i];
+#pragma unroll
+                for (int g = 1; g < KW; ++g) m = fmaxf(m, ml[g * RW + rg][quad + 8 * i].x);
+                const float base = m == -INFINITY ? 0.f : m;
+                float l = 0.f;
+#pragma unroll
+                for (int g = 0; g < KW; ++g) {
+                    const float2 x = ml[g * RW + rg][quad + 8 * i];
+                    f[g][i] = ex2(x.x - base);
+                    l += f[g][i] * x.y;
+                }
+                mx[i] = m;
+                sum[i] = l;
+            }
+#pragma unroll
+            for (int j = 0; j < DV / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = f[0][e >> 1] * o[j][e];
+#pragma unroll
+                    for (int g = 1; g < KW; ++g) x += f[g][e >> 1] * buf[((g - 1) * RW + rg) * (16 * DV) + lane + (j * 4 + e) * 32];
+                    o[j][e] = x;
+                }
+        }
+    }
+    if (kg == 0) {
+        const bool ok = may_write(p, n, flag, ring.bad_seen);
+        if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!live[i] || !ok) continue;
+            const int64_t row = static_cast<int64_t>(t0 + node[i]) * p.Hq + hq[i];
+            if (nsplit == 1) {
+                const float inv = 1.f / sum[i];
+                uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + row * DV + two);
+#pragma unroll
+                for (int j = 0; j < DV / 8; ++j) to[j * 4] = ptx::pack_bf16x2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+                if (p.lse && (lane & 3) == 0) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
+            } else {
+                const int64_t at = row * p.max_splits + split;
+                float2 *to = reinterpret_cast<float2 *>(p.part_o + at * DV + two);
+#pragma unroll
+                for (int j = 0; j < DV / 8; ++j) to[j * 4] = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+                if ((lane & 3) == 0) p.part_ml[at] = make_float2(mx[i], sum[i]);
+            }
+        }
+    }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kAttnThreads, 2) attn_bf16_kernel(const AttnParams p) {
+    using R = Ring<__nv_bfloat16, DK, DV>;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ TileRow rows[2][R::kKeys];
+    __shared__ float2 ml[4][16];
+    __shared__ int bad_seen;
+    const int64_t units = __ldg(&p.info[p.N].unit0);
+    const int first = static_cast<int>(units * blockIdx.x / gridDim.x);
+    const int last = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    if (first >= last) return;
+    if (threadIdx.x == 0) bad_seen = 0;
+    __syncthreads();
+    R ring;
+    ring.smem = smem;
+    ring.rows = rows;
+    ring.bad_seen = &bad_seen;
+    Walk cw;
+    cw.start(p, first, last);
+    ring.start(p, first, last);
+    while (cw.unit < cw.end) {
+        const int left = cw.nodes * p.G - cw.tile * kTileRows;
+        if (left <= 16) unit_bf16<DK, DV, 1>(p, ring, cw, ml);
+        else if (left <= 32) unit_bf16<DK, DV, 2>(p, ring, cw, ml);
+        else unit_bf16<DK, DV, 4>(p, ring, cw, ml);
+        cw.next_unit(p);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// fp32: fused multiply-adds; warp w has rows w, w + 4, .. of the tile, a lane one key of the scores and DV / 32 columns
+// ---------------------------------------------------------------------------------------------------------------
+constexpr int kRowsPerWarp = kTileRows / 4;
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kAttnThreads) attn_f32_kernel(const AttnParams p) {
+    using R = Ring<float, DK, DV>;
+    constexpr int VL = DV / 32;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ TileRow rows[2][R::kKeys];
+    __shared__ int bad_seen;
+    float *qs = reinterpret_cast<float *>(smem + R::kStages * R::kStage);  // [kTileRows][DK]
+    float *ps = qs + kTileRows * DK;                                       // [kTileRows][32]
+    const int64_t units = __ldg(&p.info[p.N].unit0);
+    const int begin = static_cast<int>(units * blockIdx.x / gridDim.x);
+    const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    if (begin >= end) return;
+    if (threadIdx.x == 0) bad_seen = 0;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    R ring;
+    ring.smem = smem;
+    ring.rows = rows;
+    ring.bad_seen = &bad_seen;
+    Walk cw;
+    cw.start(p, begin, end);
+    ring.start(p, begin, end);
+    const float c = p.scale * kLog2e;
+    while (cw.unit < cw.end) {
+        const int n = cw.n, t0 = cw.t0, row0 = cw.tile * kTileRows, all = cw.nodes * p.G, split = cw.split;
+        const int here = all - row0 < kTileRows ? all - row0 : kTileRows;
+        const uint32_t flag = __ldcg(p.bad + n);
+        // a warp's own rows of q (the other warps do not read them)
+        for (int r = warp; r < here; r += 4) {
+            const int nd = (row0 + r) / p.G, h = cw.head * p.G + (row0 + r) - nd * p.G;
+            const float *src = static_cast<const float *>(p.q) + (t0 + nd) * p.qs + static_cast<int64_t>(h) * DK;
+            for (int d = lane; d < DK / 4; d += 32)
+                reinterpret_cast<float4 *>(qs + r * DK)[d] = reinterpret_cast<const float4 *>(src)[d];
+        }
+        __syncwarp();
+        float o[kRowsPerWarp][VL], mx[kRowsPerWarp], sum[kRowsPerWarp];
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+            mx[i] = -INFINITY;
+            sum[i] = 0.f;
+#pragma unroll
+            for (int x = 0; x < VL; ++x) o[i][x] = 0.f;
+        }
+        while (!cw.unit_done()) {
+            const bool drafted = cw.key >= cw.key_end;
+            const int first = drafted ? cw.node : 0;
+            const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;
+            if (drafted) cw.node += R::kKeys; else cw.key += R::kKeys;
+            const TileRow ahead = ring.begin_tile(p);
+            const char *ks = ring.stage(), *vs = ks + R::kBytesK;
+            float s[kRowsPerWarp];
+#pragma unroll
+            for (int i = 0; i < kRowsPerWarp; ++i) s[i] = 0.f;
+#pragma unroll 2
+            for (int d = 0; d < DK / 4; ++d) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + lane * (R::kUnitsK * 16) + ((d ^ (lane & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < kRowsPerWarp; ++i)
+                    if (warp + 4 * i < here) {
+                        const float4 q4 = reinterpret_cast<const float4 *>(qs + (warp + 4 * i) * DK)[d];
+                        s[i] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[i]))));
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < kRowsPerWarp; ++i)
+                if (warp + 4 * i < here) {
+                    const int r = warp + 4 * i;
+                    float t = s[i] * c;
+                    bool seen = lane < count;
+                    if (drafted) seen = seen && ((__ldg(p.sees + t0 + (row0 + r) / p.G) >> (first + lane)) & 1);
+                    if (!seen) t = -INFINITY;
+                    float top = t;
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float now = fmaxf(mx[i], top), base = now == -INFINITY ? 0.f : now;
+                    const float old = exp2f(mx[i] - base), e = exp2f(t - base);
+                    mx[i] = now;
+                    float tot = e;
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, x);
+                    sum[i] = sum[i] * old + tot;
+#pragma unroll
+                    for (int x = 0; x < VL; ++x) o[i][x] *= old;
+                    ps[r * 32 + lane] = e;
+                }
+            __syncwarp();
+#pragma unroll 1
+            for (int j = 0; j < 32; j += 4) {
+                float v[4][VL];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int key = j + y, u = lane * VL / 4;
+                    const char *at = vs + key * (R::kUnitsV * 16) + ((u ^ (key & 7)) << 4) + (lane * VL % 4) * 4;
+#pragma unroll
+                    for (int x = 0; x < VL; x += 2) *reinterpret_cast<float2 *>(&v[y][x]) = *reinterpret_cast<const float2 *>(at + 4 * x);
+                }
+#pragma unroll
+                for (int i = 0; i < kRowsPerWarp; ++i)
+                    if (warp + 4 * i < here) {
+                        const float4 e = *reinterpret_cast<const float4 *>(ps + (warp + 4 * i) * 32 + j);
+#pragma unroll
+                        for (int x = 0; x < VL; ++x)
+                            o[i][x] = fmaf(e.x, v[0][x], fmaf(e.y, v[1][x], fmaf(e.z, v[2][x], fmaf(e.w, v[3][x], o[i][x]))));
+                    }
+            }
+            __syncwarp();
+            ring.end_tile(ahead);
+        }
+        __syncthreads();  // bad_seen of this unit's look-ups
+        const bool ok = may_write(p, n, flag, ring.bad_seen);
+        if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i)
+            if (ok && warp + 4 * i < here) {
+                const int r = row0 + warp + 4 * i, nd = r / p.G, h = cw.head * p.G + r - nd * p.G;
+                const int64_t row = static_cast<int64_t>(t0 + nd) * p.Hq + h;
+                const bool whole = cw.nsplit == 1;
+                const int64_t at = row * p.max_splits + split;
+                const float f = whole ? 1.f / sum[i] : 1.f;
+                float *to = (whole ? static_cast<float *>(p.o) + row * DV : p.part_o + at * DV) + lane * VL;
+#pragma unroll
+                for (int x = 0; x < VL; x += 2) *reinterpret_cast<float2 *>(to + x) = make_float2(o[i][x] * f, o[i][x + 1] * f);
+                if (lane == 0) {
+                    if (!whole) p.part_ml[at] = make_float2(mx[i], sum[i]);
+                    else if (p.lse) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
+                }
+            }
+        cw.next_unit(p);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// The parts of a row joined in order: one warp per (node, query head), a lane DV / 32 columns
+// ---------------------------------------------------------------------------------------------------------------
+template <typename T, int DV>
+__global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams p) {
+    constexpr int VL = DV / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 32) + (threadIdx.x >> 5);
+    if (row >= p.T * p.Hq) return;
+    const int64_t t = row / p.Hq;
+    if (t >= p.cu[p.N]) return;                       // packed nodes beyond the last sequence
+    const int n = p.seq_of[t];
+    if (n < 0 || n >= p.N) return;
+    const SeqInfo s = p.info[n];
+    if (s.nsplit <= 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
+    float m = -INFINITY;
+    for (int i = lane; i < s.nsplit; i += 32) m = fmaxf(m, p.part_ml[row * p.max_splits + i].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[VL] = {};
+#pragma unroll 4
+    for (int i = 0; i < s.nsplit; ++i) {
+        const int64_t at = row * p.max_splits + i;
+        const float2 ml = p.part_ml[at];
+        const float f = exp2f(ml.x - base);
+        l = fmaf(f, ml.y, l);
+#pragma unroll
+        for (int x = 0; x < VL; x += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(p.part_o + at * DV + lane * VL + x);
+            o[x] = fmaf(f, v.x, o[x]);
+            o[x + 1] = fmaf(f, v.y, o[x + 1]);
+        }
+    }
+    const float inv = 1.f / l;
+    T *to = static_cast<T *>(p.o) + row * DV + lane * VL;
+#pragma unroll
+    for (int x = 0; x < VL; ++x) to[x] = Elem<T>::from_f(o[x] * inv);
+    if (p.lse && lane == 0) p.lse[row] = (m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------------------------------------------
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct AttnLayout {
+    size_t info, bad, seq_of, sees, part_ml, part_o, total;
+    int max_splits, max_tiles;
+};
+AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
+    AttnLayout l{};
+    // a sequence of few rows has the most parts; G rows are the fewest
+    l.max_tiles = tiles_of(max_nodes * (Hq / Hkv));
+    const int64_t by_len = (max_ctx + least_chunk(1) - 1) / least_chunk(1);
+    const int64_t most = most_splits(Hkv, 1);
+    l.max_splits = static_cast<int>(by_len < 1 ? 1 : by_len < most ? by_len : most);
+    size_t off = KDA_WS_HEADER_BYTES;
+    auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
+    l.info = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
+    l.bad = take(static_cast<size_t>(N) * 4);
+    l.seq_of = take(static_cast<size_t>(T) * 4);
+    l.sees = take(static_cast<size_t>(T) * 8);
+    const size_t parts = l.max_splits > 1 ? static_cast<size_t>(T) * Hq * l.max_splits : 0;
+    l.part_ml = take(parts * sizeof(float2));
+    l.part_o = take(parts * dv * sizeof(float));
+    l.total = off;
+    return l;
+}
+
+template <typename F>
+kda_status with_smem(F kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess
+               ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <int DK, int DV>
+kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cudaStream_t s) {
+    const int sms = sm_count();
+    if (sms <= 0) return KDA_ERR_CUDA;
+    const int64_t seq_ctas = (static_cast<int64_t>(p.N) + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
+    plan_kernel<<<static_cast<unsigned>(1 + seq_ctas), kPlanThreads, 0, s>>>(p);
+    const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * max_tiles;
+    const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? 2 : 1);
+    const unsigned grid = static_cast<unsigned>(units < most ? units : most);
+    kda_status st;
+    if (dtype == KDA_BF16) {
+        using R = Ring<__nv_bfloat16, DK, DV>;
+        const size_t smem = R::kStages * R::kStage;
+        if ((st = with_smem(attn_bf16_kernel<DK, DV>, smem)) != KDA_OK) return st;
+        attn_bf16_kernel<DK, DV><<<grid, kAttnThreads, smem, s>>>(p);
+    } else {
+        using R = Ring<float, DK, DV>;
+        const size_t smem = R::kStages * R::kStage + kTileRows * (DK + 32) * sizeof(float);
+        if ((st = with_smem(attn_f32_kernel<DK, DV>, smem)) != KDA_OK) return st;
+        attn_f32_kernel<DK, DV><<<grid, kAttnThreads, smem, s>>>(p);
+    }
+    if (p.max_splits > 1) {
+        const int64_t rows = p.T * p.Hq;
+        const unsigned cg = static_cast<unsigned>((rows + kAttnThreads / 32 - 1) / (kAttnThreads / 32));
+        if (dtype == KDA_BF16) combine_kernel<__nv_bfloat16, DV><<<cg, kAttnThreads, 0, s>>>(p);
+        else combine_kernel<float, DV><<<cg, kAttnThreads, 0, s>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+size_t kda_tree_attn_workspace_size(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
+    if (N < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !kda::spec::dim_ok(dv) || max_nodes < 1 ||
+        max_nodes > KDA_MAX_TREE_NODES || max_ctx < 0)
+        return 0;
+    return kda::layout_of(N, T, Hq, Hkv, dv, max_nodes, max_ctx).total;
+}
+
+kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
+                         const int32_t *cu_nodes, const int32_t *parent, int N, int64_t T, int Hq, int Hkv, int dk,
+                         int dv, int64_t q_stride, int64_t k_stride, int64_t v_stride, int max_nodes, float scale,
+                         void *o, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    using namespace kda::spec;
+    if (!dtype_ok(dtype) || !dim_ok(dk) || !dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
+    if (N < 0 || N > (1 << 20) || T < 0 || T > 0x7fffffffLL || Hq <= 0 || Hkv <= 0 || Hq > 4096 || Hq % Hkv)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (max_nodes < 1 || max_nodes > KDA_MAX_TREE_NODES || T > static_cast<int64_t>(N) * max_nodes) return KDA_ERR_INVALID_ARGUMENT;
+    Pages c;
+    kda_status st = check_pages(cache, dtype, N, &c);
+    if (st != KDA_OK) return st;
+    const int64_t max_ctx = static_cast<int64_t>(c.page_size) * c.max_pages;
+    if (!workspace || !aligned_to(workspace, 16) ||
+        ws_bytes < kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx))
+        return KDA_ERR_WORKSPACE;
+    const int64_t vec = 16 / static_cast<int64_t>(elem_size(dtype));
+    if (!q_stride) q_stride = static_cast<int64_t>(Hq) * dk;
+    if (!k_stride) k_stride = static_cast<int64_t>(Hkv) * dk;
+    if (!v_stride) v_stride = static_cast<int64_t>(Hkv) * dv;
+    if (q_stride < static_cast<int64_t>(Hq) * dk || k_stride < static_cast<int64_t>(Hkv) * dk ||
+        v_stride < static_cast<int64_t>(Hkv) * dv || q_stride % vec || k_stride % vec || v_stride % vec)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (N > 0 && (!cu_nodes || !aligned_to(cu_nodes, 4) || !aligned_to(parent, 4))) return KDA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const kda::AttnLayout l = kda::layout_of(N, T, Hq, Hkv, dv, max_nodes, max_ctx);
+    if (static_cast<int64_t>(N) * Hkv * l.max_splits * l.max_tiles > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0 || T == 0) return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    char *ws = static_cast<char *>(workspace);
+    kda::AttnParams p{};
+    p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse; p.c = c; p.cu = cu_nodes; p.parent = parent;
+    p.T = T; p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
+    p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.max_nodes = max_nodes; p.max_splits = l.max_splits; p.scale = scale;
+    p.status = reinterpret_cast<uint32_t *>(ws);
+    p.info = reinterpret_cast<kda::SeqInfo *>(ws + l.info);
+    p.bad = reinterpret_cast<uint32_t *>(ws + l.bad);
+    p.seq_of = reinterpret_cast<int32_t *>(ws + l.seq_of);
+    p.sees = reinterpret_cast<uint64_t *>(ws + l.sees);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
+    p.part_o = reinterpret_cast<float *>(ws + l.part_o);
+    if (dk == 128) return dv == 128 ? kda::launch_attn<128, 128>(p, dtype, l.max_tiles, s) : kda::launch_attn<128, 64>(p, dtype, l.max_tiles, s);
+    return dv == 128 ? kda::launch_attn<64, 128>(p, dtype, l.max_tiles, s) : kda::launch_attn<64, 64>(p, dtype, l.max_tiles, s);
+}
+
+}  // extern "C"

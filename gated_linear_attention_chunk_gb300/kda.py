@@ -29,6 +29,8 @@ KDA_ERR_GATE_RANGE = 5
 KDA_ERR_TIMEOUT = 6
 KDA_ERR_BAD_SEQLENS = 7
 KDA_ERR_BAD_SLOT = 8
+KDA_ERR_BAD_PAGE = 9
+KDA_ERR_BAD_TREE = 10
 KDA_BF16 = 0
 KDA_F32 = 1
 KDA_WS_HEADER_BYTES = 256
@@ -79,6 +81,18 @@ _SIGS = {
     "kda_state_fork": (_int, [_vp, _i64, _vp, _vp, _int, _int, _int, _int, _vp, ctypes.c_size_t, _vp]),
     "kda_state_offload": (_int, [_vp, _i64, _vp, _int, _int, _int, _int, _vp, _vp, ctypes.c_size_t, _vp]),
     "kda_state_restore": (_int, [_vp, _i64, _vp, _int, _int, _int, _int, _vp, _vp, ctypes.c_size_t, _vp]),
+    "kda_rope": (_int, [_vp, _vp, _int, _vp, _vp, _i64, _int, _int, _int, _int, _i64, _i64, _int, ctypes.c_float, _vp,
+                        _vp, _i64, _i64, _vp]),
+    "kda_rope_bwd": (_int, [_vp, _vp, _int, _vp, _vp, _i64, _int, _int, _int, _int, _i64, _i64, _int, ctypes.c_float,
+                            _vp, _vp, _i64, _i64, _vp]),
+    "kda_tree_attn_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int, _i64]),
+    "kda_tree_attn": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _int, _int, _int, _int, _i64, _i64, _i64,
+                             _int, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "kda_cache_append": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _i64, _int, _int, _int, _i64, _i64, _vp, _vp,
+                                ctypes.c_size_t, _vp]),
+    "kda_draft_verify_workspace_size": (ctypes.c_size_t, [_int]),
+    "kda_draft_verify": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _int, _i64, _int, _i64, _i64, _vp, _vp, _vp,
+                                _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None

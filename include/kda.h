@@ -1,7 +1,10 @@
 /*
  * libkda -- Kimi Delta Attention (KDA) on one GB300 (sm_103a): packed prefill,
  * decode, ReplaySSM replay, state-pool operations, input preprocessing and the
- * short convolution, and the backward of the prefill.
+ * short convolution, and the backward of the prefill; and, for the softmax
+ * attention layers that a hybrid model has beside its KDA layers, one speculative
+ * step: rotary positions, attention of a drafted tree over a paged cache,
+ * verification of the drafted tokens, and the append of the accepted ones.
  *
  * What is computed.  The KDA paragraph of "Kimi K3 on Fireworks: Fast RL at
  * frontier scale" (kernels section) describes KDA as linear attention that
@@ -65,7 +68,10 @@ typedef enum kda_status {
                                      no room to recompute its chain (see kda_chunk_fwd)       */
     KDA_ERR_TIMEOUT = 6,          /* device: a bounded wait gave up                           */
     KDA_ERR_BAD_SEQLENS = 7,      /* device: cu_seqlens / cu_accept not a valid partition     */
-    KDA_ERR_BAD_SLOT = 8          /* device: slot index outside [0, num_slots)                */
+    KDA_ERR_BAD_SLOT = 8,         /* device: slot or row index outside its array              */
+    KDA_ERR_BAD_PAGE = 9,         /* device: page index outside the pool, or a context longer
+                                     than the block table                                     */
+    KDA_ERR_BAD_TREE = 10         /* device: a drafted node's parent or token is not valid    */
 } kda_status;
 
 typedef enum kda_dtype {
@@ -352,9 +358,149 @@ kda_status kda_replay_conv(float *state_pool, int64_t num_slots, const int32_t *
                            void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * One speculative step of a softmax-attention layer.  A hybrid model interleaves
+ * KDA layers with attention layers whose keys and values are cached, and both have
+ * to represent the same prefix ("Kimi K3 on Fireworks: Fast RL at frontier scale":
+ * the KV-cache and speculative-decoding paragraphs).  The calls below give the
+ * attention layers what kda_chunk_fwd + kda_replay give the KDA layers: the drafted
+ * tokens attend to the cache without entering it (kda_tree_attn), verification
+ * decides which of them stand (kda_draft_verify), and only those are applied, by
+ * kda_replay to the recurrent states and by kda_cache_append to the cache.
+ *
+ * Drafted trees.  Sequence n of N has the nodes [cu_nodes[n], cu_nodes[n+1]) of the
+ * packed node arrays, at most KDA_MAX_TREE_NODES.  Node 0 is the root: the token
+ * that follows the committed context (already sampled).  parent[i] is the local
+ * index of a node's parent, 0 <= parent[i] < i (the root's entry is not read);
+ * parent NULL means chains, parent[i] = i - 1.  cu_nodes [N+1] int32 on the device:
+ * cu_nodes[0] = 0, non-decreasing, cu_nodes[N] <= the number of packed nodes.
+ */
+#define KDA_MAX_TREE_NODES 64
+
+/*
+ * Rotary positions of q and k.  Pair j < rot/2 of a head's channels -- (j, j + rot/2),
+ * or (2j, 2j + 1) with interleaved != 0 -- at position p turns by the angle
+ * t = p * inv_freq[j]:
+ *     (a, b) -> mscale (a cos t - b sin t, a sin t + b cos t);
+ * the channels from rot on are copied.  kda_rope_bwd is its gradient (the transposed
+ * map: the angle's sign changes), with the output gradients in place of q and k.
+ *   q, k        [T, Hq, d], [T, Hk, d] dtype; token t of q starts q_stride elements
+ *               after token t - 1 (0: Hq * d); k likewise.  k NULL or Hk = 0: q only.
+ *   positions   [T] int32 (any value)      inv_freq [rot/2] fp64, radians per position
+ *   q_out,k_out as q, k with their own strides; may be q and k themselves (same stride).
+ * d: a multiple of 8, at most 1024; rot even, 0 <= rot <= d.  Angles are reduced in
+ * 64-bit fixed point, so far positions lose nothing; the rest is fp32, rounded once.
+ * Pointers are element-aligned; 16-byte aligned rows (and rot / 2, or interleaved rot,
+ * a multiple of 16 bytes) take the vector path.  Nothing to report from the device,
+ * so no workspace.
+ */
+kda_status kda_rope(const void *q, const void *k, kda_dtype dtype, const int32_t *positions, const double *inv_freq,
+                    int64_t T, int Hq, int Hk, int d, int rot, int64_t q_stride, int64_t k_stride, int interleaved,
+                    float mscale, void *q_out, void *k_out, int64_t q_out_stride, int64_t k_out_stride, void *stream);
+kda_status kda_rope_bwd(const void *d_q_out, const void *d_k_out, kda_dtype dtype, const int32_t *positions,
+                        const double *inv_freq, int64_t T, int Hq, int Hk, int d, int rot, int64_t q_stride,
+                        int64_t k_stride, int interleaved, float mscale, void *d_q, void *d_k, int64_t q_out_stride,
+                        int64_t k_out_stride, void *stream);
+
+/*
+ * A paged cache of keys and values: key row r of page p for head h starts at
+ * k + p * k_page_stride + r * k_row_stride + h * k_head_stride (elements; any order
+ * of the axes), its dk channels contiguous; values likewise.  Strides and pointers
+ * are multiples of 16 bytes.  Row r of sequence n lies in page
+ * block_table[n * table_stride + r / page_size], slot r % page_size; its committed
+ * context is rows [0, ctx_len[n]).  All pointers are device pointers, the struct
+ * itself is read on the host during the call.
+ */
+typedef struct kda_paged_kv {
+    void *k, *v;
+    int64_t k_page_stride, k_row_stride, k_head_stride;
+    int64_t v_page_stride, v_row_stride, v_head_stride;
+    int64_t num_pages;
+    int64_t table_stride;
+    const int32_t *block_table; /* [N, max_pages] int32 */
+    const int32_t *ctx_len;     /* [N] int32 */
+    int page_size, max_pages;
+} kda_paged_kv;
+
+/*
+ * Attention of drafted trees over a paged cache: node i of sequence n attends to the
+ * sequence's context rows, to its ancestors and to itself (a one-node tree is the plain
+ * decode step).  Query head h reads KV head h / (Hq / Hkv).
+ *   q      [T, Hq, dk] dtype, token stride q_stride elements (0: packed)
+ *   k, v   [T, Hkv, dk], [T, Hkv, dv]: the nodes' own keys and values, not in the cache
+ *   o      [T, Hq, dv] dtype, packed;  lse [T, Hq] fp32 or NULL: log sum exp(scale q.k)
+ *   max_nodes  the largest tree of the batch (1..KDA_MAX_TREE_NODES); a larger one is
+ *          reported as KDA_ERR_BAD_SEQLENS
+ * dk, dv each 64 or 128.  Scores, softmax and sums are fp32; for bf16 the weights are
+ * rounded to bf16 before they meet the values (fp32 inputs keep fp32 throughout).
+ * Long contexts are cut into parts that run concurrently and are joined in a fixed
+ * order; the cut goes by a sequence's own length and tree, so its bits do not depend
+ * on the batch.  A sequence with a device error (BAD_SEQLENS, BAD_PAGE, BAD_TREE)
+ * writes nothing.
+ */
+size_t kda_tree_attn_workspace_size(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx);
+
+kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
+                         const int32_t *cu_nodes, const int32_t *parent, int N, int64_t T, int Hq, int Hkv, int dk,
+                         int dv, int64_t q_stride, int64_t k_stride, int64_t v_stride, int max_nodes, float scale,
+                         void *o, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Append rows to a paged cache: rows j in [cu[n], cu[n+1]) go to positions
+ * ctx_len[n] + j - cu[n] of sequence n.  Row j is row `rows[j]` of k and v, or row j
+ * with rows NULL: kda_draft_verify's cu_accept and rows append the accepted nodes of a
+ * drafted tree.  cu [N+1] as cu_nodes above; A_total >= cu[N] is the number of rows
+ * given (the rest are not read).  k, v: T_src rows, strides as for kda_tree_attn.
+ *   new_len  [N] int32 or NULL: ctx_len[n] + cu[n+1] - cu[n]; must not be ctx_len itself
+ * Device errors: BAD_SEQLENS; BAD_PAGE (a sequence that does not fit its block table
+ * keeps its length and writes nothing; a row whose page is outside the pool is not
+ * written); BAD_SLOT (rows[j] outside [0, T_src): not written).  Two rows must not
+ * name the same place.  workspace: >= KDA_WS_HEADER_BYTES.
+ */
+kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
+                            const int32_t *cu, const int32_t *rows, int N, int64_t A_total, int64_t T_src, int Hkv,
+                            int dk, int dv, int64_t k_stride, int64_t v_stride, int32_t *new_len, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * Verification of drafted trees against the target model's probabilities, from given
+ * uniform numbers in [0, 1).  The walk starts at the root.  At a node with target row p
+ * and draft row q its children are tried in index order; with A = 0, R = 1 and the
+ * residual r_v = max(0, p_v - A q_v), a child with token x and number u is accepted if
+ *     u q_x R < r_x,
+ * else A += R and R = sum_v r_v.  (That is repeated rejection sampling: the residual
+ * after a refusal is max(0, r - R q) up to its mass, and max(0, max(0, a) - b) =
+ * max(0, a - b) leaves one scalar for all refusals.)  Without draft probabilities the
+ * drafts are taken as certain: accepted if u R < r_x, else R -= r_x and r_x = 0.  When
+ * no child is accepted the next token is drawn from r by u_sample: the lowest v with
+ * sum_{w <= v} r_w > u_sample sum_w r_w.  A residual without mass leaves p in its place;
+ * p without mass gives token -1.  NaN counts as no mass.
+ *   tokens       [T] int32: the nodes' tokens (the root's is not read)
+ *   target_probs [T, V] dtype, row stride target_stride elements (0: V): row i is the
+ *                target's distribution after node i
+ *   draft_probs  [T, V] dtype (draft_stride) or NULL: row i is the distribution that
+ *                node i's children were drawn from
+ *   u_accept     [T] fp32 (the root's is not read)      u_sample [N] fp32
+ * Outputs: cu_accept [N+1] int32: sequence n accepts cu_accept[n+1] - cu_accept[n] nodes,
+ * the root among them; rows [T] int32: their packed indices in order, -1 from
+ * cu_accept[N] on; next_token [N] int32.  (cu_accept and the rows' k, v, g, beta are what
+ * kda_replay takes.)  An empty tree, or one with a device error (BAD_SEQLENS, BAD_TREE),
+ * accepts nothing and gives token -1.
+ * p - A q and its sums are carried to about 1e-13 (pairs of fp32, fp64 across threads),
+ * so a decision stands unless a number lies that close to a border.
+ * V: at most 2^24.  workspace: >= kda_draft_verify_workspace_size(N).
+ */
+size_t kda_draft_verify_workspace_size(int N);
+
+kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, const int32_t *parent,
+                            const void *target_probs, const void *draft_probs, kda_dtype dtype, const float *u_accept,
+                            const float *u_sample, int N, int64_t T, int V, int64_t target_stride,
+                            int64_t draft_stride, int32_t *cu_accept, int32_t *rows, int32_t *next_token,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Synchronizes `stream`, then reads the device status word of `workspace`
  * (errors from the last call that used it).  Returns KDA_OK or the first of
- * BAD_SEQLENS, BAD_SLOT, GATE_RANGE, TIMEOUT that was raised; KDA_ERR_CUDA if
+ * BAD_SEQLENS, BAD_SLOT, GATE_RANGE, TIMEOUT, BAD_PAGE, BAD_TREE that was raised; KDA_ERR_CUDA if
  * the synchronization or the copy failed.
  */
 kda_status kda_device_status(const void *workspace, void *stream);
