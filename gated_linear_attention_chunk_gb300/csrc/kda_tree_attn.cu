@@ -263,11 +263,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// A key row of a tile: page and slot in the pools, or page kDrafted and the packed node; kNoRow: zeros.
-struct TileRow {
-    int page, slot;
+// A key row of a tile: byte offsets of its K and V rows from the tile's bases; negative: no such row (zeros).
+struct __align__(16) TileRow {
+    int64_t k, v;
 };
-constexpr int kNoRow = -1, kDrafted = -2;
 
 // The ring of key / value tiles.  A tile is kKeys rows of K, then kKeys rows of V; the 16-byte
 // units of a row are permuted by its low three row bits, so that both a column of eight rows and a row are read
@@ -285,26 +284,24 @@ struct Ring {
     int *bad_seen;               // a page of this CTA's units was out of range
     Walk w;                      // the tile after the one whose rows were looked up last
     int tile;                    // tiles consumed so far
-    int head;                    // head of the looked-up tile
-    bool any;                    // there is one
+    const char *kbase, *vbase;   // bases of the looked-up tile's rows (null: no tile)
 
     // Rows of the walk's tile; moves the walk past it.  Every thread takes part, threads < kKeys have a row.
     __device__ __forceinline__ TileRow look(const AttnParams &p) {
-        TileRow r{kNoRow, 0};
-        if (w.unit >= w.end) {
-            any = false;
-            return r;
-        }
+        constexpr int64_t es = sizeof(T);
+        TileRow r{-1, -1};
+        kbase = nullptr;
+        if (w.unit >= w.end) return r;
         const int j = threadIdx.x;
-        head = w.head;
-        any = true;
         if (w.key < w.key_end) {
+            kbase = p.c.k + w.head * p.c.kh * es;
+            vbase = p.c.v + w.head * p.c.vh * es;
             if (j < kKeys && w.key + j < w.key_end) {
-                const int at = w.key + j, pg = at / p.c.page_size;
-                r.slot = at - pg * p.c.page_size;
-                r.page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
-                if (r.page < 0 || r.page >= p.c.num_pages) {
-                    r.page = kNoRow;
+                const int at = w.key + j, pg = at / p.c.page_size, slot = at - pg * p.c.page_size;
+                const int page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
+                if (page >= 0 && page < p.c.num_pages) {
+                    r = TileRow{(page * p.c.kp + slot * p.c.kr) * es, (page * p.c.vp + slot * p.c.vr) * es};
+                } else {
                     atomicOr(p.bad + w.n, static_cast<uint32_t>(DEV_ERR_PAGE));
                     atomicOr(p.status, static_cast<uint32_t>(DEV_ERR_PAGE));
                     *bad_seen = 1;
@@ -312,7 +309,12 @@ struct Ring {
             }
             w.key += kKeys;
         } else {
-            if (j < kKeys && w.node + j < w.node_end) r = TileRow{kDrafted, w.t0 + w.node + j};
+            kbase = static_cast<const char *>(p.k) + static_cast<int64_t>(w.head) * DK * es;
+            vbase = static_cast<const char *>(p.v) + static_cast<int64_t>(w.head) * DV * es;
+            if (j < kKeys && w.node + j < w.node_end) {
+                const int64_t t = w.t0 + w.node + j;
+                r = TileRow{t * p.ks * es, t * p.vs * es};
+            }
             w.node += kKeys;
         }
         if (w.unit_done()) w.next_unit(p);
@@ -321,32 +323,46 @@ struct Ring {
     __device__ __forceinline__ void put(TileRow r, int parity) {
         if (threadIdx.x < kKeys) rows[parity][threadIdx.x] = r;
     }
+    // Byte of unit u of row r0 + step (rows a multiple of 8 apart share their permutation).
     template <int kUnits>
-    __device__ __forceinline__ void copy(uint32_t dst, const TileRow *tr, const char *pages, int64_t ps, int64_t rs,
-                                         const char *fresh, int64_t ts) {
-        constexpr int kRowsPer = kAttnThreads / kUnits;  // rows side by side
-        const int u = threadIdx.x % kUnits;
-#pragma unroll
-        for (int i = 0; i < kKeys / kRowsPer; ++i) {
-            const int r = threadIdx.x / kUnits + i * kRowsPer;
-            const TileRow x = tr[r];
-            const char *src = x.page == kDrafted ? fresh + x.slot * ts : pages + (x.page == kNoRow ? 0 : x.page * ps + x.slot * rs);
-            cp16(dst + r * (kUnits * 16) + ((u ^ (r & 7)) << 4), src + u * 16, x.page != kNoRow);
-        }
+    static __device__ __forceinline__ uint32_t place(int r0, int step, int u) {
+        const int r = (kAttnThreads / kUnits) % 8 == 0 ? r0 : r0 + step;
+        return (r0 + step) * (kUnits * 16) + ((u ^ (r & 7)) << 4);
     }
-    // Starts the copies of the looked-up tile of the given number.
+    // Starts the copies of the looked-up tile of the given number: a thread takes one 16-byte unit of every
+    // kAttnThreads / units-th row.
     __device__ __forceinline__ void issue(const AttnParams &p, int number) {
-        const int parity = number & 1;
-        if (any) {
-            constexpr int64_t es = sizeof(T);
-            const int64_t h = head;
+        if (kbase) {
+            const TileRow *tr = rows[number & 1];
             const uint32_t dst = ptx::smem_u32(smem) + static_cast<uint32_t>(number % kStages) * kStage;
-            copy<kUnitsK>(dst, rows[parity], p.c.k + h * p.c.kh * es, p.c.kp * es, p.c.kr * es,
-                          static_cast<const char *>(p.k) + h * DK * es, p.ks * es);
-            copy<kUnitsV>(dst + kBytesK, rows[parity], p.c.v + h * p.c.vh * es, p.c.vp * es, p.c.vr * es,
-                          static_cast<const char *>(p.v) + h * DV * es, p.vs * es);
+            if constexpr (kUnitsK == kUnitsV) {
+                constexpr int kSide = kAttnThreads / kUnitsK;
+                const int u = threadIdx.x % kUnitsK, r0 = threadIdx.x / kUnitsK;
+                const char *ks = kbase + u * 16, *vs = vbase + u * 16;
+#pragma unroll
+                for (int i = 0; i < kKeys / kSide; ++i) {
+                    const TileRow x = tr[r0 + i * kSide];
+                    const bool there = x.k >= 0;
+                    const uint32_t to = dst + place<kUnitsK>(r0, i * kSide, u);
+                    cp16(to, ks + x.k, there);
+                    cp16(to + kBytesK, vs + x.v, there);
+                }
+            } else {
+                copy<kUnitsK>(dst, &tr->k, kbase);
+                copy<kUnitsV>(dst + kBytesK, &tr->v, vbase);
+            }
         }
         cp_commit();
+    }
+    template <int kUnits>
+    __device__ __forceinline__ void copy(uint32_t dst, const int64_t *off, const char *base) {
+        constexpr int kSide = kAttnThreads / kUnits;
+        const int u = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
+#pragma unroll
+        for (int i = 0; i < kKeys / kSide; ++i) {
+            const int64_t x = off[2 * (r0 + i * kSide)];
+            cp16(dst + place<kUnits>(r0, i * kSide, u), base + u * 16 + x, x >= 0);
+        }
     }
     __device__ __forceinline__ void start(const AttnParams &p, int first, int last) {
         tile = 0;
