@@ -20,61 +20,14 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "kda_spec.cuh"
-#include "sm100_ptx.cuh"
+#include "kda_tree_attn.cuh"
 
 namespace kda {
 namespace {
 
-using namespace spec;
+using namespace attn;
 
-constexpr int kTileRows = 64;    // query rows of a unit
 constexpr int kAttnThreads = 128;
-
-// One sequence as the plan leaves it.
-struct __align__(16) SeqInfo {
-    int ctx, nodes, t0, unit0;   // context, nodes, first packed node, first unit
-    int nsplit, chunk, tiles, pad;
-};
-
-struct AttnParams {
-    const void *q, *k, *v;
-    void *o;
-    float *lse;
-    Pages c;
-    const int32_t *cu, *parent;
-    int64_t T, qs, ks, vs;       // token strides in elements
-    int N, Hq, Hkv, G, max_nodes, max_splits;
-    float scale;
-    uint32_t *status;
-    SeqInfo *info;               // [N + 1]; entry N holds the number of units in unit0
-    uint32_t *bad;               // [N] a page or a parent of the sequence is not valid
-    int32_t *seq_of;             // [T] sequence of a packed node
-    uint64_t *sees;              // [T] ancestors of a packed node, itself included
-    float *part_o;               // [T, Hq, max_splits, dv]
-    float2 *part_ml;             // [T, Hq, max_splits] maximum (base 2) and sum
-};
-
-// How a sequence is cut: parts of at least 256 keys (more for many rows, whose partial results would outweigh the
-// keys they save), as many as give the sequence alone about one unit per SM, whatever else is in the batch.
-constexpr int kFillUnits = 152;
-__host__ __device__ inline int most_splits(int Hkv, int tiles) {
-    const int per = Hkv * tiles;
-    return per >= kFillUnits ? 1 : (kFillUnits + per - 1) / per;
-}
-__host__ __device__ inline int least_chunk(int rows) { return rows <= 16 ? 256 : rows <= 64 ? 16 * rows : 1024; }
-__host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, int *nsplit, int *chunk) {
-    const int least = least_chunk(rows);
-    int s = (ctx + least - 1) / least;
-    const int most = most_splits(Hkv, tiles);
-    s = s < 1 ? 1 : s > most ? most : s;
-    int c = (ctx + s - 1) / s;
-    c = (c + 63) / 64 * 64;
-    if (c < 64) c = 64;
-    *chunk = c;
-    *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
-}
-__host__ __device__ inline int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
 
 __device__ __forceinline__ uint32_t seq_check(const AttnParams &p, int n, int *t0, int *m, int *ctx) {
     const int64_t a = p.cu[n], b = p.cu[n + 1], c = p.c.ctx_len[n];
@@ -92,48 +45,77 @@ constexpr int kPlanThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0) {
-        __shared__ int warp_tot[kPlanThreads / 32];
-        __shared__ int base_units;
+        // both lists at once: units of the register kernels, row tiles of the tcgen05 kernel
+        __shared__ int warp_tot[2][kPlanThreads / 32];
+        __shared__ int base_units[2];
         __shared__ uint32_t errors;
         if (threadIdx.x == 0) {
-            base_units = 0;
+            base_units[0] = base_units[1] = 0;
             errors = 0;
         }
         __syncthreads();
         for (int base = 0; base < p.N; base += kPlanThreads) {
             const int n = base + threadIdx.x;
             SeqInfo s{};
-            int units = 0;
+            int units[2] = {0, 0};
             if (n < p.N) {
                 const uint32_t err = seq_check(p, n, &s.t0, &s.nodes, &s.ctx);
                 if (err) atomicOr(&errors, err);
-                if (!err && s.nodes > 0) {
-                    const int rows = s.nodes * p.G;
-                    s.tiles = tiles_of(rows);
-                    split_of(s.ctx, rows, p.Hkv, s.tiles, &s.nsplit, &s.chunk);
-                    units = s.nsplit * s.tiles * p.Hkv;
+                const int rows = s.nodes * p.G;
+                if (!err && rows > 0) {
+                    if (p.tc && rows > kTileRows) {
+                        s.tiles = tc_tiles_of(rows);
+                        tc_split_of(s.ctx, p.Hkv, s.tiles, &s.nsplit, &s.chunk);
+                        units[1] = s.nsplit * s.tiles * p.Hkv;
+                    } else {
+                        s.tiles = tiles_of(rows);
+                        split_of(s.ctx, rows, p.Hkv, s.tiles, &s.nsplit, &s.chunk);
+                        units[0] = s.nsplit * s.tiles * p.Hkv;
+                    }
                 }
             }
-            int upto = units;
+            int upto[2] = {units[0], units[1]};
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
+                const int y0 = __shfl_up_sync(0xffffffffu, upto[0], o), y1 = __shfl_up_sync(0xffffffffu, upto[1], o);
+                if (lane >= o) {
+                    upto[0] += y0;
+                    upto[1] += y1;
+                }
             }
-            if (lane == 31) warp_tot[warp] = upto;
+            if (lane == 31) {
+                warp_tot[0][warp] = upto[0];
+                warp_tot[1][warp] = upto[1];
+            }
             __syncthreads();
-            int off = base_units;
-            for (int w = 0; w < warp; ++w) off += warp_tot[w];
-            s.unit0 = off + upto - units;
-            if (n < p.N) p.info[n] = s;
+            int off[2] = {base_units[0], base_units[1]};
+            for (int w = 0; w < warp; ++w) {
+                off[0] += warp_tot[0][w];
+                off[1] += warp_tot[1][w];
+            }
+            if (n < p.N) {
+                s.unit0 = off[0] + upto[0] - units[0];
+                p.info[n] = s;
+                if (p.tc) {
+                    s.unit0 = off[1] + upto[1] - units[1];
+                    p.info_tc[n] = s;
+                }
+            }
             __syncthreads();
-            if (threadIdx.x == kPlanThreads - 1) base_units = off + upto;
+            if (threadIdx.x == kPlanThreads - 1) {
+                base_units[0] = off[0] + upto[0];
+                base_units[1] = off[1] + upto[1];
+            }
             __syncthreads();
         }
         if (threadIdx.x == 0) {
             SeqInfo s{};
-            s.unit0 = base_units;
+            s.unit0 = base_units[0];
             p.info[p.N] = s;
+            if (p.tc) {
+                s.unit0 = base_units[1];
+                p.info_tc[p.N] = s;
+            }
             *p.status = errors;
         }
         return;
@@ -246,22 +228,6 @@ struct Walk {
         begin_unit();
     }
 };
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
-    const int n = there ? 16 : 0;  // 0: nothing is read and the 16 bytes become zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A key row of a tile: byte offsets of its K and V rows from the tile's bases; negative: no such row (zeros).
 struct __align__(16) TileRow {
@@ -790,17 +756,24 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
     const int n = p.seq_of[t];
     if (n < 0 || n >= p.N) return;
     const SeqInfo s = p.info[n];
-    if (s.nsplit <= 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
+    if (s.nsplit < 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
+    int parts = s.nsplit;
+    if (p.tc && s.nodes * p.G > kTileRows) {  // a row tile without a partner leaves two results per part
+        const int r = static_cast<int>(t - s.t0) * p.G + static_cast<int>(row - t * p.Hq) % p.G;
+        if ((r / kTcRows | 1) >= s.tiles) parts *= 2;
+    }
+    if (parts == 1) return;
     float m = -INFINITY;
-    for (int i = lane; i < s.nsplit; i += 32) m = fmaxf(m, p.part_ml[row * p.max_splits + i].x);
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row * p.max_splits + i].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[VL] = {};
 #pragma unroll 4
-    for (int i = 0; i < s.nsplit; ++i) {
+    for (int i = 0; i < parts; ++i) {
         const int64_t at = row * p.max_splits + i;
         const float2 ml = p.part_ml[at];
+        if (ml.y == 0.f) continue;  // no keys: its sums were not written
         const float f = exp2f(ml.x - base);
         l = fmaf(f, ml.y, l);
 #pragma unroll
@@ -823,7 +796,7 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct AttnLayout {
-    size_t info, bad, seq_of, sees, part_ml, part_o, total;
+    size_t info, info_tc, bad, seq_of, sees, part_ml, part_o, total;
     int max_splits, max_tiles;
 };
 AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
@@ -833,9 +806,17 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     const int64_t by_len = (max_ctx + least_chunk(1) - 1) / least_chunk(1);
     const int64_t most = most_splits(Hkv, 1);
     l.max_splits = static_cast<int>(by_len < 1 ? 1 : by_len < most ? by_len : most);
+    if (max_nodes * (Hq / Hkv) > kTileRows) {  // (a tcgen05 tile alone leaves two results per part)
+        const int64_t far = (max_ctx + kTcChunk - 1) / kTcChunk, some = (max_ctx + 1023) / 1024;
+        int64_t parts = some < most ? some : most;
+        parts = 2 * (parts > far ? parts : far);
+        if (parts < 2) parts = 2;
+        if (parts > l.max_splits) l.max_splits = static_cast<int>(parts);
+    }
     size_t off = KDA_WS_HEADER_BYTES;
     auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
     l.info = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
+    l.info_tc = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
     l.bad = take(static_cast<size_t>(N) * 4);
     l.seq_of = take(static_cast<size_t>(T) * 4);
     l.sees = take(static_cast<size_t>(T) * 8);
@@ -858,7 +839,7 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
     if (sms <= 0) return KDA_ERR_CUDA;
     const int64_t seq_ctas = (static_cast<int64_t>(p.N) + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
     plan_kernel<<<static_cast<unsigned>(1 + seq_ctas), kPlanThreads, 0, s>>>(p);
-    const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * max_tiles;
+    const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * (p.tc ? 1 : max_tiles);
     const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? 2 : 1);
     const unsigned grid = static_cast<unsigned>(units < most ? units : most);
     kda_status st;
@@ -867,6 +848,7 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
         const size_t smem = R::kStages * R::kStage;
         if ((st = with_smem(attn_bf16_kernel<DK, DV>, smem)) != KDA_OK) return st;
         attn_bf16_kernel<DK, DV><<<grid, kAttnThreads, smem, s>>>(p);
+        if (p.tc && launch_attn_tc(p, DK, DV, sms, s) != cudaSuccess) return KDA_ERR_CUDA;
     } else {
         using R = Ring<float, DK, DV>;
         const size_t smem = R::kStages * R::kStage + kTileRows * (DK + 32) * sizeof(float);
@@ -926,12 +908,14 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0 || T == 0) return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
-    kda::AttnParams p{};
+    kda::attn::AttnParams p{};
     p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse; p.c = c; p.cu = cu_nodes; p.parent = parent;
     p.T = T; p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
     p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.max_nodes = max_nodes; p.max_splits = l.max_splits; p.scale = scale;
     p.status = reinterpret_cast<uint32_t *>(ws);
-    p.info = reinterpret_cast<kda::SeqInfo *>(ws + l.info);
+    p.info = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info);
+    p.info_tc = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info_tc);
+    p.tc = dtype == KDA_BF16 && max_nodes * p.G > kda::attn::kTileRows;
     p.bad = reinterpret_cast<uint32_t *>(ws + l.bad);
     p.seq_of = reinterpret_cast<int32_t *>(ws + l.seq_of);
     p.sees = reinterpret_cast<uint64_t *>(ws + l.sees);

@@ -1,0 +1,104 @@
+// Shared by the kernels of tree attention: parameters, how a sequence is cut, small device helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_spec.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+namespace attn {
+
+using namespace spec;
+
+constexpr int kTileRows = 64;    // query rows of a unit of the register kernels
+constexpr int kTcRows = 128;     // query rows of a tcgen05 tile
+constexpr int kTcKeys = 128;     // keys of a tile there
+
+// One sequence as the plan leaves it, once for the register kernels and once for the tcgen05 kernel (a
+// sequence has units in one of the two lists).
+struct __align__(16) SeqInfo {
+    int ctx, nodes, t0, unit0;   // context, nodes, first packed node; units (tcgen05: row tiles) before it
+    int nsplit, chunk, tiles, pad;
+};
+
+struct AttnParams {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    Pages c;
+    const int32_t *cu, *parent;
+    int64_t T, qs, ks, vs;       // token strides in elements
+    int N, Hq, Hkv, G, max_nodes, max_splits;
+    int tc;                      // sequences of more than kTileRows rows go to the tcgen05 kernel
+    float scale;
+    uint32_t *status;
+    SeqInfo *info, *info_tc;     // [N + 1] each; entry N holds the total in unit0
+    uint32_t *bad;               // [N] a page or a parent of the sequence is not valid
+    int32_t *seq_of;             // [T] sequence of a packed node
+    uint64_t *sees;              // [T] ancestors of a packed node, itself included
+    float *part_o;               // [T, Hq, max_splits, dv]
+    float2 *part_ml;             // [T, Hq, max_splits] maximum (base 2) and sum
+};
+
+// How a sequence is cut: parts of at least 256 keys (more for many rows, whose partial results would outweigh the
+// keys they save), as many as give the sequence alone about one unit per SM, whatever else is in the batch.
+constexpr int kFillUnits = 152;
+__host__ __device__ inline int most_splits(int Hkv, int tiles) {
+    const int per = Hkv * tiles;
+    return per >= kFillUnits ? 1 : (kFillUnits + per - 1) / per;
+}
+__host__ __device__ inline int least_chunk(int rows) { return rows <= 16 ? 256 : rows <= 64 ? 16 * rows : 1024; }
+__host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, int *nsplit, int *chunk) {
+    const int least = least_chunk(rows);
+    int s = (ctx + least - 1) / least;
+    const int most = most_splits(Hkv, tiles);
+    s = s < 1 ? 1 : s > most ? most : s;
+    int c = (ctx + s - 1) / s;
+    c = (c + 63) / 64 * 64;
+    if (c < 64) c = 64;
+    *chunk = c;
+    *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
+}
+__host__ __device__ inline int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
+
+// The same for the tcgen05 kernel, whose units are pairs of row tiles (or one): at most kTcChunk keys, so that the second
+// pair of a sequence finds the first one's keys in L2.
+constexpr int kTcChunk = 4096;
+__host__ __device__ inline int tc_tiles_of(int rows) { return (rows + kTcRows - 1) / kTcRows; }
+__host__ __device__ inline int tc_groups_of(int tiles) { return (tiles + 1) / 2; }
+__host__ __device__ inline void tc_split_of(int ctx, int Hkv, int tiles, int *nsplit, int *chunk) {
+    int s = (ctx + 1023) / 1024;
+    const int most = most_splits(Hkv, tc_groups_of(tiles)), far = (ctx + kTcChunk - 1) / kTcChunk;
+    s = s < 1 ? 1 : s > most ? most : s;
+    if (s < far) s = far;
+    int c = (ctx + s - 1) / s;
+    c = (c + kTcKeys - 1) / kTcKeys * kTcKeys;
+    if (c < kTcKeys) c = kTcKeys;
+    *chunk = c;
+    *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
+    const int n = there ? 16 : 0;  // 0: nothing is read and the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// kda_tree_attn_tc.cu: the units of info_tc (bf16).
+cudaError_t launch_attn_tc(const AttnParams &p, int dk, int dv, int sms, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace kda

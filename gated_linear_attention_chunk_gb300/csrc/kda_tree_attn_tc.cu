@@ -1,0 +1,558 @@
+// Tree attention on the tcgen05 tensor cores, for sequences of more than 64 query rows per KV head (bf16).
+//
+// The same one-pass softmax as the register kernels.  With R rows per KV head a key costs 2 (dk + dv) R operations against
+// 2 (dk + dv) bytes, so from about 280 rows on the tensor cores bound it, and mma.sync reaches less than half of
+// their rate.  One CTA per SM works on two streams of 128 rows x 128 keys:
+//   a pair of row tiles: stream s has the rows of tile s, both take every key tile;
+//   a row tile alone:    both streams have its rows, stream s takes the key tiles of parity s, and
+//                        each leaves its own partial result.
+// Per step of a stream S = Q K^T (128 x 128, fp32, TMEM), the softmax warps turn S into weights P (bf16, written over S in
+// TMEM), O += P V (P from TMEM, V as an MN-major operand).  While one stream's softmax runs, the tensor cores work
+// for the other.  The running maximum a row's weights refer to is raised only when the true one has grown by more than
+// 2^8 beyond it, so O is seldom rescaled (fp32 and bf16 have the range for weights up to 2^8).
+//
+// Warps:  0-3 and 4-7 softmax of stream 0 and 1 (a thread per row), 8-11 fill the ring, 12 issues the MMAs.
+// TMEM:   S0 0..127, S1 128..255, O0 256.., O1 384.. (512 columns).
+// Shared memory: two Q tiles and a ring of 128-row K or V tiles, all with the 128-byte swizzle (two 64-channel
+// halves), filled by 16-byte asynchronous copies: cache rows lie anywhere, a page may have any size, and rows past the end are
+// filled with zeros.  The ring holds the tiles in the order in which they are consumed:
+// K_0 .. K_{L-1}, V_0, K_L, V_1, K_{L+1}, .. with L = 1 for a pair and 2 for a tile alone.
+//
+// Every wait is bounded (2 s): a role that gives up raises the abort flag, which ends all the others' waits; the MMAs
+// issued so far are drained and the TMEM is freed.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_tree_attn.cuh"
+
+namespace kda {
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
+constexpr int kTcThreads = (kSoftmaxWarps + kLoadWarps + 1) * 32;
+constexpr float kRaise = 8.f;  // growth (log2) of a row's maximum before its reference follows
+
+template <int DK, int DV>
+struct Smem {
+    static constexpr int kHalf = 128 * 128;                     // bytes of 128 rows x 64 channels
+    static constexpr int kQ = DK / 64 * kHalf;
+    static constexpr int kSlot = (DK > DV ? DK : DV) / 64 * kHalf;
+    static constexpr int kSlots = kSlot == 2 * kHalf ? 5 : 8;
+    static constexpr int kBytes = 2 * kQ + kSlots * kSlot + 1024;  // plus alignment
+};
+
+struct Control {
+    uint64_t full[8], empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], drained;
+    uint32_t tmem;
+    int abort, bad_seen;
+};
+
+// A wait that ends after 2 s, or as soon as another role has given up.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control &c, uint32_t *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*reinterpret_cast<volatile int *>(&c.abort)) return false;
+        if (globaltimer_ns() - t0 > 2000000000ull) {
+            *reinterpret_cast<volatile int *>(&c.abort) = 1;
+            atomicOr(status, static_cast<uint32_t>(DEV_ERR_TIMEOUT));
+            return false;
+        }
+    }
+    return true;
+}
+
+// The units of a CTA: every role walks them alike.  A unit is (sequence, KV head, part, group of two row tiles),
+// the group running fastest; a CTA's share is a range of the row tiles counted in that order.
+struct TcWalk {
+    int n, u, en, eu;                                // at unit u of sequence n; end
+    int ctx, nodes, t0, nsplit, chunk, tiles, units;  // of the sequence
+    int head, split, group;
+    bool pair;
+    int key0, nctx, keys, node_end;                  // context keys, their tiles and count; drafted keys
+    int ntiles;
+
+    static __device__ __forceinline__ void boundary(const AttnParams &p, int64_t c, int total, int *n, int *u) {
+        if (c >= total) {
+            *n = p.N;
+            *u = 0;
+            return;
+        }
+        const int at = warp_find([&](int i) { return __ldg(&p.info_tc[i].unit0); }, p.N, c);
+        const int4 a = __ldg(reinterpret_cast<const int4 *>(p.info_tc + at) + 1);
+        const int off = static_cast<int>(c) - __ldg(&p.info_tc[at].unit0), tiles = a.z;
+        *n = at;
+        *u = off / tiles * tc_groups_of(tiles) + (off % tiles + 1) / 2;
+    }
+    __device__ __forceinline__ bool live() const { return n < en || (n == en && u < eu); }
+    __device__ __forceinline__ void enter(const AttnParams &p) {
+        // to the next unit at or after (n, u) that exists
+        while (live()) {
+            const int4 a = __ldg(reinterpret_cast<const int4 *>(p.info_tc + n));
+            const int4 b = __ldg(reinterpret_cast<const int4 *>(p.info_tc + n) + 1);
+            const int next = __ldg(&p.info_tc[n + 1].unit0);
+            ctx = a.x; nodes = a.y; t0 = a.z; nsplit = b.x; chunk = b.y; tiles = b.z;
+            units = next > a.w ? p.Hkv * nsplit * tc_groups_of(tiles) : 0;
+            if (u < units) break;
+            ++n;
+            u = 0;
+        }
+        if (live()) unit();
+    }
+    __device__ __forceinline__ void unit() {
+        const int groups = tc_groups_of(tiles), hs = u / groups;
+        group = u - hs * groups;
+        head = hs / nsplit;
+        split = hs - head * nsplit;
+        pair = 2 * group + 1 < tiles;
+        key0 = split * chunk;
+        keys = ctx - key0 < chunk ? ctx - key0 : chunk;
+        if (keys < 0) keys = 0;
+        nctx = (keys + kTcKeys - 1) / kTcKeys;
+        node_end = split == nsplit - 1 ? nodes : 0;
+        ntiles = nctx + (node_end > 0 ? 1 : 0);
+    }
+    __device__ __forceinline__ void start(const AttnParams &p) {
+        const int total = __ldg(&p.info_tc[p.N].unit0);
+        boundary(p, static_cast<int64_t>(total) * blockIdx.x / gridDim.x, total, &n, &u);
+        boundary(p, static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x, total, &en, &eu);
+        enter(p);
+    }
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        if (++u < units) {
+            if (live()) unit();
+            return;
+        }
+        ++n;
+        u = 0;
+        enter(p);
+    }
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// ---- filling side -------------------------------------------------------------------------------------------
+// 128 rows of `channels` x 2 bytes: half a warp takes a row, its address from the lane that looked it up (0: zeros).
+template <int kChannels>
+__device__ __forceinline__ void copy_rows(uint32_t dst, uint64_t row_addr, int warp, int lane, const void *any) {
+    constexpr int kUnits = kChannels / 8, kSide = 32 / kUnits;  // 16-byte units of a row; rows side by side
+    const int u = lane % kUnits;
+    const uint32_t to = dst + (u >> 3) * (128 * 128);
+#pragma unroll
+    for (int i = 0; i < 32 / kSide; ++i) {
+        const int at = i * kSide + lane / kUnits, r = warp * 32 + at;
+        const uint64_t a = __shfl_sync(0xffffffffu, row_addr, at);
+        cp16(to + r * 128 + (((u & 7) ^ (r & 7)) << 4), a ? reinterpret_cast<const char *>(a) + u * 16 : any, a != 0);
+    }
+}
+
+template <int DK, int DV>
+__device__ void fill(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t ring) {
+    using S = Smem<DK, DV>;
+    constexpr int kAhead = 3;  // tiles in flight before their arrival is announced
+    const int warp = (threadIdx.x >> 5) - kSoftmaxWarps, lane = threadIdx.x & 31;
+    const int mine = warp * 32 + lane;  // this thread's row of a tile
+    TcWalk w;
+    w.start(p);
+    uint32_t item = 0, told = 0;        // ring tiles issued; announced
+    uint32_t q_uses[2] = {0, 0};
+    int alone = 0;
+    auto tell = [&](uint32_t upto) {    // every copy up to there has landed
+        fence_proxy_async_smem();
+        for (; told < upto; ++told) mbar_arrive(&c.full[told % S::kSlots]);
+    };
+    // waits until a buffer is free; whoever has to wait first announces what has landed, so that nobody waits for it
+    auto wait_free = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_test_wait(bar, parity)) return true;
+        cp_wait<0>();
+        tell(item);
+        return wait(bar, parity, c, p.status);
+    };
+    while (w.live()) {
+        // the query rows
+        bool q_pending = false;
+        for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
+            const int b = w.pair ? s : (alone & 1);
+            if (!wait_free(&c.q_empty[b], (q_uses[b] & 1) ^ 1)) return;
+            ++q_uses[b];
+            const int r = (2 * w.group + s) * kTcRows + mine;
+            uint64_t a = 0;
+            if (r < w.nodes * p.G) {
+                const int node = r / p.G;
+                a = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.q) + (w.t0 + node) * p.qs +
+                                               static_cast<int64_t>(w.head * p.G + r - node * p.G) * DK);
+            }
+            copy_rows<DK>(q_smem + b * S::kQ, a, warp, lane, p.q);
+            q_pending = true;
+        }
+        // the keys and values; rows of a tile are looked up one tile before they are needed
+        const int lead = w.pair ? 1 : 2;
+        auto look = [&](int t, uint64_t *ka, uint64_t *va) {
+            *ka = *va = 0;
+            if (t < w.nctx) {
+                const int j = t * kTcKeys + mine;
+                if (j < w.keys) {
+                    const int at = w.key0 + j, pg = at / p.c.page_size, slot = at - pg * p.c.page_size;
+                    const int page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
+                    if (page >= 0 && page < p.c.num_pages) {
+                        *ka = reinterpret_cast<uint64_t>(p.c.k) + 2 * (page * p.c.kp + slot * p.c.kr + w.head * p.c.kh);
+                        *va = reinterpret_cast<uint64_t>(p.c.v) + 2 * (page * p.c.vp + slot * p.c.vr + w.head * p.c.vh);
+                    } else {
+                        atomicOr(p.bad + w.n, static_cast<uint32_t>(DEV_ERR_PAGE));
+                        atomicOr(p.status, static_cast<uint32_t>(DEV_ERR_PAGE));
+                        *reinterpret_cast<volatile int *>(&c.bad_seen) = 1;
+                    }
+                }
+            } else if (t < w.ntiles && mine < w.node_end) {
+                const int64_t row = w.t0 + mine;
+                *ka = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.k) + row * p.ks + static_cast<int64_t>(w.head) * DK);
+                *va = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.v) + row * p.vs + static_cast<int64_t>(w.head) * DV);
+            }
+        };
+        uint64_t k_next, v_next, v_wait[2] = {0, 0};  // v_wait: value rows of the tiles whose keys are already issued
+        look(0, &k_next, &v_next);
+        for (int t = 0; t < w.ntiles + lead; ++t) {
+            // V of tile t - lead, then K of tile t
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const bool is_k = kv == 1;
+                if (is_k ? t >= w.ntiles : t < lead) continue;
+                const uint32_t slot = item % S::kSlots;
+                if (!wait_free(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1)) return;
+                if (is_k) copy_rows<DK>(ring + slot * S::kSlot, k_next, warp, lane, p.q);
+                else copy_rows<DV>(ring + slot * S::kSlot, lead == 1 ? v_wait[0] : v_wait[1], warp, lane, p.q);
+                cp_commit();
+                ++item;
+                if (q_pending) {  // (the first tile's group holds the query rows too)
+                    cp_wait<0>();
+                    tell(item);
+                    for (int s = 0; s < (w.pair ? 2 : 1); ++s) mbar_arrive(&c.q_full[w.pair ? s : (alone & 1)]);
+                    q_pending = false;
+                } else if (item - told > kAhead) {
+                    cp_wait<kAhead>();
+                    tell(item - kAhead);
+                }
+            }
+            v_wait[1] = v_wait[0];
+            v_wait[0] = v_next;
+            look(t + 1, &k_next, &v_next);
+        }
+        if (!w.pair) ++alone;
+        w.next(p);
+    }
+    cp_wait<0>();
+    tell(item);
+}
+
+// ---- issuing side (one thread) --------------------------------------------------------------------------------
+template <int DK, int DV>
+__device__ void issue(const AttnParams &p, Control &c, TcWalk w, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
+    using S = Smem<DK, DV>;
+    constexpr uint32_t id_s = idesc_bf16(128, kTcKeys, false, false);  // K-major keys
+    constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);        // values: MN-major
+    uint32_t item = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, o_uses[2] = {0, 0};
+    int alone = 0;
+    auto scores = [&](int s, int b, uint32_t slot) {
+        const uint64_t dq = sdesc_sw128(q_smem + b * S::kQ, 16, 1024), dk = sdesc_sw128(ring + slot * S::kSlot, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+            const uint32_t at = ((k >> 2) * S::kHalf + (k & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + s * 128, dq + at, dk + at, id_s, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&c.s_full[s]);
+    };
+    auto values = [&](int s, uint32_t slot, bool first) {
+        const uint64_t dv = sdesc_sw128(ring + slot * S::kSlot, S::kHalf, 1024);
+#pragma unroll
+        for (int k = 0; k < kTcKeys / 16; ++k)
+            mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, (!first || k > 0) ? 1u : 0u);
+    };
+    auto have = [&](uint32_t i) {  // ring tile i has arrived
+        const bool ok = wait(&c.full[i % S::kSlots], (i / S::kSlots) & 1, c, p.status);
+        tc_fence_after();
+        return ok;
+    };
+    auto weights = [&](int s, bool first) {  // the stream's weights are there (and its O has been read)
+        if (!wait(&c.p_full[s], p_uses[s]++ & 1, c, p.status)) return false;
+        if (first && !wait(&c.o_empty[s], (o_uses[s]++ & 1) ^ 1, c, p.status)) return false;
+        tc_fence_after();
+        return true;
+    };
+    while (w.live()) {
+        const int nt = w.ntiles;
+        if (w.pair) {
+            for (int b = 0; b < 2; ++b)
+                if (!wait(&c.q_full[b], q_uses[b]++ & 1, c, p.status)) return;
+            if (!have(item)) return;
+            scores(0, 0, item % S::kSlots);
+            scores(1, 1, item % S::kSlots);
+            mma_commit(&c.empty[item % S::kSlots]);
+            ++item;
+            for (int t = 0; t < nt; ++t) {
+                const uint32_t v = item, k = item + 1;
+                for (int s = 0; s < 2; ++s) {
+                    if (!weights(s, t == 0)) return;
+                    if (s == 0 && !have(v)) return;
+                    values(s, v % S::kSlots, t == 0);
+                    if (s == 1) mma_commit(&c.empty[v % S::kSlots]);
+                    if (t + 1 < nt) {
+                        if (s == 0 && !have(k)) return;
+                        scores(s, s, k % S::kSlots);
+                        if (s == 1) mma_commit(&c.empty[k % S::kSlots]);
+                    } else {
+                        mma_commit(&c.o_full[s]);
+                    }
+                }
+                item += t + 1 < nt ? 2 : 1;
+            }
+            mma_commit(&c.q_empty[0]);
+            mma_commit(&c.q_empty[1]);
+        } else {
+            const int b = alone & 1;
+            if (!wait(&c.q_full[b], q_uses[b]++ & 1, c, p.status)) return;
+            for (int t = 0; t < (nt < 2 ? nt : 2); ++t, ++item) {
+                if (!have(item)) return;
+                scores(t, b, item % S::kSlots);
+                mma_commit(&c.empty[item % S::kSlots]);
+            }
+            for (int t = 0; t < nt; ++t) {
+                const int s = t & 1;
+                if (!weights(s, t < 2)) return;
+                if (!have(item)) return;
+                values(s, item % S::kSlots, t < 2);
+                mma_commit(&c.empty[item % S::kSlots]);
+                ++item;
+                if (t + 2 < nt) {
+                    if (!have(item)) return;
+                    scores(s, b, item % S::kSlots);
+                    mma_commit(&c.empty[item % S::kSlots]);
+                    ++item;
+                } else {
+                    mma_commit(&c.o_full[s]);
+                }
+            }
+            mma_commit(&c.q_empty[b]);
+            ++alone;
+        }
+        w.next(p);
+    }
+}
+
+// ---- softmax side (a thread per row of its stream) ---------------------------------------------------------------
+template <int DK, int DV>
+__device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
+    const int s = threadIdx.x >> 7, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(row & 96) << 16;
+    const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * 128;
+    const float scale = p.scale * kLog2e;
+    uint32_t s_uses = 0, o_uses = 0;
+    TcWalk w;
+    w.start(p);
+    while (w.live()) {
+        const int tile = 2 * w.group + (w.pair ? s : 0);
+        const int r = tile * kTcRows + row, rows = w.nodes * p.G;
+        const bool live = r < rows;
+        const int node = live ? r / p.G : 0, hq = w.head * p.G + (live ? r - node * p.G : 0);
+        const uint32_t flag = __ldcg(p.bad + w.n);
+        const int step = w.pair ? 1 : 2, t_first = w.pair ? 0 : s;
+        float ref = -INFINITY, top = -INFINITY, sum = 0.f;
+        for (int t = t_first; t < w.ntiles; t += step) {
+            const bool drafted = t >= w.nctx;
+            const int count = drafted ? w.node_end : (w.keys - t * kTcKeys < kTcKeys ? w.keys - t * kTcKeys : kTcKeys);
+            const bool ragged = drafted || count < kTcKeys;
+            uint64_t sees = ~0ull;
+            if (drafted) sees = __ldg(p.sees + w.t0 + node);
+            // key j of the tile counts for this row: the drafted nodes are at most 64
+            auto seen = [&](int j) { return j < count && (!drafted || ((sees >> (j & 63)) & 1)); };
+            if (!wait(&c.s_full[s], s_uses++ & 1, c, p.status)) return;
+            tc_fence_after();
+            float most = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kTcKeys; x += 32) {
+                uint32_t v[32];
+                tmem_ld32(ts + x, v);
+                tmem_ld_wait();
+                if (!ragged) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) most = fmaxf(most, __uint_as_float(v[i]) * scale);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (seen(x + i)) most = fmaxf(most, __uint_as_float(v[i]) * scale);
+                }
+            }
+            top = fmaxf(top, most);
+            // the reference follows the maximum when that has left it behind (at the first keys, always)
+            const bool raise = top > ref + kRaise || (ref == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float f = raise ? ex2(ref - top) : 1.f;
+                if (raise) ref = top;
+                sum *= f;
+                if (t > t_first) {  // O holds sums: the scores being there, the products before them are done
+#pragma unroll
+                    for (int x = 0; x < DV; x += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(to + x, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                        tmem_st16(to + x, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+                        tmem_st16(to + x + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                    }
+                }
+            }
+            const float base = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+            for (int x = 0; x < kTcKeys; x += 32) {
+                uint32_t v[32], pk[16];
+                tmem_ld32(ts + x, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float e = ex2(fmaf(__uint_as_float(v[i]), scale, -base));
+                    if (ragged && !seen(x + i)) e = 0.f;
+                    sum += e;
+                    v[i] = __float_as_uint(e);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                tmem_st16(ts + x / 2, pk);  // over scores that have been read
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&c.p_full[s]);
+        }
+        const bool any = t_first < w.ntiles;
+        if (any) {
+            if (!wait(&c.o_full[s], o_uses++ & 1, c, p.status)) return;
+            tc_fence_after();
+        }
+        uint32_t err = flag;
+        if (*reinterpret_cast<volatile int *>(&c.bad_seen)) err |= __ldcg(p.bad + w.n);
+        if (flag && row == 0) atomicOr(p.status, flag);
+        const bool ok = live && !err;
+        const int64_t out = static_cast<int64_t>(w.t0 + node) * p.Hq + hq;
+        const bool whole = w.pair && w.nsplit == 1;
+        const int64_t at = out * p.max_splits + (w.pair ? w.split : 2 * w.split + s);
+        if (any) {
+            const float f = whole ? 1.f / sum : 1.f;
+#pragma unroll
+            for (int x = 0; x < DV; x += 32) {
+                uint32_t v[32];
+                tmem_ld32(to + x, v);
+                tmem_ld_wait();
+                if (ok && whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t k[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            k[j] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
+                        dst[i] = make_uint4(k[0], k[1], k[2], k[3]);
+                    }
+                } else if (ok) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + at * DV + x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&c.o_empty[s]);
+        }
+        if (ok) {
+            if (!whole) p.part_ml[at] = make_float2(ref, sum);
+            else if (p.lse) p.lse[out] = (ref + log2f(sum)) * kLn2;
+        }
+        w.next(p);
+    }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams p) {
+    using S = Smem<DK, DV>;
+    extern __shared__ char raw[];
+    __shared__ Control c;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t q_smem = base, ring = base + 2 * S::kQ;
+    if (__ldg(&p.info_tc[p.N].unit0) == 0) return;  // no such sequence in the batch
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&c.full[i], kLoadWarps * 32);
+            mbar_init(&c.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.q_full[i], kLoadWarps * 32);
+            mbar_init(&c.q_empty[i], 1);
+            mbar_init(&c.s_full[i], 1);
+            mbar_init(&c.p_full[i], 128);
+            mbar_init(&c.o_full[i], 1);
+            mbar_init(&c.o_empty[i], 128);
+        }
+        mbar_init(&c.drained, 1);
+        c.abort = c.bad_seen = 0;
+        fence_mbar_init();
+    }
+    if (warp == kSoftmaxWarps + kLoadWarps) {
+        tmem_alloc(&c.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    if (warp < kSoftmaxWarps) {
+        softmax<DK, DV>(p, c, tmem);
+    } else if (warp < kSoftmaxWarps + kLoadWarps) {
+        fill<DK, DV>(p, c, q_smem, ring);
+        cp_wait<0>();  // (after a wait that gave up, too)
+    } else {
+        TcWalk w;
+        w.start(p);  // by the whole warp: it searches together
+        if ((threadIdx.x & 31) == 0) {
+            issue<DK, DV>(p, c, w, q_smem, ring, tmem);
+            // everything issued so far ends before the TMEM goes
+            mma_commit(&c.drained);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&c.drained, 0) && globaltimer_ns() - t0 < 2000000000ull) {}
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftmaxWarps + kLoadWarps) tmem_dealloc(tmem, 512);
+}
+
+template <int DK, int DV>
+cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
+    constexpr int bytes = Smem<DK, DV>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    attn_tc_kernel<DK, DV><<<sms, kTcThreads, bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnParams &p, int dk, int dv, int sms, cudaStream_t s) {
+    if (dk == 128) return dv == 128 ? launch<128, 128>(p, sms, s) : launch<128, 64>(p, sms, s);
+    return dv == 128 ? launch<64, 128>(p, sms, s) : launch<64, 64>(p, sms, s);
+}
+
+}  // namespace attn
+}  // namespace kda
