@@ -757,12 +757,8 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
     if (n < 0 || n >= p.N) return;
     const SeqInfo s = p.info[n];
     if (s.nsplit < 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
-    int parts = s.nsplit;
-    if (p.tc && s.nodes * p.G > kTileRows) {  // a row tile without a partner leaves two results per part
-        const int r = static_cast<int>(t - s.t0) * p.G + static_cast<int>(row - t * p.Hq) % p.G;
-        if ((r / kTcRows | 1) >= s.tiles) parts *= 2;
-    }
-    if (parts == 1) return;
+    const int parts = s.nsplit;
+    if (parts == 1 || (p.tc && s.nodes * p.G > kTileRows)) return;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row * p.max_splits + i].x);
 #pragma unroll
@@ -773,7 +769,6 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
     for (int i = 0; i < parts; ++i) {
         const int64_t at = row * p.max_splits + i;
         const float2 ml = p.part_ml[at];
-        if (ml.y == 0.f) continue;  // no keys: its sums were not written
         const float f = exp2f(ml.x - base);
         l = fmaf(f, ml.y, l);
 #pragma unroll
@@ -796,7 +791,7 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct AttnLayout {
-    size_t info, info_tc, bad, seq_of, sees, part_ml, part_o, total;
+    size_t info, info_tc, bad, seq_of, sees, part_ml, part_o, tc_ml, tc_o, total;
     int max_splits, max_tiles;
 };
 AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
@@ -806,13 +801,6 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     const int64_t by_len = (max_ctx + least_chunk(1) - 1) / least_chunk(1);
     const int64_t most = most_splits(Hkv, 1);
     l.max_splits = static_cast<int>(by_len < 1 ? 1 : by_len < most ? by_len : most);
-    if (max_nodes * (Hq / Hkv) > kTileRows) {  // (a tcgen05 tile alone leaves two results per part)
-        const int64_t far = (max_ctx + kTcChunk - 1) / kTcChunk, some = (max_ctx + 1023) / 1024;
-        int64_t parts = some < most ? some : most;
-        parts = 2 * (parts > far ? parts : far);
-        if (parts < 2) parts = 2;
-        if (parts > l.max_splits) l.max_splits = static_cast<int>(parts);
-    }
     size_t off = KDA_WS_HEADER_BYTES;
     auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
     l.info = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
@@ -823,6 +811,17 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     const size_t parts = l.max_splits > 1 ? static_cast<size_t>(T) * Hq * l.max_splits : 0;
     l.part_ml = take(parts * sizeof(float2));
     l.part_o = take(parts * dv * sizeof(float));
+    // the tcgen05 kernel's: every row tile (at most one not full per sequence) in each part, twice
+    size_t tc = 0;
+    const int64_t rows = max_nodes * static_cast<int64_t>(Hq / Hkv);
+    if (rows > kTileRows) {
+        const int64_t far = (max_ctx + kTcChunk - 1) / kTcChunk, some = (max_ctx + 1023) / 1024;
+        int64_t s = some < most ? some : most;
+        s = s > far ? s : far;
+        tc = static_cast<size_t>(T * (Hq / Hkv) / kTcRows + N) * Hkv * (s < 1 ? 1 : s) * 2;
+    }
+    l.tc_ml = take(tc * kTcRows * sizeof(float2));
+    l.tc_o = take(tc * kTcRows * dv * sizeof(float));
     l.total = off;
     return l;
 }
@@ -921,6 +920,8 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     p.sees = reinterpret_cast<uint64_t *>(ws + l.sees);
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
+    p.tc_ml = reinterpret_cast<float2 *>(ws + l.tc_ml);
+    p.tc_o = reinterpret_cast<float *>(ws + l.tc_o);
     if (dk == 128) return dv == 128 ? kda::launch_attn<128, 128>(p, dtype, l.max_tiles, s) : kda::launch_attn<128, 64>(p, dtype, l.max_tiles, s);
     return dv == 128 ? kda::launch_attn<64, 128>(p, dtype, l.max_tiles, s) : kda::launch_attn<64, 64>(p, dtype, l.max_tiles, s);
 }

@@ -41,6 +41,8 @@ struct AttnParams {
     uint64_t *sees;              // [T] ancestors of a packed node, itself included
     float *part_o;               // [T, Hq, max_splits, dv]
     float2 *part_ml;             // [T, Hq, max_splits] maximum (base 2) and sum
+    float *tc_o;                 // tcgen05 kernel's parts: [part][dv / 4][kTcRows] of 4 columns
+    float2 *tc_ml;               // [part][kTcRows]
 };
 
 // How a sequence is cut: parts of at least 256 keys (more for many rows, whose partial results would outweigh the
@@ -80,6 +82,9 @@ __host__ __device__ inline void tc_split_of(int ctx, int Hkv, int tiles, int *ns
     *chunk = c;
     *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
 }
+
+// Partial results of the tcgen05 kernel, by the row tile's number in info_tc's order; a tile alone leaves two per part.
+__host__ __device__ inline int64_t tc_part(int64_t tile, int stream) { return 2 * tile + stream; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
     const int n = there ? 16 : 0;  // 0: nothing is read and the 16 bytes become zeros

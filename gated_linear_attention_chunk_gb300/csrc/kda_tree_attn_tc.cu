@@ -51,13 +51,17 @@ struct Control {
     int abort, bad_seen;
 };
 
-// A wait that ends after 2 s, or as soon as another role has given up.
+// A wait that ends after about 2 s (4e9 clocks, counted from the 64th look), or once another role has given up.
+constexpr long long kPatience = 4000000000ll;
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control &c, uint32_t *status) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    long long t0 = 0;
+    for (uint32_t spins = 1; !mbar_try_wait(bar, parity); ++spins) {
+        if (spins & 63u) continue;
         if (*reinterpret_cast<volatile int *>(&c.abort)) return false;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
+        const long long now = clock64();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kPatience) {
             *reinterpret_cast<volatile int *>(&c.abort) = 1;
             atomicOr(status, static_cast<uint32_t>(DEV_ERR_TIMEOUT));
             return false;
@@ -70,7 +74,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control &c,
 // the group running fastest; a CTA's share is a range of the row tiles counted in that order.
 struct TcWalk {
     int n, u, en, eu;                                // at unit u of sequence n; end
-    int ctx, nodes, t0, nsplit, chunk, tiles, units;  // of the sequence
+    int ctx, nodes, t0, nsplit, chunk, tiles, units, first;  // of the sequence; first: row tiles before it
     int head, split, group;
     bool pair;
     int key0, nctx, keys, node_end;                  // context keys, their tiles and count; drafted keys
@@ -95,7 +99,7 @@ struct TcWalk {
             const int4 a = __ldg(reinterpret_cast<const int4 *>(p.info_tc + n));
             const int4 b = __ldg(reinterpret_cast<const int4 *>(p.info_tc + n) + 1);
             const int next = __ldg(&p.info_tc[n + 1].unit0);
-            ctx = a.x; nodes = a.y; t0 = a.z; nsplit = b.x; chunk = b.y; tiles = b.z;
+            ctx = a.x; nodes = a.y; t0 = a.z; first = a.w; nsplit = b.x; chunk = b.y; tiles = b.z;
             units = next > a.w ? p.Hkv * nsplit * tc_groups_of(tiles) : 0;
             if (u < units) break;
             ++n;
@@ -159,34 +163,32 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, uint64_t row_addr, int w
     }
 }
 
+// Arrives on a barrier once this thread's copies so far have landed (the barrier counts every thread once).
+__device__ __forceinline__ void arrive_landed(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 template <int DK, int DV>
 __device__ void fill(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t ring) {
     using S = Smem<DK, DV>;
-    constexpr int kAhead = 3;  // tiles in flight before their arrival is announced
     const int warp = (threadIdx.x >> 5) - kSoftmaxWarps, lane = threadIdx.x & 31;
     const int mine = warp * 32 + lane;  // this thread's row of a tile
     TcWalk w;
     w.start(p);
-    uint32_t item = 0, told = 0;        // ring tiles issued; announced
+    uint32_t item = 0;                  // ring tiles issued
     uint32_t q_uses[2] = {0, 0};
     int alone = 0;
-    auto tell = [&](uint32_t upto) {    // every copy up to there has landed
-        fence_proxy_async_smem();
-        for (; told < upto; ++told) mbar_arrive(&c.full[told % S::kSlots]);
-    };
-    // waits until a buffer is free; whoever has to wait first announces what has landed, so that nobody waits for it
-    auto wait_free = [&](uint64_t *bar, uint32_t parity) {
-        if (mbar_test_wait(bar, parity)) return true;
-        cp_wait<0>();
-        tell(item);
-        return wait(bar, parity, c, p.status);
-    };
     while (w.live()) {
+        // the page of this thread's row in key tile t: loaded a tile ahead of its use
+        auto page_of = [&](int t) {
+            const int j = t * kTcKeys + mine;
+            return t < w.nctx && j < w.keys ? __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + (w.key0 + j) / p.c.page_size) : 0;
+        };
+        int page = page_of(0);
         // the query rows
-        bool q_pending = false;
         for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
             const int b = w.pair ? s : (alone & 1);
-            if (!wait_free(&c.q_empty[b], (q_uses[b] & 1) ^ 1)) return;
+            if (!wait(&c.q_empty[b], (q_uses[b] & 1) ^ 1, c, p.status)) return;
             ++q_uses[b];
             const int r = (2 * w.group + s) * kTcRows + mine;
             uint64_t a = 0;
@@ -196,65 +198,53 @@ __device__ void fill(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t 
                                                static_cast<int64_t>(w.head * p.G + r - node * p.G) * DK);
             }
             copy_rows<DK>(q_smem + b * S::kQ, a, warp, lane, p.q);
-            q_pending = true;
+            arrive_landed(&c.q_full[b]);
         }
-        // the keys and values; rows of a tile are looked up one tile before they are needed
+        // the keys and values
         const int lead = w.pair ? 1 : 2;
-        auto look = [&](int t, uint64_t *ka, uint64_t *va) {
-            *ka = *va = 0;
+        uint64_t k_row = 0, v_row = 0, v_wait[2] = {0, 0};  // v_wait: value rows of the last tiles whose keys were issued
+        for (int t = 0; t < w.ntiles + lead; ++t) {
+            k_row = v_row = 0;
             if (t < w.nctx) {
                 const int j = t * kTcKeys + mine;
                 if (j < w.keys) {
-                    const int at = w.key0 + j, pg = at / p.c.page_size, slot = at - pg * p.c.page_size;
-                    const int page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
+                    const int64_t slot = (w.key0 + j) % p.c.page_size;
                     if (page >= 0 && page < p.c.num_pages) {
-                        *ka = reinterpret_cast<uint64_t>(p.c.k) + 2 * (page * p.c.kp + slot * p.c.kr + w.head * p.c.kh);
-                        *va = reinterpret_cast<uint64_t>(p.c.v) + 2 * (page * p.c.vp + slot * p.c.vr + w.head * p.c.vh);
+                        k_row = reinterpret_cast<uint64_t>(p.c.k) + 2 * (page * p.c.kp + slot * p.c.kr + w.head * p.c.kh);
+                        v_row = reinterpret_cast<uint64_t>(p.c.v) + 2 * (page * p.c.vp + slot * p.c.vr + w.head * p.c.vh);
                     } else {
                         atomicOr(p.bad + w.n, static_cast<uint32_t>(DEV_ERR_PAGE));
                         atomicOr(p.status, static_cast<uint32_t>(DEV_ERR_PAGE));
                         *reinterpret_cast<volatile int *>(&c.bad_seen) = 1;
                     }
                 }
+                page = page_of(t + 1);
             } else if (t < w.ntiles && mine < w.node_end) {
                 const int64_t row = w.t0 + mine;
-                *ka = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.k) + row * p.ks + static_cast<int64_t>(w.head) * DK);
-                *va = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.v) + row * p.vs + static_cast<int64_t>(w.head) * DV);
+                k_row = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.k) + row * p.ks + static_cast<int64_t>(w.head) * DK);
+                v_row = reinterpret_cast<uint64_t>(static_cast<const __nv_bfloat16 *>(p.v) + row * p.vs + static_cast<int64_t>(w.head) * DV);
             }
-        };
-        uint64_t k_next, v_next, v_wait[2] = {0, 0};  // v_wait: value rows of the tiles whose keys are already issued
-        look(0, &k_next, &v_next);
-        for (int t = 0; t < w.ntiles + lead; ++t) {
             // V of tile t - lead, then K of tile t
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const bool is_k = kv == 1;
-                if (is_k ? t >= w.ntiles : t < lead) continue;
+            if (t >= lead) {
                 const uint32_t slot = item % S::kSlots;
-                if (!wait_free(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1)) return;
-                if (is_k) copy_rows<DK>(ring + slot * S::kSlot, k_next, warp, lane, p.q);
-                else copy_rows<DV>(ring + slot * S::kSlot, lead == 1 ? v_wait[0] : v_wait[1], warp, lane, p.q);
-                cp_commit();
+                if (!wait(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1, c, p.status)) return;
+                copy_rows<DV>(ring + slot * S::kSlot, lead == 1 ? v_wait[0] : v_wait[1], warp, lane, p.q);
+                arrive_landed(&c.full[slot]);
                 ++item;
-                if (q_pending) {  // (the first tile's group holds the query rows too)
-                    cp_wait<0>();
-                    tell(item);
-                    for (int s = 0; s < (w.pair ? 2 : 1); ++s) mbar_arrive(&c.q_full[w.pair ? s : (alone & 1)]);
-                    q_pending = false;
-                } else if (item - told > kAhead) {
-                    cp_wait<kAhead>();
-                    tell(item - kAhead);
-                }
+            }
+            if (t < w.ntiles) {
+                const uint32_t slot = item % S::kSlots;
+                if (!wait(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1, c, p.status)) return;
+                copy_rows<DK>(ring + slot * S::kSlot, k_row, warp, lane, p.q);
+                arrive_landed(&c.full[slot]);
+                ++item;
             }
             v_wait[1] = v_wait[0];
-            v_wait[0] = v_next;
-            look(t + 1, &k_next, &v_next);
+            v_wait[0] = v_row;
         }
         if (!w.pair) ++alone;
         w.next(p);
     }
-    cp_wait<0>();
-    tell(item);
 }
 
 // ---- issuing side (one thread) --------------------------------------------------------------------------------
@@ -280,8 +270,9 @@ __device__ void issue(const AttnParams &p, Control &c, TcWalk w, uint32_t q_smem
         for (int k = 0; k < kTcKeys / 16; ++k)
             mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, (!first || k > 0) ? 1u : 0u);
     };
-    auto have = [&](uint32_t i) {  // ring tile i has arrived
+    auto have = [&](uint32_t i) {  // ring tile i has landed; the copies' writes become visible to the MMAs
         const bool ok = wait(&c.full[i % S::kSlots], (i / S::kSlots) & 1, c, p.status);
+        fence_proxy_async_smem();
         tc_fence_after();
         return ok;
     };
@@ -304,12 +295,11 @@ __device__ void issue(const AttnParams &p, Control &c, TcWalk w, uint32_t q_smem
             for (int t = 0; t < nt; ++t) {
                 const uint32_t v = item, k = item + 1;
                 for (int s = 0; s < 2; ++s) {
+                    if (s == 0 && !(have(v) && (t + 1 >= nt || have(k)))) return;  // while the softmax works
                     if (!weights(s, t == 0)) return;
-                    if (s == 0 && !have(v)) return;
                     values(s, v % S::kSlots, t == 0);
                     if (s == 1) mma_commit(&c.empty[v % S::kSlots]);
                     if (t + 1 < nt) {
-                        if (s == 0 && !have(k)) return;
                         scores(s, s, k % S::kSlots);
                         if (s == 1) mma_commit(&c.empty[k % S::kSlots]);
                     } else {
@@ -330,13 +320,12 @@ __device__ void issue(const AttnParams &p, Control &c, TcWalk w, uint32_t q_smem
             }
             for (int t = 0; t < nt; ++t) {
                 const int s = t & 1;
+                if (!have(item) || (t + 2 < nt && !have(item + 1))) return;  // while the softmax works
                 if (!weights(s, t < 2)) return;
-                if (!have(item)) return;
                 values(s, item % S::kSlots, t < 2);
                 mma_commit(&c.empty[item % S::kSlots]);
                 ++item;
                 if (t + 2 < nt) {
-                    if (!have(item)) return;
                     scores(s, b, item % S::kSlots);
                     mma_commit(&c.empty[item % S::kSlots]);
                     ++item;
@@ -380,19 +369,27 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
             if (!wait(&c.s_full[s], s_uses++ & 1, c, p.status)) return;
             tc_fence_after();
             float most = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < kTcKeys; x += 32) {
-                uint32_t v[32];
-                tmem_ld32(ts + x, v);
-                tmem_ld_wait();
-                if (!ragged) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) most = fmaxf(most, __uint_as_float(v[i]) * scale);
-                } else {
+            if (ragged) {
+#pragma unroll 1
+                for (int x = 0; x < kTcKeys; x += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(ts + x, v);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (seen(x + i)) most = fmaxf(most, __uint_as_float(v[i]) * scale);
                 }
+            } else {
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < kTcKeys; x += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(ts + x, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[i]) * scale);
+                }
+                most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             }
             top = fmaxf(top, most);
             // the reference follows the maximum when that has left it behind (at the first keys, always)
@@ -415,21 +412,40 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
                 }
             }
             const float base = ref == -INFINITY ? 0.f : ref;
+            if (ragged) {
+#pragma unroll 1
+                for (int x = 0; x < kTcKeys; x += 32) {
+                    uint32_t v[32], pk[16];
+                    tmem_ld32(ts + x, v);
+                    tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < kTcKeys; x += 32) {
-                uint32_t v[32], pk[16];
-                tmem_ld32(ts + x, v);
-                tmem_ld_wait();
+                    for (int i = 0; i < 32; ++i) {
+                        const float e = seen(x + i) ? ex2(fmaf(__uint_as_float(v[i]), scale, -base)) : 0.f;
+                        sum += e;
+                        v[i] = __float_as_uint(e);
+                    }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float e = ex2(fmaf(__uint_as_float(v[i]), scale, -base));
-                    if (ragged && !seen(x + i)) e = 0.f;
-                    sum += e;
-                    v[i] = __float_as_uint(e);
+                    for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    tmem_st16(ts + x / 2, pk);  // over scores that have been read
                 }
+            } else {
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                tmem_st16(ts + x / 2, pk);  // over scores that have been read
+                for (int x = 0; x < kTcKeys; x += 32) {
+                    uint32_t v[32], pk[16];
+                    tmem_ld32(ts + x, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float e0 = ex2(fmaf(__uint_as_float(v[i]), scale, -base));
+                        const float e1 = ex2(fmaf(__uint_as_float(v[i + 1]), scale, -base));
+                        s4[i & 2] += e0;
+                        s4[(i & 2) + 1] += e1;
+                        pk[i / 2] = pack_bf16x2(e0, e1);
+                    }
+                    tmem_st16(ts + x / 2, pk);
+                }
+                sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -446,7 +462,7 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
         const bool ok = live && !err;
         const int64_t out = static_cast<int64_t>(w.t0 + node) * p.Hq + hq;
         const bool whole = w.pair && w.nsplit == 1;
-        const int64_t at = out * p.max_splits + (w.pair ? w.split : 2 * w.split + s);
+        const int64_t part = tc_part(w.first + (static_cast<int64_t>(w.head) * w.nsplit + w.split) * w.tiles + tile, w.pair ? 0 : s);
         if (any) {
             const float f = whole ? 1.f / sum : 1.f;
 #pragma unroll
@@ -464,19 +480,17 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
                             k[j] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
                         dst[i] = make_uint4(k[0], k[1], k[2], k[3]);
                     }
-                } else if (ok) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + at * DV + x);
+                } else if (!whole) {  // [DV / 4][row]: a warp's stores are consecutive
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.tc_o) + (part * (DV / 4) + x / 4) * kTcRows + row;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) dst[i * kTcRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
             tc_fence_before();
             mbar_arrive(&c.o_empty[s]);
         }
-        if (ok) {
-            if (!whole) p.part_ml[at] = make_float2(ref, sum);
-            else if (p.lse) p.lse[out] = (ref + log2f(sum)) * kLn2;
-        }
+        if (!whole) p.tc_ml[part * kTcRows + row] = make_float2(ref, sum);
+        else if (ok && p.lse) p.lse[out] = (ref + log2f(sum)) * kLn2;
         w.next(p);
     }
 }
@@ -527,8 +541,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             issue<DK, DV>(p, c, w, q_smem, ring, tmem);
             // everything issued so far ends before the TMEM goes
             mma_commit(&c.drained);
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&c.drained, 0) && globaltimer_ns() - t0 < 2000000000ull) {}
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&c.drained, 0) && clock64() - t0 < kPatience) {}
         }
         __syncwarp();
     }
@@ -538,12 +552,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     if (warp == kSoftmaxWarps + kLoadWarps) tmem_dealloc(tmem, 512);
 }
 
+// The parts of a row tile joined in order: a thread per row, kCombCols columns of it.
+constexpr int kCombCols = 32;
+
+template <int DV>
+__global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p) {
+    const int n = blockIdx.x, max_tiles = gridDim.y / p.Hkv;
+    const int head = blockIdx.y / max_tiles, tile = blockIdx.y - head * max_tiles, c0 = blockIdx.z * kCombCols;
+    const SeqInfo s = p.info_tc[n];
+    if (p.info_tc[n + 1].unit0 == s.unit0 || tile >= s.tiles) return;
+    const bool alone = (tile | 1) >= s.tiles;
+    if ((!alone && s.nsplit == 1) || p.bad[n]) return;
+    const int row = threadIdx.x, r = tile * kTcRows + row, parts = alone ? 2 * s.nsplit : s.nsplit;
+    if (r >= s.nodes * p.G) return;
+    const int64_t id0 = s.unit0 + static_cast<int64_t>(head) * s.nsplit * s.tiles + tile;
+    auto part = [&](int i) { return alone ? tc_part(id0 + static_cast<int64_t>(i >> 1) * s.tiles, i & 1) : tc_part(id0 + static_cast<int64_t>(i) * s.tiles, 0); };
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) m = fmaxf(m, p.tc_ml[part(i) * kTcRows + row].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[kCombCols] = {};
+#pragma unroll 2
+    for (int i = 0; i < parts; ++i) {
+        const float2 ml = p.tc_ml[part(i) * kTcRows + row];
+        if (ml.y == 0.f) continue;  // no keys: its sums were not written
+        const float f = exp2f(ml.x - base);
+        l = fmaf(f, ml.y, l);
+        const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
+#pragma unroll
+        for (int j = 0; j < kCombCols / 4; ++j) {
+            const float4 v = src[j * kTcRows];
+            o[4 * j] = fmaf(f, v.x, o[4 * j]);
+            o[4 * j + 1] = fmaf(f, v.y, o[4 * j + 1]);
+            o[4 * j + 2] = fmaf(f, v.z, o[4 * j + 2]);
+            o[4 * j + 3] = fmaf(f, v.w, o[4 * j + 3]);
+        }
+    }
+    const float inv = 1.f / l;
+    const int node = r / p.G;
+    const int64_t out = static_cast<int64_t>(s.t0 + node) * p.Hq + head * p.G + r - node * p.G;
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + c0);
+#pragma unroll
+    for (int i = 0; i < kCombCols / 8; ++i) {
+        uint32_t k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = pack_bf16x2(o[8 * i + 2 * j] * inv, o[8 * i + 2 * j + 1] * inv);
+        to[i] = make_uint4(k[0], k[1], k[2], k[3]);
+    }
+    if (p.lse && c0 == 0) p.lse[out] = (m + log2f(l)) * kLn2;
+}
+
 template <int DK, int DV>
 cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr int bytes = Smem<DK, DV>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     attn_tc_kernel<DK, DV><<<sms, kTcThreads, bytes, s>>>(p);
+    const dim3 grid(p.N, p.Hkv * tc_tiles_of(p.max_nodes * p.G), DV / kCombCols);
+    combine_tc_kernel<DV><<<grid, kTcRows, 0, s>>>(p);
     return cudaGetLastError();
 }
 
