@@ -33,7 +33,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
-constexpr int kTcThreads = (kSoftmaxWarps + kLoadWarps + 1) * 32;
+constexpr int kTcThreads = 512;  // four warpgroups; the last one's other three warps have no role
 constexpr float kRaise = 8.f;  // growth (log2) of a row's maximum before its reference follows
 
 template <int DK, int DV>
@@ -50,6 +50,33 @@ struct Control {
     uint32_t tmem;
     int abort, bad_seen;
 };
+
+// Registers, launched with 128 for each of 512 threads: a softmax thread holds a row's 128 scores and takes 168, the
+// others 88 (168 + 168 + 88 + 88 = 4 x 128).
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory"); }
+__device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory"); }
+
+// Two floats at a time (each rounded as by the scalar instruction).
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // A wait that ends after about 2 s (4e9 clocks, counted from the 64th look), or once another role has given up.
 constexpr long long kPatience = 4000000000ll;
@@ -146,6 +173,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 
 // ---- filling side -------------------------------------------------------------------------------------------
@@ -247,38 +283,55 @@ __device__ void fill(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t 
     }
 }
 
-// ---- issuing side (one thread) --------------------------------------------------------------------------------
+// ---- issuing side (one warp) ----------------------------------------------------------------------------------
+// Every lane runs this code and one is elected inside each instruction: issued that way a TMEM-operand product of this
+// shape takes about half the clocks that it takes from a single thread in a branch.
+__device__ __forceinline__ void mma_bf16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Control &c, uint32_t *status) {
+    return __all_sync(0xffffffffu, wait(bar, parity, c, status));
+}
 template <int DK, int DV>
-__device__ void issue(const AttnParams &p, Control &c, TcWalk w, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
+__device__ void issue(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
     using S = Smem<DK, DV>;
     constexpr uint32_t id_s = idesc_bf16(128, kTcKeys, false, false);  // K-major keys
     constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);        // values: MN-major
     uint32_t item = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, o_uses[2] = {0, 0};
     int alone = 0;
+    TcWalk w;
+    w.start(p);
     auto scores = [&](int s, int b, uint32_t slot) {
         const uint64_t dq = sdesc_sw128(q_smem + b * S::kQ, 16, 1024), dk = sdesc_sw128(ring + slot * S::kSlot, 16, 1024);
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k) {
             const uint32_t at = ((k >> 2) * S::kHalf + (k & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + s * 128, dq + at, dk + at, id_s, k > 0 ? 1u : 0u);
+            mma_bf16_ss_warp(tmem + s * 128, dq + at, dk + at, id_s, k > 0 ? 1u : 0u);
         }
-        mma_commit(&c.s_full[s]);
+        mma_commit_warp(&c.s_full[s]);
     };
     auto values = [&](int s, uint32_t slot, bool first) {
         const uint64_t dv = sdesc_sw128(ring + slot * S::kSlot, S::kHalf, 1024);
 #pragma unroll
         for (int k = 0; k < kTcKeys / 16; ++k)
-            mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, (!first || k > 0) ? 1u : 0u);
+            mma_bf16_ts_warp(tmem + 256 + s * 128, tmem + s * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, (!first || k > 0) ? 1u : 0u);
     };
-    auto have = [&](uint32_t i) {  // ring tile i has landed; the copies' writes become visible to the MMAs
-        const bool ok = wait(&c.full[i % S::kSlots], (i / S::kSlots) & 1, c, p.status);
-        fence_proxy_async_smem();
-        tc_fence_after();
+    auto have = [&](uint32_t i) {  // ring tile i has landed
+        const bool ok = wait_warp(&c.full[i % S::kSlots], (i / S::kSlots) & 1, c, p.status);
         return ok;
     };
+    auto landed = [&] {  // the copies' writes become visible to the MMAs that follow
+        fence_proxy_async_smem();
+        tc_fence_after();
+    };
     auto weights = [&](int s, bool first) {  // the stream's weights are there (and its O has been read)
-        if (!wait(&c.p_full[s], p_uses[s]++ & 1, c, p.status)) return false;
-        if (first && !wait(&c.o_empty[s], (o_uses[s]++ & 1) ^ 1, c, p.status)) return false;
+        if (!wait_warp(&c.p_full[s], p_uses[s]++ & 1, c, p.status)) return false;
+        if (first && !wait_warp(&c.o_empty[s], (o_uses[s]++ & 1) ^ 1, c, p.status)) return false;
         tc_fence_after();
         return true;
     };
@@ -286,54 +339,60 @@ __device__ void issue(const AttnParams &p, Control &c, TcWalk w, uint32_t q_smem
         const int nt = w.ntiles;
         if (w.pair) {
             for (int b = 0; b < 2; ++b)
-                if (!wait(&c.q_full[b], q_uses[b]++ & 1, c, p.status)) return;
+                if (!wait_warp(&c.q_full[b], q_uses[b]++ & 1, c, p.status)) return;
             if (!have(item)) return;
+            landed();
             scores(0, 0, item % S::kSlots);
             scores(1, 1, item % S::kSlots);
-            mma_commit(&c.empty[item % S::kSlots]);
+            mma_commit_warp(&c.empty[item % S::kSlots]);
             ++item;
             for (int t = 0; t < nt; ++t) {
                 const uint32_t v = item, k = item + 1;
                 for (int s = 0; s < 2; ++s) {
-                    if (s == 0 && !(have(v) && (t + 1 >= nt || have(k)))) return;  // while the softmax works
+                    if (s == 0) {  // while the softmax works
+                        if (!have(v) || (t + 1 < nt && !have(k))) return;
+                        landed();
+                    }
                     if (!weights(s, t == 0)) return;
                     values(s, v % S::kSlots, t == 0);
-                    if (s == 1) mma_commit(&c.empty[v % S::kSlots]);
+                    if (s == 1) mma_commit_warp(&c.empty[v % S::kSlots]);
                     if (t + 1 < nt) {
                         scores(s, s, k % S::kSlots);
-                        if (s == 1) mma_commit(&c.empty[k % S::kSlots]);
+                        if (s == 1) mma_commit_warp(&c.empty[k % S::kSlots]);
                     } else {
-                        mma_commit(&c.o_full[s]);
+                        mma_commit_warp(&c.o_full[s]);
                     }
                 }
                 item += t + 1 < nt ? 2 : 1;
             }
-            mma_commit(&c.q_empty[0]);
-            mma_commit(&c.q_empty[1]);
+            mma_commit_warp(&c.q_empty[0]);
+            mma_commit_warp(&c.q_empty[1]);
         } else {
             const int b = alone & 1;
-            if (!wait(&c.q_full[b], q_uses[b]++ & 1, c, p.status)) return;
+            if (!wait_warp(&c.q_full[b], q_uses[b]++ & 1, c, p.status)) return;
             for (int t = 0; t < (nt < 2 ? nt : 2); ++t, ++item) {
                 if (!have(item)) return;
+                landed();
                 scores(t, b, item % S::kSlots);
-                mma_commit(&c.empty[item % S::kSlots]);
+                mma_commit_warp(&c.empty[item % S::kSlots]);
             }
             for (int t = 0; t < nt; ++t) {
                 const int s = t & 1;
                 if (!have(item) || (t + 2 < nt && !have(item + 1))) return;  // while the softmax works
+                landed();
                 if (!weights(s, t < 2)) return;
                 values(s, item % S::kSlots, t < 2);
-                mma_commit(&c.empty[item % S::kSlots]);
+                mma_commit_warp(&c.empty[item % S::kSlots]);
                 ++item;
                 if (t + 2 < nt) {
                     scores(s, b, item % S::kSlots);
-                    mma_commit(&c.empty[item % S::kSlots]);
+                    mma_commit_warp(&c.empty[item % S::kSlots]);
                     ++item;
                 } else {
-                    mma_commit(&c.o_full[s]);
+                    mma_commit_warp(&c.o_full[s]);
                 }
             }
-            mma_commit(&c.q_empty[b]);
+            mma_commit_warp(&c.q_empty[b]);
             ++alone;
         }
         w.next(p);
@@ -346,7 +405,11 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
     const int s = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(row & 96) << 16;
     const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * 128;
-    const float scale = p.scale * kLog2e;
+    // a masked score is the one that the scale takes to -inf; a scale of zero has no such score, nor has it a row whose
+    // weights differ: it becomes the smallest one that has
+    const float given = p.scale * kLog2e;
+    const float scale = given == 0.f ? 1e-37f : given;
+    const uint32_t hidden = __float_as_uint(scale > 0.f ? -INFINITY : INFINITY);
     uint32_t s_uses = 0, o_uses = 0;
     TcWalk w;
     w.start(p);
@@ -364,34 +427,42 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
             const bool ragged = drafted || count < kTcKeys;
             uint64_t sees = ~0ull;
             if (drafted) sees = __ldg(p.sees + w.t0 + node);
-            // key j of the tile counts for this row: the drafted nodes are at most 64
-            auto seen = [&](int j) { return j < count && (!drafted || ((sees >> (j & 63)) & 1)); };
             if (!wait(&c.s_full[s], s_uses++ & 1, c, p.status)) return;
             tc_fence_after();
-            float most = -INFINITY;
+            // the row's scores, all in registers
+            uint32_t v[kTcKeys];
+#pragma unroll
+            for (int x = 0; x < kTcKeys; x += 32) tmem_ld32(ts + x, *reinterpret_cast<uint32_t(*)[32]>(&v[x]));
+            tmem_ld_wait();
             if (ragged) {
-#pragma unroll 1
+                // key j counts for this row: below `count`, and among the drafted nodes (at most 64) an ancestor
+#pragma unroll
                 for (int x = 0; x < kTcKeys; x += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(ts + x, v);
-                    tmem_ld_wait();
+                    const int here = count - x;
+                    uint32_t bits = here >= 32 ? 0xffffffffu : here > 0 ? (1u << here) - 1u : 0u;
+                    if (drafted) bits &= x == 0 ? static_cast<uint32_t>(sees) : static_cast<uint32_t>(sees >> 32);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (seen(x + i)) most = fmaxf(most, __uint_as_float(v[i]) * scale);
+                        if (!((bits >> i) & 1u)) v[x + i] = hidden;
                 }
-            } else {
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int x = 0; x < kTcKeys; x += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(ts + x, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[i]) * scale);
-                }
-                most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             }
-            top = fmaxf(top, most);
+            float m4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(v[j]);
+            if (scale > 0.f) {
+#pragma unroll
+                for (int i = 4; i < kTcKeys; i += 4)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], __uint_as_float(v[i + j]));
+                m4[0] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            } else {
+#pragma unroll
+                for (int i = 4; i < kTcKeys; i += 4)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m4[j] = fminf(m4[j], __uint_as_float(v[i + j]));
+                m4[0] = fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
+            }
+            top = fmaxf(top, m4[0] * scale);
             // the reference follows the maximum when that has left it behind (at the first keys, always)
             const bool raise = top > ref + kRaise || (ref == -INFINITY && top > -INFINITY);
             if (__any_sync(0xffffffffu, raise)) {
@@ -399,54 +470,34 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
                 if (raise) ref = top;
                 sum *= f;
                 if (t > t_first) {  // O holds sums: the scores being there, the products before them are done
-#pragma unroll
-                    for (int x = 0; x < DV; x += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(to + x, v);
+#pragma unroll 1
+                    for (int x = 0; x < DV; x += 8) {
+                        uint32_t o[8];
+                        tmem_ld8(to + x, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                        tmem_st16(to + x, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-                        tmem_st16(to + x + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st8(to + x, o);
                     }
                 }
             }
             const float base = ref == -INFINITY ? 0.f : ref;
-            if (ragged) {
-#pragma unroll 1
-                for (int x = 0; x < kTcKeys; x += 32) {
-                    uint32_t v[32], pk[16];
-                    tmem_ld32(ts + x, v);
-                    tmem_ld_wait();
+            const uint64_t scale2 = pair2(scale, scale), base2 = pair2(-base, -base);
+            uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float e = seen(x + i) ? ex2(fmaf(__uint_as_float(v[i]), scale, -base)) : 0.f;
-                        sum += e;
-                        v[i] = __float_as_uint(e);
-                    }
+            for (int x = 0; x < kTcKeys; x += 32) {
+                uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    tmem_st16(ts + x / 2, pk);  // over scores that have been read
+                for (int i = 0; i < 16; ++i) {
+                    const float2 e = unpair2(fma2(pair2(__uint_as_float(v[x + 2 * i]), __uint_as_float(v[x + 2 * i + 1])), scale2, base2));
+                    const float e0 = ex2(e.x), e1 = ex2(e.y);
+                    s2[i & 1] = add2(s2[i & 1], pair2(e0, e1));
+                    pk[i] = pack_bf16x2(e0, e1);
                 }
-            } else {
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < kTcKeys; x += 32) {
-                    uint32_t v[32], pk[16];
-                    tmem_ld32(ts + x, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float e0 = ex2(fmaf(__uint_as_float(v[i]), scale, -base));
-                        const float e1 = ex2(fmaf(__uint_as_float(v[i + 1]), scale, -base));
-                        s4[i & 2] += e0;
-                        s4[(i & 2) + 1] += e1;
-                        pk[i / 2] = pack_bf16x2(e0, e1);
-                    }
-                    tmem_st16(ts + x / 2, pk);
-                }
-                sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                tmem_st16(ts + x / 2, pk);  // over scores that have been read
             }
+            const float2 sa = unpair2(s2[0]), sb = unpair2(s2[1]);
+            sum += (sa.x + sa.y) + (sb.x + sb.y);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&c.p_full[s]);
@@ -480,7 +531,7 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
                             k[j] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
                         dst[i] = make_uint4(k[0], k[1], k[2], k[3]);
                     }
-                } else if (!whole) {  // [DV / 4][row]: a warp's stores are consecutive
+                } else if (live && !whole) {  // [DV / 4][row]: a warp's stores are consecutive
                     uint4 *dst = reinterpret_cast<uint4 *>(p.tc_o) + (part * (DV / 4) + x / 4) * kTcRows + row;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dst[i * kTcRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -489,7 +540,7 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
             tc_fence_before();
             mbar_arrive(&c.o_empty[s]);
         }
-        if (!whole) p.tc_ml[part * kTcRows + row] = make_float2(ref, sum);
+        if (live && !whole) p.tc_ml[part * kTcRows + row] = make_float2(ref, sum);
         else if (ok && p.lse) p.lse[out] = (ref + log2f(sum)) * kLn2;
         w.next(p);
     }
@@ -530,20 +581,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     if (warp < kSoftmaxWarps) {
+        regs_more();
         softmax<DK, DV>(p, c, tmem);
     } else if (warp < kSoftmaxWarps + kLoadWarps) {
+        regs_less();
         fill<DK, DV>(p, c, q_smem, ring);
         cp_wait<0>();  // (after a wait that gave up, too)
     } else {
-        TcWalk w;
-        w.start(p);  // by the whole warp: it searches together
-        if ((threadIdx.x & 31) == 0) {
-            issue<DK, DV>(p, c, w, q_smem, ring, tmem);
-            // everything issued so far ends before the TMEM goes
-            mma_commit(&c.drained);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&c.drained, 0) && clock64() - t0 < kPatience) {}
-        }
+        regs_less();
+    }
+    if (warp == kSoftmaxWarps + kLoadWarps) {
+        issue<DK, DV>(p, c, q_smem, ring, tmem);
+        __syncwarp();
+        mma_commit_warp(&c.drained);  // everything issued so far ends before the TMEM goes
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&c.drained, 0) && clock64() - t0 < kPatience) {}
         __syncwarp();
     }
     tc_fence_before();
@@ -553,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
 }
 
 // The parts of a row tile joined in order: a thread per row, kCombCols columns of it.
-constexpr int kCombCols = 32;
+constexpr int kCombCols = 8;
 
 template <int DV>
 __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p) {
@@ -572,20 +624,20 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p)
     for (int i = 0; i < parts; ++i) m = fmaxf(m, p.tc_ml[part(i) * kTcRows + row].x);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[kCombCols] = {};
-#pragma unroll 2
+#pragma unroll 8
     for (int i = 0; i < parts; ++i) {
         const float2 ml = p.tc_ml[part(i) * kTcRows + row];
-        if (ml.y == 0.f) continue;  // no keys: its sums were not written
+        const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
+        const bool empty = ml.y == 0.f;  // no keys: its sums were not written
         const float f = exp2f(ml.x - base);
         l = fmaf(f, ml.y, l);
-        const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
 #pragma unroll
         for (int j = 0; j < kCombCols / 4; ++j) {
             const float4 v = src[j * kTcRows];
-            o[4 * j] = fmaf(f, v.x, o[4 * j]);
-            o[4 * j + 1] = fmaf(f, v.y, o[4 * j + 1]);
-            o[4 * j + 2] = fmaf(f, v.z, o[4 * j + 2]);
-            o[4 * j + 3] = fmaf(f, v.w, o[4 * j + 3]);
+            o[4 * j] = fmaf(f, empty ? 0.f : v.x, o[4 * j]);
+            o[4 * j + 1] = fmaf(f, empty ? 0.f : v.y, o[4 * j + 1]);
+            o[4 * j + 2] = fmaf(f, empty ? 0.f : v.z, o[4 * j + 2]);
+            o[4 * j + 3] = fmaf(f, empty ? 0.f : v.w, o[4 * j + 3]);
         }
     }
     const float inv = 1.f / l;
