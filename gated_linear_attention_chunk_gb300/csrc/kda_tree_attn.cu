@@ -44,6 +44,7 @@ constexpr int kPlanThreads = 256;
 // CTA 0: the list of sequences and units, and the status word.  The others, a warp per sequence: masks.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_go();
     if (blockIdx.x == 0) {
         // both lists at once: units of the register kernels, row tiles of the tcgen05 kernel
         __shared__ int warp_tot[2][kPlanThreads / 32];
@@ -583,6 +584,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_bf16_kernel(const AttnPa
     __shared__ TileRow rows[2][R::kKeys];
     __shared__ float2 ml[4][16];
     __shared__ int bad_seen;
+    grid_wait();
+    grid_go();
     const int64_t units = __ldg(&p.info[p.N].unit0);
     const int first = static_cast<int>(units * blockIdx.x / gridDim.x);
     const int last = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
@@ -619,6 +622,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_f32_kernel(const AttnParams
     __shared__ int bad_seen;
     float *qs = reinterpret_cast<float *>(smem + R::kStages * R::kStage);  // [kTileRows][DK]
     float *ps = qs + kTileRows * DK;                                       // [kTileRows][32]
+    grid_wait();
+    grid_go();
     const int64_t units = __ldg(&p.info[p.N].unit0);
     const int begin = static_cast<int>(units * blockIdx.x / gridDim.x);
     const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
@@ -748,11 +753,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_f32_kernel(const AttnParams
 template <typename T, int DV>
 __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams p) {
     constexpr int VL = DV / 32;
+    grid_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 32) + (threadIdx.x >> 5);
     if (row >= p.T * p.Hq) return;
     const int64_t t = row / p.Hq;
-    if (t >= p.cu[p.N]) return;                       // packed nodes beyond the last sequence
+    // (a packed node beyond the last sequence has no entry: whatever is read there does not contain it)
     const int n = p.seq_of[t];
     if (n < 0 || n >= p.N) return;
     const SeqInfo s = p.info[n];
@@ -826,12 +832,6 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     return l;
 }
 
-template <typename F>
-kda_status with_smem(F kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess
-               ? KDA_OK : KDA_ERR_CUDA;
-}
-
 template <int DK, int DV>
 kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cudaStream_t s) {
     const int sms = sm_count();
@@ -841,24 +841,24 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
     const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * (p.tc ? 1 : max_tiles);
     const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? 2 : 1);
     const unsigned grid = static_cast<unsigned>(units < most ? units : most);
-    kda_status st;
     if (dtype == KDA_BF16) {
         using R = Ring<__nv_bfloat16, DK, DV>;
-        const size_t smem = R::kStages * R::kStage;
-        if ((st = with_smem(attn_bf16_kernel<DK, DV>, smem)) != KDA_OK) return st;
-        attn_bf16_kernel<DK, DV><<<grid, kAttnThreads, smem, s>>>(p);
+        const int smem = R::kStages * R::kStage;
+        if (!smem_opt_in<attn_bf16_kernel<DK, DV>>(smem)) return KDA_ERR_CUDA;
+        if (launch_after(attn_bf16_kernel<DK, DV>, dim3(grid), kAttnThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
         if (p.tc && launch_attn_tc(p, DK, DV, sms, s) != cudaSuccess) return KDA_ERR_CUDA;
     } else {
         using R = Ring<float, DK, DV>;
-        const size_t smem = R::kStages * R::kStage + kTileRows * (DK + 32) * sizeof(float);
-        if ((st = with_smem(attn_f32_kernel<DK, DV>, smem)) != KDA_OK) return st;
-        attn_f32_kernel<DK, DV><<<grid, kAttnThreads, smem, s>>>(p);
+        const int smem = R::kStages * R::kStage + kTileRows * (DK + 32) * static_cast<int>(sizeof(float));
+        if (!smem_opt_in<attn_f32_kernel<DK, DV>>(smem)) return KDA_ERR_CUDA;
+        if (launch_after(attn_f32_kernel<DK, DV>, dim3(grid), kAttnThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (p.max_splits > 1) {
         const int64_t rows = p.T * p.Hq;
         const unsigned cg = static_cast<unsigned>((rows + kAttnThreads / 32 - 1) / (kAttnThreads / 32));
-        if (dtype == KDA_BF16) combine_kernel<__nv_bfloat16, DV><<<cg, kAttnThreads, 0, s>>>(p);
-        else combine_kernel<float, DV><<<cg, kAttnThreads, 0, s>>>(p);
+        const cudaError_t e = dtype == KDA_BF16 ? launch_after(combine_kernel<__nv_bfloat16, DV>, dim3(cg), kAttnThreads, 0, s, p)
+                                                : launch_after(combine_kernel<float, DV>, dim3(cg), kAttnThreads, 0, s, p);
+        if (e != cudaSuccess) return KDA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -554,6 +554,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     const int warp = threadIdx.x >> 5;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t q_smem = base, ring = base + 2 * S::kQ;
+    grid_wait();
+    grid_go();
     if (__ldg(&p.info_tc[p.N].unit0) == 0) return;  // no such sequence in the batch
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
@@ -609,6 +611,7 @@ constexpr int kCombCols = 8;
 
 template <int DV>
 __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p) {
+    grid_wait();
     const int n = blockIdx.x, max_tiles = gridDim.y / p.Hkv;
     const int head = blockIdx.y / max_tiles, tile = blockIdx.y - head * max_tiles, c0 = blockIdx.z * kCombCols;
     const SeqInfo s = p.info_tc[n];
@@ -657,12 +660,11 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p)
 template <int DK, int DV>
 cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr int bytes = Smem<DK, DV>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (!smem_opt_in<attn_tc_kernel<DK, DV>>(bytes)) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_after(attn_tc_kernel<DK, DV>, dim3(sms), kTcThreads, bytes, s, p);
     if (e != cudaSuccess) return e;
-    attn_tc_kernel<DK, DV><<<sms, kTcThreads, bytes, s>>>(p);
     const dim3 grid(p.N, p.Hkv * tc_tiles_of(p.max_nodes * p.G), DV / kCombCols);
-    combine_tc_kernel<DV><<<grid, kTcRows, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(combine_tc_kernel<DV>, grid, kTcRows, 0, s, p);
 }
 
 }  // namespace

@@ -35,6 +35,9 @@ class _PagedKV(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object around it)
+
+
 def _code(t: torch.Tensor, name: str) -> int:
     code = _CODES.get(t.dtype)
     if code is None:
@@ -44,22 +47,28 @@ def _code(t: torch.Tensor, name: str) -> int:
 
 def _token_stride(t, name: str, dtype, H: int, d: int, T: Optional[int] = None) -> int:
     """Checks a [T, H, d] tensor whose tokens may be strided (a slice of a fused projection); its token stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    try:
+        n, h, e = t.shape
+        if t.dtype is dtype and t.is_cuda and h == H and e == d and (T is None or n == T):
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and (s1 == d or H == 1):
+                if n <= 1:
+                    return 0
+                if s0 >= H * d:
+                    return s0
+                raise ValueError(f"{name} must not have overlapping tokens (stride {s0} < {H * d})")
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    except ValueError as e:
+        if str(e).startswith(name):
+            raise
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != H or shape[2] != d or (T is not None and shape[0] != T):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({'T' if T is None else T}, {H}, {d})")
-    if strides[2] != 1 or (H > 1 and strides[1] != d):
-        raise ValueError(f"{name} must have contiguous tokens (only its first dimension may be strided)")
-    if shape[0] <= 1:
-        return 0
-    if strides[0] < H * d:
-        raise ValueError(f"{name} must not have overlapping tokens (stride {strides[0]} < {H * d})")
-    return strides[0]
+    if t.dim() != 3 or t.shape[1:] != (H, d) or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({'T' if T is None else T}, {H}, {d})")
+    raise ValueError(f"{name} must have contiguous tokens (only its first dimension may be strided)")
 
 
 def _ints(t, name: str, n: Optional[int] = None):
@@ -68,33 +77,25 @@ def _ints(t, name: str, n: Optional[int] = None):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 1 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA vector")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} has {t.shape[0]} entries, expected {n}")
+    if n is not None and shape[0] != n:
+        raise ValueError(f"{name} has {shape[0]} entries, expected {n}")
     return t.data_ptr()
 
 
-class _On:
-    """The stream of a call, its tensors' device current; what is allocated inside belongs to that stream."""
-
-    def __init__(self, device, stream):
-        self.handle = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-        here = torch.cuda.current_device()
-        self.ctx = []
-        if stream is not None:
-            self.ctx.append(torch.cuda.stream(stream))
-        elif device.index is not None and device.index != here:
-            self.ctx.append(torch.cuda.device(device))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+def _on(device, stream, call):
+    """``call(handle)`` with the tensors' device current, on the given stream or the current one; what it allocates
+    belongs to that stream."""
+    index = device.index
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(_raw_stream(index))
+        with torch.cuda.device(device):
+            return call(_raw_stream(index))
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _check(rc: int, where: str):
@@ -102,31 +103,28 @@ def _check(rc: int, where: str):
         raise KdaError(rc, where)
 
 
-def _workspace(workspace, nbytes: int, device):
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace
-
-
-def _cache(k_pages, v_pages, block_table, ctx_len, dtype, Hkv: int, dk: int, dv: int) -> Tuple[_PagedKV, int]:
+def _cache(k_pages, v_pages, block_table, ctx_len, dtype, Hkv: int, dk: int, dv: int) -> Tuple[_PagedKV, int, int]:
+    """The checked cache as its C struct; the number of sequences, and the rows that a block table can name."""
     for name, t, d in (("k_pages", k_pages, dk), ("v_pages", v_pages, dv)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda or t.dtype != dtype or t.dim() != 4 or t.stride(3) != 1:
+        shape = t.shape
+        if not t.is_cuda or t.dtype is not dtype or len(shape) != 4 or t.stride(3) != 1:
             raise ValueError(f"{name} must be a CUDA tensor [pages, page_size, Hkv, d] of {dtype} with contiguous channels")
-        if t.shape[2] != Hkv or t.shape[3] != d:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, page_size, {Hkv}, {d}]")
-    if k_pages.shape[:2] != v_pages.shape[:2]:
+        if shape[2] != Hkv or shape[3] != d:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected [pages, page_size, {Hkv}, {d}]")
+    pages, page, _, _ = k_pages.shape
+    if v_pages.shape[0] != pages or v_pages.shape[1] != page:
         raise ValueError("k_pages and v_pages must have the same pages and page size")
-    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda or block_table.dtype != torch.int32 \
+    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda or block_table.dtype is not torch.int32 \
             or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be an int32 CUDA matrix [N, max_pages] with contiguous rows")
     N, max_pages = block_table.shape
-    ctx = _ints(ctx_len, "ctx_len", N)
-    ks, vs = k_pages.stride(), v_pages.stride()
-    return _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], k_pages.shape[0],
-                    block_table.stride(0) if N > 1 else max_pages, block_table.data_ptr(), ctx, k_pages.shape[1],
-                    max_pages), N
+    k0, k1, k2, _ = k_pages.stride()
+    v0, v1, v2, _ = v_pages.stride()
+    return _PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), k0, k1, k2, v0, v1, v2, pages,
+                    block_table.stride(0) if N > 1 else max_pages, block_table.data_ptr(), _ints(ctx_len, "ctx_len", N), page,
+                    max_pages), N, page * max_pages
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -182,30 +180,28 @@ def _rope(name, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out, st
     T, Hq, d = q.shape
     dt, code = q.dtype, _code(q, "q")
     qs = _token_stride(q, "q", dt, Hq, d)
-    Hk, ks, kos = 0, 0, 0
+    Hk, ks = 0, 0
     if k is not None:
         Hk = k.shape[1]
         ks = _token_stride(k, "k", dt, Hk, d, T)
     pos = _ints(positions, "positions", T)
-    if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or not inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous fp64 CUDA vector")
-    with _On(q.device, stream) as handle:
-        if q_out is None:
-            q_out, qos = torch.empty(T, Hq, d, dtype=dt, device=q.device), 0
+
+    def call(handle):
+        qo = torch.empty((T, Hq, d), dtype=dt, device=q.device) if q_out is None else q_out
+        qos = 0 if q_out is None else _token_stride(q_out, "q_out", dt, Hq, d, T)
+        if k is None:
+            ko, kos, kp, kop = None, 0, None, None
         else:
-            qos = _token_stride(q_out, "q_out", dt, Hq, d, T)
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty(T, Hk, d, dtype=dt, device=q.device)
-            else:
-                kos = _token_stride(k_out, "k_out", dt, Hk, d, T)
-        else:
-            k_out = None
-        rc = getattr(lib, name)(q.data_ptr(), None if k is None else k.data_ptr(), code, pos, inv_freq.data_ptr(), T, Hq, Hk,
-                                d, 2 * inv_freq.shape[0], qs, ks, bool(interleaved), mscale, q_out.data_ptr(),
-                                None if k is None else k_out.data_ptr(), qos, kos, handle)
-    _check(rc, name)
-    return q_out, k_out
+            ko = torch.empty((T, Hk, d), dtype=dt, device=q.device) if k_out is None else k_out
+            kos = 0 if k_out is None else _token_stride(k_out, "k_out", dt, Hk, d, T)
+            kp, kop = k.data_ptr(), ko.data_ptr()
+        _check(getattr(lib, name)(q.data_ptr(), kp, code, pos, inv_freq.data_ptr(), T, Hq, Hk, d, 2 * inv_freq.shape[0], qs, ks,
+                                  bool(interleaved), mscale, qo.data_ptr(), kop, qos, kos, handle), name)
+        return qo, ko
+
+    return _on(q.device, stream, call)
 
 
 def kda_tree_attn_workspace_size(N: int, T: int, Hq: int, Hkv: int, dv: int, max_nodes: int, max_ctx: int) -> int:
@@ -229,26 +225,28 @@ def kda_tree_attn(q, k, v, k_pages, v_pages, block_table, ctx_len, cu_nodes, par
     dt, code = q.dtype, _code(q, "q")
     qs = _token_stride(q, "q", dt, Hq, dk)
     ks, vs = _token_stride(k, "k", dt, Hkv, dk, T), _token_stride(v, "v", dt, Hkv, dv, T)
-    cache, N = _cache(k_pages, v_pages, block_table, ctx_len, dt, Hkv, dk, dv)
+    cache, N, max_ctx = _cache(k_pages, v_pages, block_table, ctx_len, dt, Hkv, dk, dv)
     cu, par = _ints(cu_nodes, "cu_nodes", N + 1), _ints(parent, "parent", T)
-    with _On(q.device, stream) as handle:
-        if o is None:
-            o = torch.empty(T, Hq, dv, dtype=dt, device=q.device)
+    if o is not None:
+        _kda._need(o, "o", dt, (T, Hq, dv))
+    if lse is not None:
+        _kda._need(lse, "lse", torch.float32, (T, Hq))
+
+    def call(handle):
+        dev = q.device
+        out = torch.empty((T, Hq, dv), dtype=dt, device=dev) if o is None else o
+        sums = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None and return_lse else lse
+        if workspace is None:  # (0 for sizes that the call itself refuses)
+            size = lib.kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx) or KDA_WS_HEADER_BYTES
+            ws = torch.empty((size,), dtype=torch.uint8, device=dev)
         else:
-            _kda._need(o, "o", dt, (T, Hq, dv))
-        if lse is not None:
-            _kda._need(lse, "lse", torch.float32, (T, Hq))
-        elif return_lse:
-            lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(max(KDA_WS_HEADER_BYTES, lib.kda_tree_attn_workspace_size(
-                N, T, Hq, Hkv, dv, max_nodes, cache.page_size * cache.max_pages)), dtype=torch.uint8, device=q.device)
-        rc = lib.kda_tree_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, ctypes.byref(cache), cu, par, N, T, Hq, Hkv, dk,
-                               dv, qs, ks, vs, max_nodes, dk ** -0.5 if scale is None else scale, o.data_ptr(),
-                               None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), handle)
-    _check(rc, "kda_tree_attn")
-    return o, lse
+            ws, size = workspace, workspace.numel() * workspace.element_size()
+        _check(lib.kda_tree_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, ctypes.byref(cache), cu, par, N, T, Hq, Hkv, dk,
+                                 dv, qs, ks, vs, max_nodes, dk ** -0.5 if scale is None else scale, out.data_ptr(),
+                                 None if sums is None else sums.data_ptr(), ws.data_ptr(), size, handle), "kda_tree_attn")
+        return out, sums
+
+    return _on(q.device, stream, call)
 
 
 def kda_cache_append(k, v, k_pages, v_pages, block_table, ctx_len, cu, rows=None, new_len=None, workspace=None,
@@ -262,18 +260,19 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, ctx_len, cu, rows=None
     dv = v.shape[2]
     dt, code = k.dtype, _code(k, "k")
     ks, vs = _token_stride(k, "k", dt, Hkv, dk), _token_stride(v, "v", dt, Hkv, dv, T)
-    cache, N = _cache(k_pages, v_pages, block_table, ctx_len, dt, Hkv, dk, dv)
+    cache, N, _ = _cache(k_pages, v_pages, block_table, ctx_len, dt, Hkv, dk, dv)
     c, r = _ints(cu, "cu", N + 1), _ints(rows, "rows")
-    with _On(k.device, stream) as handle:
-        if new_len is None:
-            new_len = torch.empty(N, dtype=torch.int32, device=k.device)
-        workspace = _workspace(workspace, KDA_WS_HEADER_BYTES, k.device)
-        rc = lib.kda_cache_append(k.data_ptr(), v.data_ptr(), code, ctypes.byref(cache), c, r, N,
-                                  T if rows is None else rows.shape[0], T, Hkv, dk, dv, ks, vs,
-                                  _ints(new_len, "new_len", N), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), handle)
-    _check(rc, "kda_cache_append")
-    return new_len
+
+    def call(handle):
+        new = torch.empty((N,), dtype=torch.int32, device=k.device) if new_len is None else new_len
+        ws = torch.empty((KDA_WS_HEADER_BYTES,), dtype=torch.uint8, device=k.device) if workspace is None else workspace
+        _check(lib.kda_cache_append(k.data_ptr(), v.data_ptr(), code, ctypes.byref(cache), c, r, N,
+                                    T if rows is None else rows.shape[0], T, Hkv, dk, dv, ks, vs,
+                                    _ints(new, "new_len", N), ws.data_ptr(), ws.numel() * ws.element_size(), handle),
+               "kda_cache_append")
+        return new
+
+    return _on(k.device, stream, call)
 
 
 def kda_draft_verify_workspace_size(N: int) -> int:
@@ -295,29 +294,29 @@ def kda_draft_verify(tokens, cu_nodes, target_probs, u_accept, u_sample, parent=
     N = cu_nodes.shape[0] - 1
     code = _code(target_probs, "target_probs")
     for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
-        if t is not None and (not t.is_cuda or t.dtype != target_probs.dtype or tuple(t.shape) != (T, V)
+        if t is not None and (not t.is_cuda or t.dtype is not target_probs.dtype or t.shape != (T, V)
                               or (V > 1 and t.stride(1) != 1)):
             raise ValueError(f"{name} must be a CUDA matrix [{T}, {V}] of {target_probs.dtype} with contiguous rows")
     for name, t, n in (("u_accept", u_accept, T), ("u_sample", u_sample, N)):
-        if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+        if not t.is_cuda or t.dtype is not torch.float32 or t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp32 CUDA vector of {n}")
     tok, cu, par = _ints(tokens, "tokens", T), _ints(cu_nodes, "cu_nodes"), _ints(parent, "parent", T)
     dev = target_probs.device
-    with _On(dev, stream) as handle:
-        if cu_accept is None:
-            cu_accept = torch.empty(N + 1, dtype=torch.int32, device=dev)
-        if rows is None:
-            rows = torch.empty(T, dtype=torch.int32, device=dev)
-        if next_token is None:
-            next_token = torch.empty(N, dtype=torch.int32, device=dev)
+
+    def call(handle):
+        counts = torch.empty((N + 1,), dtype=torch.int32, device=dev) if cu_accept is None else cu_accept
+        packed = torch.empty((T,), dtype=torch.int32, device=dev) if rows is None else rows
+        nxt = torch.empty((N,), dtype=torch.int32, device=dev) if next_token is None else next_token
         if workspace is None:
-            workspace = torch.empty(lib.kda_draft_verify_workspace_size(N), dtype=torch.uint8, device=dev)
-        rc = lib.kda_draft_verify(tok, cu, par, target_probs.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-                                  code, u_accept.data_ptr(), u_sample.data_ptr(), N, T, V,
-                                  target_probs.stride(0) if T > 1 else 0,
-                                  draft_probs.stride(0) if draft_probs is not None and T > 1 else 0,
-                                  _ints(cu_accept, "cu_accept", N + 1), _ints(rows, "rows", T),
-                                  _ints(next_token, "next_token", N), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), handle)
-    _check(rc, "kda_draft_verify")
-    return cu_accept, rows, next_token
+            size = lib.kda_draft_verify_workspace_size(N)
+            ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+        else:
+            ws, size = workspace, workspace.numel() * workspace.element_size()
+        q, qs = (None, 0) if draft_probs is None else (draft_probs.data_ptr(), draft_probs.stride(0) if T > 1 else 0)
+        _check(lib.kda_draft_verify(tok, cu, par, target_probs.data_ptr(), q, code, u_accept.data_ptr(), u_sample.data_ptr(), N, T,
+                                    V, target_probs.stride(0) if T > 1 else 0, qs, _ints(counts, "cu_accept", N + 1),
+                                    _ints(packed, "rows", T), _ints(nxt, "next_token", N), ws.data_ptr(), size, handle),
+               "kda_draft_verify")
+        return counts, packed, nxt
+
+    return _on(dev, stream, call)
