@@ -34,10 +34,12 @@ namespace {
 
 using namespace spec;
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kSegUnit = 1024;    // elements of one segment step of a warp
+constexpr int kSegUnit = 1024;    // elements of a segment (of one step of it, where a row has more than kMaxSegs)
+constexpr int kLoadUnit = 512;    // elements that a warp has in flight
 constexpr int kMaxSegs = 1024;    // segments of a row
+constexpr int kMaxCluster = 8;    // CTAs per sequence
 constexpr int kMaxNodes = KDA_MAX_TREE_NODES;
 
 struct VerifyParams {
@@ -97,14 +99,13 @@ __device__ __forceinline__ void load_vec(const Row<T> &r, int64_t e, int V, floa
 
 // Sum of the residual over the segment steps [s0, s1) by one warp (every lane returns it).
 template <typename T, bool kDraft>
-__device__ double segment_sum(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t s0, int64_t s1, double A,
-                              const int32_t *removed, int nremoved) {
-    constexpr int W = Elem<T>::kVec, L = kSegUnit / 32 / W;  // vectors per lane and step
+__device__ __forceinline__ double segment_sum(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t s0, int64_t s1,
+                                              double A, const int32_t *removed, int nremoved) {
+    constexpr int W = Elem<T>::kVec, L = kLoadUnit / 32 / W;  // vectors per lane
     const int lane = threadIdx.x & 31;
     const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
     Pair acc{0.f, 0.f};
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t e0 = s * kSegUnit - shift;
+    for (int64_t e0 = s0 * kSegUnit - shift; e0 < s1 * kSegUnit - shift; e0 += kLoadUnit) {
         float pv[L][W], qv[kDraft ? L : 1][W];
 #pragma unroll
         for (int i = 0; i < L; ++i) load_vec(p, e0 + (i * 32 + lane) * W, V, pv[i]);
@@ -114,7 +115,7 @@ __device__ double segment_sum(const Row<T> &p, const Row<T> &q, bool use_q, int 
         }
         for (int j = 0; j < nremoved; ++j) {  // refused certain drafts: no mass
             const int64_t x = removed[j] - e0;
-            if (x >= 0 && x < kSegUnit) {
+            if (x >= 0 && x < kLoadUnit) {
 #pragma unroll
                 for (int i = 0; i < L; ++i)
 #pragma unroll
@@ -150,54 +151,81 @@ __device__ __forceinline__ double warp_scan(double x) {  // inclusive, in lane o
     return x;
 }
 
-// The lowest element whose running sum, `before` included, passes `point`, within the steps [s0, s1); the last
-// element with mass if rounding leaves none; -1 without mass.  By one warp.
+// The lowest element of the steps [s0, s1) whose running sum, `before` included, passes `point`; the last element with
+// mass if rounding leaves none; -1 without mass.  By one warp: the lane sums of 32 consecutive elements each find the
+// run, then one element per lane.
 template <typename T, bool kDraft>
-__device__ int segment_find(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t s0, int64_t s1, double A,
-                            const int32_t *removed, int nremoved, double before, double point) {
-    constexpr int W = Elem<T>::kVec, L = kSegUnit / 32 / W;
+__device__ __forceinline__ int segment_find(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t s0, int64_t s1,
+                                            double A, const int32_t *removed, int nremoved, double before, double point) {
+    constexpr int W = Elem<T>::kVec, kRun = kSegUnit / 32;
     const int lane = threadIdx.x & 31;
-    int last = -1;
+    const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
+    bool found = false;
+    int64_t run0 = 0;           // first element of the run that holds the point
+    double run_before = 0.0;
     for (int64_t s = s0; s < s1; ++s) {
-        const int64_t e0 = s * kSegUnit - shift;
-        for (int i = 0; i < L; ++i) {
-            const int64_t e = e0 + (i * 32 + lane) * W;
+        const int64_t mine0 = s * kSegUnit - shift + lane * kRun;
+        Pair acc{0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kRun / W; ++i) {
             float pv[W], qv[W];
-            load_vec(p, e, V, pv);
-            if (kDraft && use_q) load_vec(q, e, V, qv);
-            double r[W], mine = 0.0;
+            load_vec(p, mine0 + i * W, V, pv);
+            if (kDraft && use_q) load_vec(q, mine0 + i * W, V, qv);
+            for (int j = 0; j < nremoved; ++j) {
+                const int64_t x = removed[j] - (mine0 + i * W);
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    if (x == w) pv[w] = 0.f;
+            }
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                double x = kDraft && use_q ? static_cast<double>(pv[w]) - A * static_cast<double>(qv[w]) : static_cast<double>(pv[w]);
-                for (int j = 0; j < nremoved; ++j)
-                    if (removed[j] == e + w) x = 0.0;
-                r[w] = x > 0.0 ? x : 0.0;
-                mine += r[w];
+                const Pair r = kDraft && use_q ? residual(pv[w], qv[w], ah, al) : Pair{pv[w] > 0.f ? pv[w] : 0.f, 0.f};
+                add(acc, r.hi, r.lo);
             }
-            const double upto = warp_scan(mine);
-            double run = before + (upto - mine);
-            int hit = -1, top = -1;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                run += r[w];
-                if (r[w] > 0.0) {
-                    top = static_cast<int>(e) + w;
-                    if (hit < 0 && run > point) hit = top;
-                }
-            }
-            const uint32_t any = __ballot_sync(0xffffffffu, hit >= 0);
-            if (any) return __shfl_sync(0xffffffffu, hit, __ffs(any) - 1);
-            const uint32_t some = __ballot_sync(0xffffffffu, top >= 0);
-            if (some) last = __shfl_sync(0xffffffffu, top, 31 - __clz(some));
-            before += __shfl_sync(0xffffffffu, upto, 31);
         }
+        const double mine = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
+        const double upto = warp_scan(mine), excl = before + (upto - mine);
+        const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0.0 && before + upto > point);
+        const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
+        if (hit || some) {      // (without a hit: the last run with mass, until a later step has one)
+            const int src = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+            found = true;
+            run0 = __shfl_sync(0xffffffffu, mine0, src);
+            run_before = __shfl_sync(0xffffffffu, excl, src);
+        }
+        if (hit) break;
+        before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return last;
+    if (!found) return -1;
+    const int64_t e = run0 + lane;
+    double x = 0.0;
+    if (e >= 0 && e < V) {
+        x = static_cast<double>(Elem<T>::to_f(p.base[e]));
+        if (kDraft && use_q) x -= A * static_cast<double>(Elem<T>::to_f(q.base[e]));
+        for (int j = 0; j < nremoved; ++j)
+            if (removed[j] == e) x = 0.0;
+        if (!(x > 0.0)) x = 0.0;
+    }
+    const double upto = run_before + warp_scan(x);
+    const uint32_t hit = __ballot_sync(0xffffffffu, x > 0.0 && upto > point);
+    const uint32_t some = __ballot_sync(0xffffffffu, x > 0.0);
+    if (!some) return -1;
+    return static_cast<int>(run0) + (hit ? __ffs(hit) - 1 : 31 - __clz(some));
+}
+
+// The children of a node as bits, from the parents that a warp's lanes hold.
+__device__ __forceinline__ uint64_t children(const int (&par)[2], int node) {
+    return (static_cast<uint64_t>(__ballot_sync(0xffffffffu, par[1] == node)) << 32) | __ballot_sync(0xffffffffu, par[0] == node);
 }
 
 // What the walk waits for, decided by warp 0 of every CTA alike and read by all of its threads.
 enum Step : int { kPassResidual, kPassFinal, kDone };
+struct __align__(16) Node {
+    double u, p, q;              // its number, and its token's mass in its parent's rows
+    int tok, pad;
+};
 struct Shared {
+    Node node[kMaxNodes];
     double sums[2][kMaxSegs];    // this CTA's segments (in place), one buffer per pass parity
     double all[kMaxSegs];        // every segment of the last pass
     double A, R, total;
@@ -207,7 +235,7 @@ struct Shared {
 };
 
 template <typename T, bool kDraft>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyParams p) {
     __shared__ Shared sh;
     __shared__ int warp_tot[kVerWarps];
     __shared__ bool is_last;
@@ -223,8 +251,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     const int m = err ? 0 : static_cast<int>(t1 - t0);
 
     // the nodes, two per lane (node lane and lane + 32), in warp 0 of every CTA
-    int par[2] = {-2, -2}, tok[2] = {0, 0};
-    double u[2] = {0, 0}, px[2] = {0, 0}, qx[2] = {1, 1};
+    int par[2] = {-2, -2}, tok[2] = {-1, -1};
     uint64_t accepted = 0;
     int cur = 0;
     double A = 0.0, R = 1.0;
@@ -238,14 +265,14 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
             if (i >= 1 && i < m) {
                 par[w] = p.parent ? p.parent[t0 + i] : i - 1;
                 tok[w] = p.tokens[t0 + i];
-                u[w] = static_cast<double>(p.u_accept[t0 + i]);
+                const float u = p.u_accept[t0 + i];
                 if (par[w] < 0 || par[w] >= i || tok[w] < 0 || tok[w] >= p.V) {
                     bad = true;
-                    par[w] = -2;
-                    tok[w] = 0;
                 } else {
-                    px[w] = static_cast<double>(Elem<T>::to_f(static_cast<const T *>(p.target)[(t0 + par[w]) * p.ts + tok[w]]));
-                    if (kDraft) qx[w] = static_cast<double>(Elem<T>::to_f(static_cast<const T *>(p.draft)[(t0 + par[w]) * p.ds + tok[w]]));
+                    Node nd{static_cast<double>(u), 0.0, 1.0, tok[w], 0};
+                    nd.p = static_cast<double>(Elem<T>::to_f(static_cast<const T *>(p.target)[(t0 + par[w]) * p.ts + tok[w]]));
+                    if (kDraft) nd.q = static_cast<double>(Elem<T>::to_f(static_cast<const T *>(p.draft)[(t0 + par[w]) * p.ds + tok[w]]));
+                    sh.node[i] = nd;
                 }
             }
         }
@@ -253,13 +280,21 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
         if (lane == 0) {
             sh.step = (err || m == 0) ? kDone : kPassResidual;
             sh.nremoved = 0;
+            if (rank == 0 && err) atomicOr(p.status, err);
         }
         accepted = (err || m == 0) ? 0ull : 1ull;
     }
-    if (rank == 0 && threadIdx.x == 0 && err) atomicOr(p.status, err);
     __syncthreads();
     bool dead = sh.step == kDone;
     __syncthreads();
+    bool told = false;         // this sequence's accepted nodes are published
+    // publishes the accepted nodes and counts the sequence off (early: the packing needs no token)
+    auto publish = [&] {
+        p.accepted[n] = accepted;
+        __threadfence();
+        is_last = atomicAdd(p.status + 1, 1u) == static_cast<uint32_t>(p.N) - 1;
+        told = true;
+    };
 
     int token = -1;
     int parity = 0;
@@ -274,32 +309,26 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
                     R = sh.total;
                     pending = false;
                 }
-                while (true) {
-                    const uint64_t kids = (static_cast<uint64_t>(__ballot_sync(0xffffffffu, par[1] == cur)) << 32) |
-                                          __ballot_sync(0xffffffffu, par[0] == cur);
-                    const uint64_t open = kids & ~tried;
-                    if (!open) break;
-                    const int c = __ffsll(static_cast<long long>(open)) - 1;
-                    const int src = c & 31;
-                    const double cu_ = __shfl_sync(0xffffffffu, c < 32 ? u[0] : u[1], src);
-                    const double cp = __shfl_sync(0xffffffffu, c < 32 ? px[0] : px[1], src);
-                    const double cq = __shfl_sync(0xffffffffu, c < 32 ? qx[0] : qx[1], src);
-                    const int ct = __shfl_sync(0xffffffffu, c < 32 ? tok[0] : tok[1], src);
-                    double rx = cp;
+                uint64_t kids = children(par, cur);
+                while (kids & ~tried) {
+                    const int c = __ffsll(static_cast<long long>(kids & ~tried)) - 1;
+                    const Node nd = sh.node[c];
+                    double rx = nd.p;
                     if (kDraft) {
-                        rx = cp - A * cq;
-                    } else {
-                        for (int j = 0; j < nrem; ++j)
-                            if (sh.removed[j] == ct) rx = 0.0;
+                        rx -= A * nd.q;
+                    } else if (tried) {  // a token refused before has no mass left
+                        const bool same = (tok[0] == nd.tok && ((tried >> lane) & 1)) || (tok[1] == nd.tok && ((tried >> (lane + 32)) & 1));
+                        if (__any_sync(0xffffffffu, same)) rx = 0.0;
                     }
                     rx = rx > 0.0 ? rx : 0.0;
-                    if (cu_ * cq * R < rx) {
+                    if (nd.u * nd.q * R < rx) {
                         accepted |= 1ull << c;
                         cur = c;
                         A = 0.0;
                         R = 1.0;
                         tried = 0;
                         nrem = 0;
+                        kids = children(par, cur);
                     } else {
                         tried |= 1ull << c;
                         if (kDraft) {
@@ -308,17 +337,12 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
                             break;
                         }
                         R -= rx;
-                        if (lane == 0) sh.removed[nrem] = ct;
+                        if (lane == 0) sh.removed[nrem] = nd.tok;
                         ++nrem;
-                        __syncwarp();
                     }
                 }
                 // a refusal with children left to try needs R; otherwise the same pass serves the draw
-                if (pending) {
-                    const uint64_t kids = (static_cast<uint64_t>(__ballot_sync(0xffffffffu, par[1] == cur)) << 32) |
-                                          __ballot_sync(0xffffffffu, par[0] == cur);
-                    if (kids & ~tried) step = kPassResidual;
-                }
+                if (pending && (kids & ~tried)) step = kPassResidual;
             } else {
                 A = 0.0;
                 nrem = 0;
@@ -329,6 +353,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
                 sh.step = step;
                 sh.nremoved = nrem;
                 sh.use_q = kDraft && A != 0.0;
+                if (rank == 0 && step == kPassFinal && !told) publish();
             }
         }
         __syncthreads();
@@ -416,9 +441,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     // ---- the sequence's outputs; the last sequence to finish packs them all
     if (rank == 0 && threadIdx.x == 0) {
         p.next_token[n] = token;
-        p.accepted[n] = accepted;
-        __threadfence();
-        is_last = atomicAdd(p.status + 1, 1u) == static_cast<uint32_t>(p.N) - 1;
+        if (!told) publish();
     }
     if (rank == 0) {
         __syncthreads();
@@ -526,9 +549,10 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
     p.nseg = static_cast<int>((steps + p.seg_steps - 1) / p.seg_steps);
     const int sms = sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
-    // CTAs per sequence: enough to cover the SMs twice, no more than the row's segments can use
+    // CTAs per sequence: as many as leave all sequences resident at once (four CTAs per SM), no more than the row's
+    // segments can use
     int C = 1;
-    while (C < 8 && static_cast<int64_t>(N) * C < 2 * sms && 2 * C * kda::kVerWarps <= p.nseg + kda::kVerWarps) C *= 2;
+    while (C < kda::kMaxCluster && static_cast<int64_t>(N) * 2 * C <= 4 * sms && C * kda::kVerWarps < p.nseg) C *= 2;
     if (dtype == KDA_BF16)
         return draft_probs ? kda::launch_verify<__nv_bfloat16, true>(p, C, s) : kda::launch_verify<__nv_bfloat16, false>(p, C, s);
     return draft_probs ? kda::launch_verify<float, true>(p, C, s) : kda::launch_verify<float, false>(p, C, s);

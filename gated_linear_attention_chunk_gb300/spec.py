@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -36,6 +37,7 @@ class _PagedKV(ctypes.Structure):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object around it)
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _code(t: torch.Tensor, name: str) -> int:
@@ -101,6 +103,30 @@ def _on(device, stream, call):
 def _check(rc: int, where: str):
     if rc:
         raise KdaError(rc, where)
+
+
+_KEEP_BYTES = 64 << 20  # scratch up to this size is kept for the next call
+_scratch = threading.local()
+
+
+def _workspace(workspace, nbytes: int, device, handle):
+    """The caller's workspace, or scratch: ``(address, bytes, owner)``.
+
+    Scratch is one buffer per thread, device and stream, since the calls on a stream run one after the other; it grows, and holds
+    nothing from call to call.  Calls that a graph records, and large ones, get a buffer of their own."""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if nbytes <= _KEEP_BYTES and not _capturing():
+        kept = _scratch.__dict__
+        key = (device.index, handle)
+        entry = kept.get(key)
+        if entry is None or entry[1] < nbytes:
+            size = max(nbytes, 1 << 16)
+            buf = torch.empty((size,), dtype=torch.uint8, device=device)
+            entry = kept[key] = (buf.data_ptr(), size, buf)
+        return entry
+    buf = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    return buf.data_ptr(), nbytes, buf
 
 
 def _cache(k_pages, v_pages, block_table, ctx_len, dtype, Hkv: int, dk: int, dv: int) -> Tuple[_PagedKV, int, int]:
@@ -236,14 +262,13 @@ def kda_tree_attn(q, k, v, k_pages, v_pages, block_table, ctx_len, cu_nodes, par
         dev = q.device
         out = torch.empty((T, Hq, dv), dtype=dt, device=dev) if o is None else o
         sums = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None and return_lse else lse
-        if workspace is None:  # (0 for sizes that the call itself refuses)
-            size = lib.kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx) or KDA_WS_HEADER_BYTES
-            ws = torch.empty((size,), dtype=torch.uint8, device=dev)
-        else:
-            ws, size = workspace, workspace.numel() * workspace.element_size()
+        need = 0  # (0 for sizes that the call itself refuses)
+        if workspace is None:
+            need = lib.kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx) or KDA_WS_HEADER_BYTES
+        ws, size, _ = _workspace(workspace, need, dev, handle)
         _check(lib.kda_tree_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, ctypes.byref(cache), cu, par, N, T, Hq, Hkv, dk,
                                  dv, qs, ks, vs, max_nodes, dk ** -0.5 if scale is None else scale, out.data_ptr(),
-                                 None if sums is None else sums.data_ptr(), ws.data_ptr(), size, handle), "kda_tree_attn")
+                                 None if sums is None else sums.data_ptr(), ws, size, handle), "kda_tree_attn")
         return out, sums
 
     return _on(q.device, stream, call)
@@ -265,10 +290,10 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, ctx_len, cu, rows=None
 
     def call(handle):
         new = torch.empty((N,), dtype=torch.int32, device=k.device) if new_len is None else new_len
-        ws = torch.empty((KDA_WS_HEADER_BYTES,), dtype=torch.uint8, device=k.device) if workspace is None else workspace
+        ws, size, _ = _workspace(workspace, KDA_WS_HEADER_BYTES, k.device, handle)
         _check(lib.kda_cache_append(k.data_ptr(), v.data_ptr(), code, ctypes.byref(cache), c, r, N,
                                     T if rows is None else rows.shape[0], T, Hkv, dk, dv, ks, vs,
-                                    _ints(new, "new_len", N), ws.data_ptr(), ws.numel() * ws.element_size(), handle),
+                                    _ints(new, "new_len", N), ws, size, handle),
                "kda_cache_append")
         return new
 
@@ -304,18 +329,17 @@ def kda_draft_verify(tokens, cu_nodes, target_probs, u_accept, u_sample, parent=
     dev = target_probs.device
 
     def call(handle):
-        counts = torch.empty((N + 1,), dtype=torch.int32, device=dev) if cu_accept is None else cu_accept
-        packed = torch.empty((T,), dtype=torch.int32, device=dev) if rows is None else rows
-        nxt = torch.empty((N,), dtype=torch.int32, device=dev) if next_token is None else next_token
-        if workspace is None:
-            size = lib.kda_draft_verify_workspace_size(N)
-            ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+        if cu_accept is None and rows is None and next_token is None:  # one allocation for the three
+            counts, packed, nxt = torch.empty((2 * N + 1 + T,), dtype=torch.int32, device=dev).split((N + 1, T, N))
         else:
-            ws, size = workspace, workspace.numel() * workspace.element_size()
+            counts = torch.empty((N + 1,), dtype=torch.int32, device=dev) if cu_accept is None else cu_accept
+            packed = torch.empty((T,), dtype=torch.int32, device=dev) if rows is None else rows
+            nxt = torch.empty((N,), dtype=torch.int32, device=dev) if next_token is None else next_token
+        ws, size, _ = _workspace(workspace, KDA_WS_HEADER_BYTES + 8 * N, dev, handle)
         q, qs = (None, 0) if draft_probs is None else (draft_probs.data_ptr(), draft_probs.stride(0) if T > 1 else 0)
         _check(lib.kda_draft_verify(tok, cu, par, target_probs.data_ptr(), q, code, u_accept.data_ptr(), u_sample.data_ptr(), N, T,
                                     V, target_probs.stride(0) if T > 1 else 0, qs, _ints(counts, "cu_accept", N + 1),
-                                    _ints(packed, "rows", T), _ints(nxt, "next_token", N), ws.data_ptr(), size, handle),
+                                    _ints(packed, "rows", T), _ints(nxt, "next_token", N), ws, size, handle),
                "kda_draft_verify")
         return counts, packed, nxt
 
