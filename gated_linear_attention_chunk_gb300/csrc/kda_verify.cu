@@ -10,14 +10,14 @@
 // One cluster of CTAs per sequence.  Everything the walk compares -- parent, token, number, p_x and q_x
 // of every node -- is gathered at once, two nodes per lane of one warp; the walk itself then runs in registers and
 // touches a whole row only after a refusal (draft rows given) and for the final draw.  Such a pass cuts
-// the row into segments of kSeg elements, a warp each, and leaves the segments' sums in shared memory,
+// the row into segments of kSegUnit elements (or a multiple), two per warp at a time, and leaves the segments' sums in shared memory,
 // where every CTA of the cluster reads them all in the same order; the draw then needs only the one segment that
 // holds its point again.  So a sequence costs about one reading of one row (two with draft rows),
 // which bounds it: the rest is the latency of the walk's dependent loads.
 //
 // Precision: the answers are whole numbers, so a rounding shows only next to a border, where a flat
 // distribution over 10^5 tokens has one every 10^-5.  p - A q is carried as an unevaluated fp32 pair with
-// the error terms of its product and difference, sums as pairs within a thread and in fp64 across threads:
+// the error terms of its product and difference, and so are all sums:
 // about 1e-13 of the mass, at the cost of about 20 fp32 operations per element (fp64 arithmetic per element would
 // be several times slower than the loads).  The order of the sums is fixed and does not depend on the cluster's size.
 #include <cooperative_groups.h>
@@ -36,9 +36,8 @@ using namespace spec;
 
 constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kSegUnit = 1024;    // elements of a segment (of one step of it, where a row has more than kMaxSegs)
-constexpr int kLoadUnit = 512;    // elements that a warp has in flight
-constexpr int kMaxSegs = 1024;    // segments of a row
+constexpr int kSegUnit = 256;     // elements of a segment (of one step of it, where a row has more than kMaxSegs)
+constexpr int kMaxSegs = 512;     // segments of a row
 constexpr int kMaxCluster = 8;    // CTAs per sequence
 constexpr int kMaxNodes = KDA_MAX_TREE_NODES;
 
@@ -97,126 +96,168 @@ __device__ __forceinline__ void load_vec(const Row<T> &r, int64_t e, int V, floa
     }
 }
 
-// Sum of the residual over the segment steps [s0, s1) by one warp (every lane returns it).
-template <typename T, bool kDraft>
-__device__ __forceinline__ double segment_sum(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t s0, int64_t s1,
-                                              double A, const int32_t *removed, int nremoved) {
-    constexpr int W = Elem<T>::kVec, L = kLoadUnit / 32 / W;  // vectors per lane
+// Refused certain drafts (two per lane): takes their mass out of the elements e0 + (i * 32 + lane) * W + w of a step.
+template <int L, int W>
+__device__ __forceinline__ void take_out(float (&v)[L][W], int64_t e0, const int (&gone)[2]) {
     const int lane = threadIdx.x & 31;
-    const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
-    Pair acc{0.f, 0.f};
-    for (int64_t e0 = s0 * kSegUnit - shift; e0 < s1 * kSegUnit - shift; e0 += kLoadUnit) {
-        float pv[L][W], qv[kDraft ? L : 1][W];
 #pragma unroll
-        for (int i = 0; i < L; ++i) load_vec(p, e0 + (i * 32 + lane) * W, V, pv[i]);
-        if (kDraft && use_q) {
+    for (int g = 0; g < 2; ++g) {
+        const int64_t off = gone[g] - e0;
+        for (uint32_t hit = __ballot_sync(0xffffffffu, gone[g] >= 0 && off >= 0 && off < L * W * 32); hit; hit &= hit - 1) {
+            const int x = __shfl_sync(0xffffffffu, static_cast<int>(off), __ffs(hit) - 1);
 #pragma unroll
-            for (int i = 0; i < L; ++i) load_vec(q, e0 + (i * 32 + lane) * W, V, qv[kDraft ? i : 0]);
+            for (int i = 0; i < L; ++i)
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    if (x == (i * 32 + lane) * W + w) v[i][w] = 0.f;
         }
-        for (int j = 0; j < nremoved; ++j) {  // refused certain drafts: no mass
-            const int64_t x = removed[j] - e0;
-            if (x >= 0 && x < kLoadUnit) {
-#pragma unroll
-                for (int i = 0; i < L; ++i)
-#pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        if (x == (i * 32 + lane) * W + w) pv[i][w] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if (kDraft && use_q) {
-                    const Pair r = residual(pv[i][w], qv[kDraft ? i : 0][w], ah, al);
-                    add(acc, r.hi, r.lo);
-                } else {
-                    add(acc, pv[i][w] > 0.f ? pv[i][w] : 0.f, 0.f);
-                }
-            }
     }
-    double sum = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
 }
 
-__device__ __forceinline__ double warp_scan(double x) {  // inclusive, in lane order
+// Sums of the residual over two neighbouring segments by one warp: the first in lane 0, the second in lane 16.  Lanes
+// and warps are joined in pairs of fp32 as well: fp64 additions here would take longer than the loads.
+template <typename T, bool kDraft>
+__device__ __forceinline__ Pair segment_sums(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t first,
+                                               int steps, double A, const int (&gone)[2]) {
+    constexpr int W = Elem<T>::kVec, L = kSegUnit / 32 / W;  // vectors per lane, segment and step
+    const int lane = threadIdx.x & 31;
+    const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
+    Pair acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    for (int s = 0; s < steps; ++s) {
+        float pv[2][L][W], qv[2][kDraft ? L : 1][W];
+        int64_t e0[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            e0[g] = first + static_cast<int64_t>(g * steps + s) * kSegUnit;
+#pragma unroll
+            for (int i = 0; i < L; ++i) load_vec(p, e0[g] + (i * 32 + lane) * W, V, pv[g][i]);
+            if (kDraft && use_q) {
+#pragma unroll
+                for (int i = 0; i < L; ++i) load_vec(q, e0[g] + (i * 32 + lane) * W, V, qv[g][kDraft ? i : 0]);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (!kDraft) take_out(pv[g], e0[g], gone);
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    if (kDraft && use_q) {
+                        const Pair r = residual(pv[g][i][w], qv[g][kDraft ? i : 0][w], ah, al);
+                        add(acc[g], r.hi, r.lo);
+                    } else {
+                        add(acc[g], pv[g][i][w] > 0.f ? pv[g][i][w] : 0.f, 0.f);
+                    }
+                }
+        }
+    }
+    const bool low = lane < 16;
+    Pair mine = low ? acc[0] : acc[1];
+    const Pair give = low ? acc[1] : acc[0];
+    add(mine, __shfl_xor_sync(0xffffffffu, give.hi, 16), __shfl_xor_sync(0xffffffffu, give.lo, 16));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, mine.hi, o), lo = __shfl_xor_sync(0xffffffffu, mine.lo, o);
+        add(mine, hi, lo);
+    }
+    return mine;
+}
+
+__device__ __forceinline__ Pair warp_scan(Pair x) {  // inclusive, in lane order
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const float hi = __shfl_up_sync(0xffffffffu, x.hi, o), lo = __shfl_up_sync(0xffffffffu, x.lo, o);
+        if (lane >= o) add(x, hi, lo);
     }
     return x;
 }
+__device__ __forceinline__ double value(Pair x) { return static_cast<double>(x.hi) + static_cast<double>(x.lo); }
+__device__ __forceinline__ Pair from_lane(Pair x, int lane) {
+    return Pair{__shfl_sync(0xffffffffu, x.hi, lane), __shfl_sync(0xffffffffu, x.lo, lane)};
+}
 
-// The lowest element of the steps [s0, s1) whose running sum, `before` included, passes `point`; the last element with
-// mass if rounding leaves none; -1 without mass.  By one warp: the lane sums of 32 consecutive elements each find the
-// run, then one element per lane.
+// Where a running sum passes a point: of one weight per lane, in lane order, the first lane whose sum, `before`
+// included, is above `point` (`before` becomes the sum ahead of it); otherwise hit is false, the last lane with mass or -1
+// is returned, and `before` becomes the sum of all.
+__device__ __forceinline__ int pass_point(Pair weight, double &before, double point, bool &hit) {
+    const Pair upto = warp_scan(weight);
+    const double sum = before + value(upto);
+    const uint32_t over = __ballot_sync(0xffffffffu, weight.hi > 0.f && sum > point);
+    const uint32_t some = __ballot_sync(0xffffffffu, weight.hi > 0.f);
+    hit = over != 0;
+    const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : -1;
+    const double own = value(weight);
+    if (hit) before = __shfl_sync(0xffffffffu, sum - own, at);
+    else before = __shfl_sync(0xffffffffu, sum, 31);
+    return at;
+}
+
+// The element of the steps [s0, s1) at which the running sum passes `point` (as pass_point).  By one warp: first the
+// run of kRun consecutive elements, then the element, one per lane.
 template <typename T, bool kDraft>
 __device__ __forceinline__ int segment_find(const Row<T> &p, const Row<T> &q, bool use_q, int shift, int V, int64_t s0, int64_t s1,
-                                            double A, const int32_t *removed, int nremoved, double before, double point) {
+                                            double A, const int (&gone)[2], double before, double point) {
     constexpr int W = Elem<T>::kVec, kRun = kSegUnit / 32;
     const int lane = threadIdx.x & 31;
     const float ah = static_cast<float>(A), al = static_cast<float>(A - static_cast<double>(ah));
-    bool found = false;
-    int64_t run0 = 0;           // first element of the run that holds the point
-    double run_before = 0.0;
+    int best = -1;
     for (int64_t s = s0; s < s1; ++s) {
-        const int64_t mine0 = s * kSegUnit - shift + lane * kRun;
-        Pair acc{0.f, 0.f};
+        const int64_t first = s * kSegUnit - shift, mine0 = first + lane * kRun;
+        Pair r[kRun], acc{0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kRun / W; ++i) {
             float pv[W], qv[W];
             load_vec(p, mine0 + i * W, V, pv);
             if (kDraft && use_q) load_vec(q, mine0 + i * W, V, qv);
-            for (int j = 0; j < nremoved; ++j) {
-                const int64_t x = removed[j] - (mine0 + i * W);
 #pragma unroll
-                for (int w = 0; w < W; ++w)
-                    if (x == w) pv[w] = 0.f;
-            }
+            for (int w = 0; w < W; ++w)
+                r[i * W + w] = kDraft && use_q ? residual(pv[w], qv[w], ah, al) : Pair{pv[w] > 0.f ? pv[w] : 0.f, 0.f};
+        }
+        if (!kDraft) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const Pair r = kDraft && use_q ? residual(pv[w], qv[w], ah, al) : Pair{pv[w] > 0.f ? pv[w] : 0.f, 0.f};
-                add(acc, r.hi, r.lo);
+            for (int g = 0; g < 2; ++g) {
+                const int64_t off = gone[g] - first;
+                for (uint32_t out = __ballot_sync(0xffffffffu, gone[g] >= 0 && off >= 0 && off < kSegUnit); out; out &= out - 1) {
+                    const int x = __shfl_sync(0xffffffffu, static_cast<int>(off), __ffs(out) - 1);
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i)
+                        if (x == lane * kRun + i) r[i] = Pair{0.f, 0.f};
+                }
             }
         }
-        const double mine = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
-        const double upto = warp_scan(mine), excl = before + (upto - mine);
-        const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0.0 && before + upto > point);
-        const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
-        if (hit || some) {      // (without a hit: the last run with mass, until a later step has one)
-            const int src = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-            found = true;
-            run0 = __shfl_sync(0xffffffffu, mine0, src);
-            run_before = __shfl_sync(0xffffffffu, excl, src);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) add(acc, r[i].hi, r[i].lo);
+        double ahead = before;
+        bool hit;
+        const int run = pass_point(acc, ahead, point, hit);
+        if (run >= 0) {
+            Pair mine{0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const Pair x = from_lane(r[i], run);
+                if (lane == i) mine = x;
+            }
+            double in = hit ? ahead : -INFINITY;
+            bool sure;
+            const int e = pass_point(mine, in, point, sure);
+            if (e >= 0) best = static_cast<int>(first) + run * kRun + e;
         }
         if (hit) break;
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        before = ahead;
     }
-    if (!found) return -1;
-    const int64_t e = run0 + lane;
-    double x = 0.0;
-    if (e >= 0 && e < V) {
-        x = static_cast<double>(Elem<T>::to_f(p.base[e]));
-        if (kDraft && use_q) x -= A * static_cast<double>(Elem<T>::to_f(q.base[e]));
-        for (int j = 0; j < nremoved; ++j)
-            if (removed[j] == e) x = 0.0;
-        if (!(x > 0.0)) x = 0.0;
-    }
-    const double upto = run_before + warp_scan(x);
-    const uint32_t hit = __ballot_sync(0xffffffffu, x > 0.0 && upto > point);
-    const uint32_t some = __ballot_sync(0xffffffffu, x > 0.0);
-    if (!some) return -1;
-    return static_cast<int>(run0) + (hit ? __ffs(hit) - 1 : 31 - __clz(some));
+    return best;
 }
 
 // The children of a node as bits, from the parents that a warp's lanes hold.
 __device__ __forceinline__ uint64_t children(const int (&par)[2], int node) {
     return (static_cast<uint64_t>(__ballot_sync(0xffffffffu, par[1] == node)) << 32) | __ballot_sync(0xffffffffu, par[0] == node);
 }
+
+// The cluster barrier in two halves.
+__device__ __forceinline__ void cg_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cg_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // What the walk waits for, decided by warp 0 of every CTA alike and read by all of its threads.
 enum Step : int { kPassResidual, kPassFinal, kDone };
@@ -226,12 +267,12 @@ struct __align__(16) Node {
 };
 struct Shared {
     Node node[kMaxNodes];
-    double sums[2][kMaxSegs];    // this CTA's segments (in place), one buffer per pass parity
-    double all[kMaxSegs];        // every segment of the last pass
+    Pair sums[2][kMaxSegs];      // this CTA's segments (in place), one buffer per pass parity
+    Pair all[kMaxSegs];          // every segment of the last pass
     double A, R, total;
     int32_t removed[kMaxNodes];
+    uint64_t accepted;
     int nremoved, cur, step, use_q;
-    int count_before;            // last CTA: running counts
 };
 
 template <typename T, bool kDraft>
@@ -246,6 +287,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int64_t t0 = p.cu[n], t1 = p.cu[n + 1];
+    const float u_draw = p.u_sample[n];
     uint32_t err = 0;
     if (t0 < 0 || t0 > t1 || t1 > p.T || t1 - t0 > kMaxNodes || (n == 0 && t0 != 0)) err = DEV_ERR_SEQLENS;
     const int m = err ? 0 : static_cast<int>(t1 - t0);
@@ -280,6 +322,8 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
         if (lane == 0) {
             sh.step = (err || m == 0) ? kDone : kPassResidual;
             sh.nremoved = 0;
+            sh.accepted = 0;
+            is_last = false;
             if (rank == 0 && err) atomicOr(p.status, err);
         }
         accepted = (err || m == 0) ? 0ull : 1ull;
@@ -288,12 +332,52 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     bool dead = sh.step == kDone;
     __syncthreads();
     bool told = false;         // this sequence's accepted nodes are published
-    // publishes the accepted nodes and counts the sequence off (early: the packing needs no token)
+    // publishes the accepted nodes and counts the sequence off: as soon as the walk has ended, beside the draw's pass
+    const bool publisher = rank == 0 && threadIdx.x == 32;
     auto publish = [&] {
-        p.accepted[n] = accepted;
+        p.accepted[n] = sh.accepted;
         __threadfence();
         is_last = atomicAdd(p.status + 1, 1u) == static_cast<uint32_t>(p.N) - 1;
+        __threadfence();
         told = true;
+    };
+
+    // packs every sequence's accepted nodes: the warps but the first of the CTA that counted off last
+    bool packed = false;
+    auto pack = [&] {
+        constexpr int kPackThreads = kVerThreads - 32;
+        const int tid = threadIdx.x - 32;
+        int base_count = 0;
+        for (int base = 0; base < p.N; base += kPackThreads) {
+            const int i = base + tid;
+            const uint64_t bits = i < p.N ? __ldcg(p.accepted + i) : 0ull;
+            const int64_t first = i < p.N ? p.cu[i] : 0;
+            const int mine = __popcll(bits);
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (lane == 31) warp_tot[warp] = upto;
+            asm volatile("bar.sync 1, %0;" ::"n"(kPackThreads) : "memory");
+            int off = base_count, all = base_count;
+            for (int w = 1; w < kVerWarps; ++w) {
+                if (w < warp) off += warp_tot[w];
+                all += warp_tot[w];
+            }
+            if (i < p.N) {
+                // (overlapping ranges of a bad cu_nodes could count more than T nodes)
+                p.cu_accept[i + 1] = off + upto < p.T ? off + upto : static_cast<int32_t>(p.T);
+                uint64_t b = bits;
+                for (int at = off + upto - mine; b && at < p.T; b &= b - 1, ++at)
+                    p.rows[at] = static_cast<int32_t>(first) + __ffsll(static_cast<long long>(b)) - 1;
+            }
+            base_count = all;
+            asm volatile("bar.sync 1, %0;" ::"n"(kPackThreads) : "memory");
+        }
+        if (tid == 0) p.cu_accept[0] = 0;
+        for (int64_t i = base_count + tid; i < p.T; i += kPackThreads) p.rows[i] = -1;
     };
 
     int token = -1;
@@ -353,83 +437,66 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
                 sh.step = step;
                 sh.nremoved = nrem;
                 sh.use_q = kDraft && A != 0.0;
-                if (rank == 0 && step == kPassFinal && !told) publish();
+                sh.accepted = accepted;
             }
         }
         __syncthreads();
         const int step = sh.step, row = sh.cur, removed = sh.nremoved;
         const bool use_q = kDraft && sh.use_q;
         const double a = sh.A;
+        if (publisher && step == kPassFinal && !told) publish();
         // ---- one pass over the current row
         Row<T> pr{static_cast<const T *>(p.target) + (t0 + row) * p.ts, true};
         Row<T> qr{kDraft ? static_cast<const T *>(p.draft) + (t0 + row) * p.ds : nullptr, true};
         const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(pr.base) & 15u) / sizeof(T));
         if (kDraft) qr.vec = ((reinterpret_cast<uintptr_t>(qr.base) / sizeof(T) - shift) * sizeof(T) & 15u) == 0;
         const int64_t steps = (static_cast<int64_t>(p.V) + shift + kSegUnit - 1) / kSegUnit;
-        double *mine = sh.sums[parity];
-        for (int sg = rank + C * warp; sg < p.nseg; sg += C * kVerWarps) {
-            const int64_t s0 = static_cast<int64_t>(sg) * p.seg_steps;
-            const int64_t s1 = s0 + p.seg_steps < steps ? s0 + p.seg_steps : steps;
-            const double sum = segment_sum<T, kDraft>(pr, qr, use_q, shift, p.V, s0, s1, a, sh.removed, removed);
+        Pair *mine = sh.sums[parity];
+        int gone[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) gone[g] = !kDraft && lane + 32 * g < removed ? sh.removed[lane + 32 * g] : -1;
+        for (int sg = 2 * (rank + C * warp); sg < p.nseg; sg += 2 * C * kVerWarps) {
+            const Pair sum = segment_sums<T, kDraft>(pr, qr, use_q, shift, p.V, static_cast<int64_t>(sg) * p.seg_steps * kSegUnit - shift,
+                                                       p.seg_steps, a, gone);
             if (lane == 0) mine[sg] = sum;
+            if (lane == 16 && sg + 1 < p.nseg) mine[sg + 1] = sum;
         }
         cluster.sync();
         for (int sg = threadIdx.x; sg < p.nseg; sg += kVerThreads) {
-            const double *from = cluster.map_shared_rank(mine, sg % C);
+            const Pair *from = cluster.map_shared_rank(mine, (sg >> 1) % C);
             sh.all[sg] = from[sg];
         }
         __syncthreads();
         if (warp == 0) {
-            // lane l holds a run of consecutive segments; their scan gives the total and finds the draw
+            // lane l holds a run of consecutive segments; their scan gives the total, and the run that holds the draw
             const int per = (p.nseg + 31) / 32;
-            double part = 0.0;
+            Pair part{0.f, 0.f};
             for (int i = 0; i < per; ++i)
-                if (lane * per + i < p.nseg) part += sh.all[lane * per + i];
-            const double upto = warp_scan(part);
-            const double total = __shfl_sync(0xffffffffu, upto, 31);
+                if (lane * per + i < p.nseg) add(part, sh.all[lane * per + i].hi, sh.all[lane * per + i].lo);
+            const double total = value(from_lane(warp_scan(part), 31));
             if (step == kPassResidual) {
                 if (lane == 0) sh.total = total;
+            } else if (!(total > 0.0) && !fallback && (use_q || removed > 0)) {
+                if (lane == 0) sh.step = kPassResidual;  // a residual without mass: once more, over p itself
             } else {
-                // (a residual without mass: once more, over p itself)
-                const bool again = !(total > 0.0) && !fallback && (use_q || removed > 0);
-                if (again) {
-                    if (lane == 0) sh.step = kPassResidual;
-                } else {
-                    const double point = static_cast<double>(p.u_sample[n]) * total;
-                    int sg = -1, top = -1;
-                    double run = upto - part, before = 0.0, top_before = 0.0;
-                    for (int i = 0; i < per; ++i) {
-                        const int at = lane * per + i;
-                        if (at >= p.nseg) break;
-                        const double x = sh.all[at];
-                        if (x > 0.0) {
-                            top = at;
-                            top_before = run;
-                            if (sg < 0 && run + x > point) {
-                                sg = at;
-                                before = run;
-                            }
-                        }
-                        run += x;
-                    }
-                    uint32_t any = __ballot_sync(0xffffffffu, sg >= 0);
-                    int src = __ffs(any) - 1;
-                    if (!any) {  // rounding at the far end: the last segment with mass
-                        any = __ballot_sync(0xffffffffu, top >= 0);
-                        src = 31 - __clz(any);
-                        sg = top;
-                        before = top_before;
-                    }
-                    if (any && rank == 0) {
-                        sg = __shfl_sync(0xffffffffu, sg, src);
-                        before = __shfl_sync(0xffffffffu, before, src);
-                        const int64_t s0 = static_cast<int64_t>(sg) * p.seg_steps;
-                        const int64_t s1 = s0 + p.seg_steps < steps ? s0 + p.seg_steps : steps;
-                        token = segment_find<T, kDraft>(pr, qr, use_q, shift, p.V, s0, s1, a, sh.removed, removed, before, point);
-                    }
-                    if (lane == 0) sh.step = kDone;
+                if (rank == 0 && total > 0.0) {
+                    const double point = static_cast<double>(u_draw) * total;
+                    double before = 0.0;
+                    bool hit;
+                    const int run = pass_point(part, before, point, hit);
+                    if (!hit) before = -INFINITY;  // rounding at the far end: the last one with mass throughout
+                    const int at = run * per + lane;
+                    const int sg = pass_point(lane < per && at < p.nseg ? sh.all[at] : Pair{0.f, 0.f}, before, point, hit);
+                    if (!hit) before = -INFINITY;
+                    const int64_t s0 = static_cast<int64_t>(run * per + sg) * p.seg_steps;
+                    const int64_t s1 = s0 + p.seg_steps < steps ? s0 + p.seg_steps : steps;
+                    token = segment_find<T, kDraft>(pr, qr, use_q, shift, p.V, s0, s1, a, gone, before, point);
                 }
+                if (lane == 0) sh.step = kDone;
             }
+        } else if (rank == 0 && step == kPassFinal && is_last && !packed) {
+            pack();              // beside the draw
+            packed = true;
         }
         __syncthreads();
         dead = sh.step == kDone;
@@ -439,49 +506,14 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     }
 
     // ---- the sequence's outputs; the last sequence to finish packs them all
-    if (rank == 0 && threadIdx.x == 0) {
-        p.next_token[n] = token;
-        if (!told) publish();
-    }
+    cg_arrive();
+    if (rank == 0 && threadIdx.x == 0) p.next_token[n] = token;
+    if (publisher && !told) publish();
     if (rank == 0) {
         __syncthreads();
-        if (is_last) {
-            __threadfence();
-            if (threadIdx.x == 0) {
-                sh.count_before = 0;
-                p.cu_accept[0] = 0;
-            }
-            __syncthreads();
-            for (int base = 0; base < p.N; base += kVerThreads) {
-                const int i = base + threadIdx.x;
-                const uint64_t bits = i < p.N ? __ldcg(p.accepted + i) : 0ull;
-                const int mine = __popcll(bits);
-                int upto = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                if (lane == 31) warp_tot[warp] = upto;
-                __syncthreads();
-                int off = sh.count_before;
-                for (int w = 0; w < warp; ++w) off += warp_tot[w];
-                if (i < p.N) {
-                    // (overlapping ranges of a bad cu_nodes could count more than T nodes)
-                    p.cu_accept[i + 1] = off + upto < p.T ? off + upto : static_cast<int32_t>(p.T);
-                    const int64_t first = p.cu[i];
-                    uint64_t b = bits;
-                    for (int at = off + upto - mine; b && at < p.T; b &= b - 1, ++at)
-                        p.rows[at] = static_cast<int32_t>(first) + __ffsll(static_cast<long long>(b)) - 1;
-                }
-                __syncthreads();
-                if (threadIdx.x == kVerThreads - 1) sh.count_before = off + upto;
-                __syncthreads();
-            }
-            for (int64_t i = sh.count_before + threadIdx.x; i < p.T; i += kVerThreads) p.rows[i] = -1;
-        }
+        if (is_last && !packed && warp > 0) pack();
     }
-    cluster.sync();  // no CTA leaves while another may still read its sums
+    cg_wait();  // no CTA leaves while another may still read its sums
 }
 
 template <typename T, bool kDraft>
@@ -552,7 +584,7 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
     // CTAs per sequence: as many as leave all sequences resident at once (four CTAs per SM), no more than the row's
     // segments can use
     int C = 1;
-    while (C < kda::kMaxCluster && static_cast<int64_t>(N) * 2 * C <= 4 * sms && C * kda::kVerWarps < p.nseg) C *= 2;
+    while (C < kda::kMaxCluster && static_cast<int64_t>(N) * 2 * C <= 4 * sms && 2 * C * kda::kVerWarps < p.nseg) C *= 2;
     if (dtype == KDA_BF16)
         return draft_probs ? kda::launch_verify<__nv_bfloat16, true>(p, C, s) : kda::launch_verify<__nv_bfloat16, false>(p, C, s);
     return draft_probs ? kda::launch_verify<float, true>(p, C, s) : kda::launch_verify<float, false>(p, C, s);
