@@ -3,7 +3,9 @@
 Each CUDA translation unit is compiled in parallel with nvcc, then linked into
 one shared library with the CUDA runtime linked statically, so loading the
 library needs no GPU and no driver (the host-side argument checks work on any
-machine).
+machine).  A second library, ``_spec.so``, is the Python binding of the
+speculative-step calls (``csrc/spec_binding.cpp``, compiled with g++ against the
+installed torch and linked to libkda.so beside it).
 """
 from __future__ import annotations
 
@@ -13,11 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libkda.so")
+BINDING_SRC = os.path.join(CSRC, "spec_binding.cpp")
+BINDING = os.path.join(OUT_DIR, "_spec.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
@@ -35,13 +40,41 @@ def sources():
 
 def _deps_mtime() -> float:
     files = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-    files.append(os.path.join(os.path.dirname(PKG), "include", "kda.h"))
+    files += [BINDING_SRC, os.path.join(os.path.dirname(PKG), "include", "kda.h")]
     return max(os.path.getmtime(f) for f in files if os.path.exists(f))
+
+
+def _compile_binding() -> str:
+    """The binding's object file (its link needs libkda.so)."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    obj = os.path.join(OUT_DIR, "spec_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *("-I" + p for p in include), "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    libs = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + OUT_DIR, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L" + libs, "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libkda.so; returns its path.  Skips work when up to date."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING)):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -58,13 +91,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -19,8 +19,14 @@ def kda():
     return m
 
 
+class _PagedKV(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_void_p) for x in ("k", "v")] + [(x, ctypes.c_int64) for x in (
+        "k_page_stride", "k_row_stride", "k_head_stride", "v_page_stride", "v_row_stride", "v_head_stride", "num_pages",
+        "table_stride")] + [(x, ctypes.c_void_p) for x in ("block_table", "ctx_len")] + [
+        (x, ctypes.c_int) for x in ("page_size", "max_pages")]
+
+
 def _cache(kda, **kw):
-    from gated_linear_attention_chunk_gb300.spec import _PagedKV
     f = dict(k=FAKE, v=FAKE, k_page_stride=16 * 1024, k_row_stride=1024, k_head_stride=128, v_page_stride=16 * 1024,
              v_row_stride=1024, v_head_stride=128, num_pages=8, table_stride=4, block_table=FAKE, ctx_len=FAKE, page_size=16,
              max_pages=4)
@@ -105,7 +111,7 @@ def test_python_checks(kda):
     with pytest.raises(ValueError):
         kda.kda_rope(x, None, pos, w)
     with pytest.raises(TypeError):
-        kda.kda_rope(x.double(), None, pos, w)
+        kda.kda_rope([1.0], None, pos, w)
     with pytest.raises(ValueError):
         kda.kda_draft_verify(pos, pos, torch.zeros(2, 5), torch.zeros(2), torch.zeros(1))
 
