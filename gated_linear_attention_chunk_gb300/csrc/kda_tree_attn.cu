@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_tree_attn.cuh"
 
 namespace kda {
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
                         units[1] = s.nsplit * s.tiles * p.Hkv;
                     } else {
                         s.tiles = tiles_of(rows);
-                        split_of(s.ctx, rows, p.Hkv, s.tiles, &s.nsplit, &s.chunk);
+                        split_of(s.ctx, rows, p.Hkv, s.tiles, p.wide, &s.nsplit, &s.chunk);
                         units[0] = s.nsplit * s.tiles * p.Hkv;
                     }
                 }
@@ -241,6 +243,7 @@ struct __align__(16) TileRow {
 template <typename T, int DK, int DV>
 struct Ring {
     static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kThreads = 128;
     static constexpr int kStages = 3;
     static constexpr int kUnitsK = DK * static_cast<int>(sizeof(T)) / 16, kUnitsV = DV * static_cast<int>(sizeof(T)) / 16;
     static constexpr int kBytesK = kKeys * kUnitsK * 16, kBytesV = kKeys * kUnitsV * 16;
@@ -293,17 +296,17 @@ struct Ring {
     // Byte of unit u of row r0 + step (rows a multiple of 8 apart share their permutation).
     template <int kUnits>
     static __device__ __forceinline__ uint32_t place(int r0, int step, int u) {
-        const int r = (kAttnThreads / kUnits) % 8 == 0 ? r0 : r0 + step;
+        const int r = (kThreads / kUnits) % 8 == 0 ? r0 : r0 + step;
         return (r0 + step) * (kUnits * 16) + ((u ^ (r & 7)) << 4);
     }
     // Starts the copies of the looked-up tile of the given number: a thread takes one 16-byte unit of every
-    // kAttnThreads / units-th row.
+    // kThreads / units-th row.
     __device__ __forceinline__ void issue(const AttnParams &p, int number) {
         if (kbase) {
             const TileRow *tr = rows[number & 1];
             const uint32_t dst = ptx::smem_u32(smem) + static_cast<uint32_t>(number % kStages) * kStage;
             if constexpr (kUnitsK == kUnitsV) {
-                constexpr int kSide = kAttnThreads / kUnitsK;
+                constexpr int kSide = kThreads / kUnitsK;
                 const int u = threadIdx.x % kUnitsK, r0 = threadIdx.x / kUnitsK;
                 const char *ks = kbase + u * 16, *vs = vbase + u * 16;
 #pragma unroll
@@ -323,7 +326,7 @@ struct Ring {
     }
     template <int kUnits>
     __device__ __forceinline__ void copy(uint32_t dst, const int64_t *off, const char *base) {
-        constexpr int kSide = kAttnThreads / kUnits;
+        constexpr int kSide = kThreads / kUnits;
         const int u = threadIdx.x % kUnits, r0 = threadIdx.x / kUnits;
 #pragma unroll
         for (int i = 0; i < kKeys / kSide; ++i) {
@@ -383,8 +386,76 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The warps along the keys joined in order: maxima and sums in all of them, and of the fragments of o (row quad in
+// elements 0 and 1, quad + 8 in 2 and 3) each warp has the part kg of KW.
+template <int WARPS, int RW, int DV>
+__device__ __forceinline__ void join_warps(char *scratch, float2 (*ml)[16], float (&o)[DV / 8][4], float (&mx)[2], float (&sum)[2]) {
+    constexpr int KW = WARPS / RW, NP = DV / 8 / KW;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = warp % RW, kg = warp / RW, quad = lane >> 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    }
+    if constexpr (KW > 1) {
+        // [part][other warp][rg][fragment element][lane]
+        float *buf = reinterpret_cast<float *>(scratch) + lane;
+        auto place = [&](int part, int from) { return ((part * (KW - 1) + (from < part ? from : from - 1)) * RW + rg) * (NP * 4 * 32); };
+        __syncthreads();  // the last tile's readers are done with the stage
+        if ((lane & 3) == 0) {
+            ml[warp][quad] = make_float2(mx[0], sum[0]);
+            ml[warp][quad + 8] = make_float2(mx[1], sum[1]);
+        }
+#pragma unroll
+        for (int part = 0; part < KW; ++part)
+            if (part != kg) {
+                float *to = buf + place(part, kg);
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) to[(j * 4 + e) * 32] = o[part * NP + j][e];
+            }
+        __syncthreads();
+        float f[KW][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float2 x[KW];
+            float m = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < KW; ++g) {
+                x[g] = ml[g * RW + rg][quad + 8 * i];
+                m = fmaxf(m, x[g].x);
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            float l = 0.f;
+#pragma unroll
+            for (int g = 0; g < KW; ++g) {
+                f[g][i] = ex2(x[g].x - base);
+                l += f[g][i] * x[g].y;
+            }
+            mx[i] = m;
+            sum[i] = l;
+        }
+#pragma unroll
+        for (int part = 0; part < KW; ++part)
+            if (part == kg) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = 0.f;
+#pragma unroll
+                        for (int g = 0; g < KW; ++g)
+                            x += f[g][e >> 1] * (g == part ? o[part * NP + j][e] : buf[place(part, g) + (j * 4 + e) * 32]);
+                        o[part * NP + j][e] = x;
+                    }
+            }
+    }
+}
+
 template <int DK, int DV, int RW>
-__device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat16, DK, DV> &ring, Walk &cw, float2 (*ml)[16]) {
+__device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat16, DK, DV> &ring, Walk &cw, float2 (*ml)[16],
+                                          uint32_t (&qf)[DK / 16][4], bool same_rows) {
     using R = Ring<__nv_bfloat16, DK, DV>;
     constexpr int KW = 4 / RW, NT = 8 / KW;  // warps along the keys; 8-key columns of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -404,7 +475,7 @@ __device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat1
         node[i] = live[i] ? r / p.G : 0;
         hq[i] = cw.head * p.G + (live[i] ? r - node[i] * p.G : 0);
     }
-    uint32_t qf[DK / 16][4];
+    if (!same_rows)  // (the part before this one had the same)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) + (t0 + node[i]) * p.qs + static_cast<int64_t>(hq[i]) * DK + two;
@@ -503,86 +574,242 @@ __device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat1
         }
         ring.end_tile(ahead);
     }
+    join_warps<4, RW, DV>(ring.scratch(), ml, o, mx, sum);
+    const bool ok = may_write(p, n, flag, ring.bad_seen);
+    if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
+    constexpr int NP = DV / 8 / KW;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-    }
-    if constexpr (KW > 1) {
-        // the warps along the keys are joined in order by the first of them
-        float *buf = reinterpret_cast<float *>(ring.scratch());
-        __syncthreads();  // the last tile's readers are done with the stage
-        if ((lane & 3) == 0) {
-            ml[warp][quad] = make_float2(mx[0], sum[0]);
-            ml[warp][quad + 8] = make_float2(mx[1], sum[1]);
-        }
-        if (kg > 0) {
-            float *to = buf + ((kg - 1) * RW + rg) * (16 * DV) + lane;
+        if (!live[i] || !ok) continue;
+        const int64_t row = static_cast<int64_t>(t0 + node[i]) * p.Hq + hq[i];
+        const bool whole = nsplit == 1, first_lane = kg == 0 && (lane & 3) == 0;
+        if (whole) {
+            const float inv = 1.f / sum[i];
+            uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + row * DV + two);
 #pragma unroll
-            for (int j = 0; j < DV / 8; ++j)
+            for (int part = 0; part < KW; ++part)
+                if (part == kg) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) to[(j * 4 + e) * 32] = o[j][e];
-        }
-        __syncthreads();
-        if (kg == 0) {
-            float f[KW][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float m = mx[i];
-#pragma unroll
-                for (int g = 1; g < KW; ++g) m = fmaxf(m, ml[g * RW + rg][quad + 8 * i].x);
-                const float base = m == -INFINITY ? 0.f : m;
-                float l = 0.f;
-#pragma unroll
-                for (int g = 0; g < KW; ++g) {
-                    const float2 x = ml[g * RW + rg][quad + 8 * i];
-                    f[g][i] = ex2(x.x - base);
-                    l += f[g][i] * x.y;
+                    for (int j = part * NP; j < (part + 1) * NP; ++j) to[j * 4] = ptx::pack_bf16x2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
                 }
-                mx[i] = m;
-                sum[i] = l;
-            }
+            if (p.lse && first_lane) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
+        } else {
+            const int64_t at = row * p.max_splits + split;
+            float2 *to = reinterpret_cast<float2 *>(p.part_o + at * DV + two);
 #pragma unroll
-            for (int j = 0; j < DV / 8; ++j)
+            for (int part = 0; part < KW; ++part)
+                if (part == kg) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = f[0][e >> 1] * o[j][e];
-#pragma unroll
-                    for (int g = 1; g < KW; ++g) x += f[g][e >> 1] * buf[((g - 1) * RW + rg) * (16 * DV) + lane + (j * 4 + e) * 32];
-                    o[j][e] = x;
+                    for (int j = part * NP; j < (part + 1) * NP; ++j) to[j * 4] = make_float2(o[j][2 * i], o[j][2 * i + 1]);
                 }
-        }
-    }
-    if (kg == 0) {
-        const bool ok = may_write(p, n, flag, ring.bad_seen);
-        if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!live[i] || !ok) continue;
-            const int64_t row = static_cast<int64_t>(t0 + node[i]) * p.Hq + hq[i];
-            if (nsplit == 1) {
-                const float inv = 1.f / sum[i];
-                uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + row * DV + two);
-#pragma unroll
-                for (int j = 0; j < DV / 8; ++j) to[j * 4] = ptx::pack_bf16x2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
-                if (p.lse && (lane & 3) == 0) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
-            } else {
-                const int64_t at = row * p.max_splits + split;
-                float2 *to = reinterpret_cast<float2 *>(p.part_o + at * DV + two);
-#pragma unroll
-                for (int j = 0; j < DV / 8; ++j) to[j * 4] = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-                if ((lane & 3) == 0) p.part_ml[at] = make_float2(mx[i], sum[i]);
-            }
+            if (first_lane) p.part_ml[at] = make_float2(mx[i], sum[i]);
         }
     }
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_bf16_kernel(const AttnParams p) {
-    using R = Ring<__nv_bfloat16, DK, DV>;
+// ---------------------------------------------------------------------------------------------------------------
+// fp32: the same walk with m16n8k8 products in three tf32 terms
+// ---------------------------------------------------------------------------------------------------------------
+// x = hi + lo + at most 2^-22 |x|, both with the 11 significant bits of tf32; a product is hi hi + hi lo + lo hi, which
+// leaves about the rounding of an fp32 sum of this length, at a third of the tensor rate (and at that rate
+// this path is bound: fused multiply-adds took several times as long).  An infinity or NaN is all in hi, and 0 in `fin`, the hi of the two
+// cross terms, so that they add nothing to what it makes of the first one.
+struct Split {
+    uint32_t hi, fin, lo;
+};
+__device__ __forceinline__ Split split(float x) {
+    const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
+    const bool ok = (hi & 0x7f800000u) != 0x7f800000u;
+    return {hi, ok ? hi : 0u, ok ? __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u : 0u};
+}
+__device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The order in which an instruction's k index runs over channels or keys is free as long as both operands agree: a lane takes
+// eight consecutive channels of every 32 (two 16-byte reads without bank conflicts), and the weights' accumulator fragment
+// is the next product's operand as it is.
+template <int DK, int DV, int RW>
+__device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV> &ring, Walk &cw, float2 (*ml)[16],
+                                         float (&qf)[DK / 32][2][8], bool same_rows) {
+    using R = Ring<float, DK, DV>;
+    constexpr int KW = R::kThreads / 32 / RW, NT = R::kKeys / 8 / KW;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rg = warp % RW, kg = warp / RW, key0 = kg * (R::kKeys / KW);
+    const int quad = lane >> 2, j4 = lane & 3;
+    const int n = cw.n, t0 = cw.t0, split_no = cw.split, nsplit = cw.nsplit, rows = cw.nodes * p.G;
+    const uint32_t flag = __ldcg(p.bad + n);
+    const float c = p.scale * kLog2e;
+    int node[2], hq[2];
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = cw.tile * kTileRows + rg * 16 + quad + 8 * i;
+        live[i] = r < rows;
+        node[i] = live[i] ? r / p.G : 0;
+        hq[i] = cw.head * p.G + (live[i] ? r - node[i] * p.G : 0);
+    }
+    if (!same_rows)  // channels 32 g + 8 j4 + 0..7 of the two rows
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float *src = static_cast<const float *>(p.q) + (t0 + node[i]) * p.qs + static_cast<int64_t>(hq[i]) * DK + 8 * j4;
+#pragma unroll
+        for (int g = 0; g < DK / 32; ++g)
+#pragma unroll
+            for (int x = 0; x < 8; x += 4)
+                *reinterpret_cast<float4 *>(&qf[g][i][x]) = live[i] ? *reinterpret_cast<const float4 *>(src + 32 * g + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float o[DV / 8][4];  // fragment 4 g + q: columns 32 g + 8 j4 + q and + 4 of the two rows
+#pragma unroll
+    for (int j = 0; j < DV / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+
+    while (!cw.unit_done()) {
+        const bool drafted = cw.key >= cw.key_end;
+        const int first = drafted ? cw.node : 0;
+        const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;
+        if (drafted) cw.node += R::kKeys; else cw.key += R::kKeys;
+        const TileRow ahead = ring.begin_tile(p);
+        const char *ks = ring.stage(), *vs = ks + R::kBytesK;
+        // hi hi, and the cross terms apart where one column of keys alone would leave the products waiting for one another
+        float s[NT][4], x[4];
+        constexpr bool kApart = NT == 1;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = x[e] = 0.f;
+#pragma unroll
+        for (int g = 0; g < DK / 32; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float kf[NT][4];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int row = key0 + j * 8 + quad, u = 8 * g + 2 * j4 + h;
+                    *reinterpret_cast<float4 *>(kf[j]) = *reinterpret_cast<const float4 *>(ks + row * (R::kUnitsK * 16) + ((u ^ (row & 7)) << 4));
+                }
+#pragma unroll
+                for (int y = 0; y < 4; y += 2) {
+                    const Split a0 = split(qf[g][0][4 * h + y]), a1 = split(qf[g][1][4 * h + y]);
+                    const Split a2 = split(qf[g][0][4 * h + y + 1]), a3 = split(qf[g][1][4 * h + y + 1]);
+                    const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, af[4] = {a0.fin, a1.fin, a2.fin, a3.fin};
+                    const uint32_t al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const Split b0 = split(kf[j][y]), b1 = split(kf[j][y + 1]);
+                        mma1688(s[j], ah, b0.hi, b1.hi);
+                        mma1688(kApart ? x : s[j], af, b0.lo, b1.lo);
+                        mma1688(kApart ? x : s[j], al, b0.fin, b1.fin);
+                    }
+                }
+            }
+        uint64_t sees[2] = {~0ull, ~0ull};
+        if (drafted) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sees[i] = __ldg(p.sees + t0 + node[i]) >> first;
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = key0 + j * 8 + 2 * j4 + (e & 1);
+                float t = (kApart ? s[j][e] + x[e] : s[j][e]) * c;
+                if (key >= count || !((sees[e >> 1] >> key) & 1)) t = -INFINITY;
+                s[j][e] = t;
+                top[e >> 1] = fmaxf(top[e >> 1], t);
+            }
+        float old[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+            const float now = fmaxf(mx[i], top[i]);
+            const float base = now == -INFINITY ? 0.f : now;
+            old[i] = exp2f(mx[i] - base);
+            mx[i] = now;
+            top[i] = base;
+            sum[i] *= old[i];
+        }
+        if (__any_sync(0xffffffffu, old[0] != 1.f || old[1] != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < DV / 8; ++j) {
+                o[j][0] *= old[0];
+                o[j][1] *= old[0];
+                o[j][2] *= old[1];
+                o[j][3] *= old[1];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+            // weights of keys 8 k + 2 j4 (k index j4) and + 1 (j4 + 4)
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[i] = exp2f(s[k][i] - top[i >> 1]);
+                sum[i >> 1] += e[i];
+            }
+            const Split a0 = split(e[0]), a1 = split(e[2]), a2 = split(e[1]), a3 = split(e[3]);
+            const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, af[4] = {a0.fin, a1.fin, a2.fin, a3.fin};
+            const uint32_t al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
+            const int row = key0 + 8 * k + 2 * j4;
+#pragma unroll
+            for (int g = 0; g < DV / 32; ++g) {
+                float v0[4], v1[4];  // columns 32 g + 4 quad + 0..3 of the two keys
+                const int u = 8 * g + quad;
+                *reinterpret_cast<float4 *>(v0) = *reinterpret_cast<const float4 *>(vs + row * (R::kUnitsV * 16) + ((u ^ (row & 7)) << 4));
+                *reinterpret_cast<float4 *>(v1) = *reinterpret_cast<const float4 *>(vs + (row + 1) * (R::kUnitsV * 16) + ((u ^ ((row + 1) & 7)) << 4));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const Split b0 = split(v0[q]), b1 = split(v1[q]);
+                    mma1688(o[4 * g + q], ah, b0.hi, b1.hi);
+                    mma1688(o[4 * g + q], af, b0.lo, b1.lo);
+                    mma1688(o[4 * g + q], al, b0.fin, b1.fin);
+                }
+            }
+        }
+        ring.end_tile(ahead);
+    }
+    join_warps<R::kThreads / 32, RW, DV>(ring.scratch(), ml, o, mx, sum);
+    const bool ok = may_write(p, n, flag, ring.bad_seen);
+    if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
+    constexpr int NP = DV / 8 / KW;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (!live[i] || !ok) continue;
+        const int64_t row = static_cast<int64_t>(t0 + node[i]) * p.Hq + hq[i];
+        const bool whole = nsplit == 1;
+        const int64_t at = row * p.max_splits + split_no;
+        const float f = whole ? 1.f / sum[i] : 1.f;
+        float *to = (whole ? static_cast<float *>(p.o) + row * DV : p.part_o + at * DV) + 8 * j4;
+#pragma unroll
+        for (int part = 0; part < KW; ++part)
+            if (part == kg) {
+#pragma unroll
+                for (int j = part * NP; j < (part + 1) * NP; j += NP > 1 ? 2 : 1)  // fragments 4 g + q, q + 1
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float *at_j = to + 32 * (j / 4) + 4 * h + j % 4;
+                        if constexpr (NP > 1) *reinterpret_cast<float2 *>(at_j) = make_float2(o[j][2 * i + h] * f, o[j + 1][2 * i + h] * f);
+                        else *at_j = o[j][2 * i + h] * f;
+                    }
+            }
+        if (kg == 0 && j4 == 0) {
+            if (!whole) p.part_ml[at] = make_float2(mx[i], sum[i]);
+            else if (p.lse) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
+        }
+    }
+}
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, 2) attn_kernel(const AttnParams p) {
+    using R = Ring<T, DK, DV>;
     extern __shared__ __align__(128) char smem[];
     __shared__ TileRow rows[2][R::kKeys];
-    __shared__ float2 ml[4][16];
+    __shared__ float2 ml[R::kThreads / 32][16];
     __shared__ int bad_seen;
     grid_wait();
     grid_go();
@@ -599,150 +826,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_bf16_kernel(const AttnPa
     Walk cw;
     cw.start(p, first, last);
     ring.start(p, first, last);
+    std::conditional_t<sizeof(T) == 2, uint32_t[DK / 16][4], float[DK / 32][2][8]> qf;
+    bool same = false;
     while (cw.unit < cw.end) {
         const int left = cw.nodes * p.G - cw.tile * kTileRows;
-        if (left <= 16) unit_bf16<DK, DV, 1>(p, ring, cw, ml);
-        else if (left <= 32) unit_bf16<DK, DV, 2>(p, ring, cw, ml);
-        else unit_bf16<DK, DV, 4>(p, ring, cw, ml);
-        cw.next_unit(p);
-    }
-}
-
-// ---------------------------------------------------------------------------------------------------------------
-// fp32: fused multiply-adds; warp w has rows w, w + 4, .. of the tile, a lane one key of the scores and DV / 32 columns
-// ---------------------------------------------------------------------------------------------------------------
-constexpr int kRowsPerWarp = kTileRows / 4;
-
-template <int DK, int DV>
-__global__ void __launch_bounds__(kAttnThreads) attn_f32_kernel(const AttnParams p) {
-    using R = Ring<float, DK, DV>;
-    constexpr int VL = DV / 32;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ TileRow rows[2][R::kKeys];
-    __shared__ int bad_seen;
-    float *qs = reinterpret_cast<float *>(smem + R::kStages * R::kStage);  // [kTileRows][DK]
-    float *ps = qs + kTileRows * DK;                                       // [kTileRows][32]
-    grid_wait();
-    grid_go();
-    const int64_t units = __ldg(&p.info[p.N].unit0);
-    const int begin = static_cast<int>(units * blockIdx.x / gridDim.x);
-    const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
-    if (begin >= end) return;
-    if (threadIdx.x == 0) bad_seen = 0;
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    R ring;
-    ring.smem = smem;
-    ring.rows = rows;
-    ring.bad_seen = &bad_seen;
-    Walk cw;
-    cw.start(p, begin, end);
-    ring.start(p, begin, end);
-    const float c = p.scale * kLog2e;
-    while (cw.unit < cw.end) {
-        const int n = cw.n, t0 = cw.t0, row0 = cw.tile * kTileRows, all = cw.nodes * p.G, split = cw.split;
-        const int here = all - row0 < kTileRows ? all - row0 : kTileRows;
-        const uint32_t flag = __ldcg(p.bad + n);
-        // a warp's own rows of q (the other warps do not read them)
-        for (int r = warp; r < here; r += 4) {
-            const int nd = (row0 + r) / p.G, h = cw.head * p.G + (row0 + r) - nd * p.G;
-            const float *src = static_cast<const float *>(p.q) + (t0 + nd) * p.qs + static_cast<int64_t>(h) * DK;
-            for (int d = lane; d < DK / 4; d += 32)
-                reinterpret_cast<float4 *>(qs + r * DK)[d] = reinterpret_cast<const float4 *>(src)[d];
+        if constexpr (sizeof(T) == 2) {
+            if (left <= 16) unit_bf16<DK, DV, 1>(p, ring, cw, ml, qf, same);
+            else if (left <= 32) unit_bf16<DK, DV, 2>(p, ring, cw, ml, qf, same);
+            else unit_bf16<DK, DV, 4>(p, ring, cw, ml, qf, same);
+        } else {
+            if (left <= 16) unit_f32<DK, DV, 1>(p, ring, cw, ml, qf, same);
+            else if (left <= 32) unit_f32<DK, DV, 2>(p, ring, cw, ml, qf, same);
+            else unit_f32<DK, DV, 4>(p, ring, cw, ml, qf, same);
         }
-        __syncwarp();
-        float o[kRowsPerWarp][VL], mx[kRowsPerWarp], sum[kRowsPerWarp];
-#pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-            mx[i] = -INFINITY;
-            sum[i] = 0.f;
-#pragma unroll
-            for (int x = 0; x < VL; ++x) o[i][x] = 0.f;
-        }
-        while (!cw.unit_done()) {
-            const bool drafted = cw.key >= cw.key_end;
-            const int first = drafted ? cw.node : 0;
-            const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;
-            if (drafted) cw.node += R::kKeys; else cw.key += R::kKeys;
-            const TileRow ahead = ring.begin_tile(p);
-            const char *ks = ring.stage(), *vs = ks + R::kBytesK;
-            float s[kRowsPerWarp];
-#pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i) s[i] = 0.f;
-#pragma unroll 2
-            for (int d = 0; d < DK / 4; ++d) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(ks + lane * (R::kUnitsK * 16) + ((d ^ (lane & 7)) << 4));
-#pragma unroll
-                for (int i = 0; i < kRowsPerWarp; ++i)
-                    if (warp + 4 * i < here) {
-                        const float4 q4 = reinterpret_cast<const float4 *>(qs + (warp + 4 * i) * DK)[d];
-                        s[i] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[i]))));
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i)
-                if (warp + 4 * i < here) {
-                    const int r = warp + 4 * i;
-                    float t = s[i] * c;
-                    bool seen = lane < count;
-                    if (drafted) seen = seen && ((__ldg(p.sees + t0 + (row0 + r) / p.G) >> (first + lane)) & 1);
-                    if (!seen) t = -INFINITY;
-                    float top = t;
-#pragma unroll
-                    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    const float now = fmaxf(mx[i], top), base = now == -INFINITY ? 0.f : now;
-                    const float old = exp2f(mx[i] - base), e = exp2f(t - base);
-                    mx[i] = now;
-                    float tot = e;
-#pragma unroll
-                    for (int x = 16; x > 0; x >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, x);
-                    sum[i] = sum[i] * old + tot;
-#pragma unroll
-                    for (int x = 0; x < VL; ++x) o[i][x] *= old;
-                    ps[r * 32 + lane] = e;
-                }
-            __syncwarp();
-#pragma unroll 1
-            for (int j = 0; j < 32; j += 4) {
-                float v[4][VL];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int key = j + y, u = lane * VL / 4;
-                    const char *at = vs + key * (R::kUnitsV * 16) + ((u ^ (key & 7)) << 4) + (lane * VL % 4) * 4;
-#pragma unroll
-                    for (int x = 0; x < VL; x += 2) *reinterpret_cast<float2 *>(&v[y][x]) = *reinterpret_cast<const float2 *>(at + 4 * x);
-                }
-#pragma unroll
-                for (int i = 0; i < kRowsPerWarp; ++i)
-                    if (warp + 4 * i < here) {
-                        const float4 e = *reinterpret_cast<const float4 *>(ps + (warp + 4 * i) * 32 + j);
-#pragma unroll
-                        for (int x = 0; x < VL; ++x)
-                            o[i][x] = fmaf(e.x, v[0][x], fmaf(e.y, v[1][x], fmaf(e.z, v[2][x], fmaf(e.w, v[3][x], o[i][x]))));
-                    }
-            }
-            __syncwarp();
-            ring.end_tile(ahead);
-        }
-        __syncthreads();  // bad_seen of this unit's look-ups
-        const bool ok = may_write(p, n, flag, ring.bad_seen);
-        if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
-#pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i)
-            if (ok && warp + 4 * i < here) {
-                const int r = row0 + warp + 4 * i, nd = r / p.G, h = cw.head * p.G + r - nd * p.G;
-                const int64_t row = static_cast<int64_t>(t0 + nd) * p.Hq + h;
-                const bool whole = cw.nsplit == 1;
-                const int64_t at = row * p.max_splits + split;
-                const float f = whole ? 1.f / sum[i] : 1.f;
-                float *to = (whole ? static_cast<float *>(p.o) + row * DV : p.part_o + at * DV) + lane * VL;
-#pragma unroll
-                for (int x = 0; x < VL; x += 2) *reinterpret_cast<float2 *>(to + x) = make_float2(o[i][x] * f, o[i][x + 1] * f);
-                if (lane == 0) {
-                    if (!whole) p.part_ml[at] = make_float2(mx[i], sum[i]);
-                    else if (p.lse) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
-                }
-            }
+        same = cw.split + 1 < cw.nsplit;
         cw.next_unit(p);
     }
 }
@@ -804,7 +901,7 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     AttnLayout l{};
     // a sequence of few rows has the most parts; G rows are the fewest
     l.max_tiles = tiles_of(max_nodes * (Hq / Hkv));
-    const int64_t by_len = (max_ctx + least_chunk(1) - 1) / least_chunk(1);
+    const int64_t by_len = (max_ctx + least_chunk(1, true) - 1) / least_chunk(1, true);
     const int64_t most = most_splits(Hkv, 1);
     l.max_splits = static_cast<int>(by_len < 1 ? 1 : by_len < most ? by_len : most);
     size_t off = KDA_WS_HEADER_BYTES;
@@ -839,19 +936,19 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
     const int64_t seq_ctas = (static_cast<int64_t>(p.N) + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
     plan_kernel<<<static_cast<unsigned>(1 + seq_ctas), kPlanThreads, 0, s>>>(p);
     const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * (p.tc ? 1 : max_tiles);
-    const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? 2 : 1);
-    const unsigned grid = static_cast<unsigned>(units < most ? units : most);
+    const int64_t most = static_cast<int64_t>(sms) * 2;
+    const dim3 grid(static_cast<unsigned>(units < most ? units : most));
     if (dtype == KDA_BF16) {
         using R = Ring<__nv_bfloat16, DK, DV>;
-        const int smem = R::kStages * R::kStage;
-        if (!smem_opt_in<attn_bf16_kernel<DK, DV>>(smem)) return KDA_ERR_CUDA;
-        if (launch_after(attn_bf16_kernel<DK, DV>, dim3(grid), kAttnThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
+        constexpr int smem = R::kStages * R::kStage;
+        if (!smem_opt_in<attn_kernel<__nv_bfloat16, DK, DV>>(smem)) return KDA_ERR_CUDA;
+        if (launch_after(attn_kernel<__nv_bfloat16, DK, DV>, grid, R::kThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
         if (p.tc && launch_attn_tc(p, DK, DV, sms, s) != cudaSuccess) return KDA_ERR_CUDA;
     } else {
         using R = Ring<float, DK, DV>;
-        const int smem = R::kStages * R::kStage + kTileRows * (DK + 32) * static_cast<int>(sizeof(float));
-        if (!smem_opt_in<attn_f32_kernel<DK, DV>>(smem)) return KDA_ERR_CUDA;
-        if (launch_after(attn_f32_kernel<DK, DV>, dim3(grid), kAttnThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
+        constexpr int smem = R::kStages * R::kStage;
+        if (!smem_opt_in<attn_kernel<float, DK, DV>>(smem)) return KDA_ERR_CUDA;
+        if (launch_after(attn_kernel<float, DK, DV>, grid, R::kThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (p.max_splits > 1) {
         const int64_t rows = p.T * p.Hq;
@@ -914,6 +1011,7 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     p.status = reinterpret_cast<uint32_t *>(ws);
     p.info = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info);
     p.info_tc = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info_tc);
+    p.wide = dtype == KDA_F32;
     p.tc = dtype == KDA_BF16 && max_nodes * p.G > kda::attn::kTileRows;
     p.bad = reinterpret_cast<uint32_t *>(ws + l.bad);
     p.seq_of = reinterpret_cast<int32_t *>(ws + l.seq_of);

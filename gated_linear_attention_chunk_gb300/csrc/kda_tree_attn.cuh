@@ -32,6 +32,7 @@ struct AttnParams {
     const int32_t *cu, *parent;
     int64_t T, qs, ks, vs;       // token strides in elements
     int N, Hq, Hkv, G, max_nodes, max_splits;
+    bool wide;                   // fp32
     int tc;                      // sequences of more than kTileRows rows go to the tcgen05 kernel
     float scale;
     uint32_t *status;
@@ -52,9 +53,12 @@ __host__ __device__ inline int most_splits(int Hkv, int tiles) {
     const int per = Hkv * tiles;
     return per >= kFillUnits ? 1 : (kFillUnits + per - 1) / per;
 }
-__host__ __device__ inline int least_chunk(int rows) { return rows <= 16 ? 256 : rows <= 64 ? 16 * rows : 1024; }
-__host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, int *nsplit, int *chunk) {
-    const int least = least_chunk(rows);
+__host__ __device__ inline int least_chunk(int rows, bool wide) {
+    if (wide) return rows <= 32 ? 128 : rows <= 64 ? 4 * rows : 256;
+    return rows <= 16 ? 384 : rows <= 64 ? 8 * rows : 1024;
+}
+__host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, bool wide, int *nsplit, int *chunk) {
+    const int least = least_chunk(rows, wide);
     int s = (ctx + least - 1) / least;
     const int most = most_splits(Hkv, tiles);
     s = s < 1 ? 1 : s > most ? most : s;

@@ -431,7 +431,7 @@ typedef struct kda_paged_kv {
  *   max_nodes  the largest tree of the batch (1..KDA_MAX_TREE_NODES); a larger one is
  *          reported as KDA_ERR_BAD_SEQLENS
  * dk, dv each 64 or 128.  Scores, softmax and sums are fp32; for bf16 the weights are
- * rounded to bf16 before they meet the values (fp32 inputs keep fp32 throughout).
+ * rounded to bf16 before they meet the values (fp32 inputs: products in three tf32 terms, about 22 bits).
  * Long contexts are cut into parts that run concurrently and are joined in a fixed
  * order; the cut goes by a sequence's own length and tree, so its bits do not depend
  * on the batch.  A sequence with a device error (BAD_SEQLENS, BAD_PAGE, BAD_TREE)
