@@ -9,7 +9,7 @@
 // product, with no error that grows beyond |p| 2^-54 turns.  Its signed top 32 bits then go
 // through sincospif.
 //
-// The bytes of q and k, read and written once, bound it.  A CTA takes kTokens tokens at a time: one
+// The bytes of q and k, read and written once, bound it.  A CTA takes up to kTokens tokens at a time: one
 // sine and cosine per (token, pair) into shared memory, used by every head of that token; a thread
 // keeps one 16-byte column of a head (half layout: the two 16-byte halves of its pairs) and
 // walks the (token, head) rows.
@@ -41,7 +41,8 @@ namespace {
 using namespace spec;
 
 constexpr int kRopeThreads = 256;
-constexpr int kTokens = 4;  // tokens whose sines and cosines a CTA holds at a time
+constexpr int kTokens = 4;  // at most so many tokens' sines and cosines are held at a time
+constexpr int kUnroll = 2;  // rows in flight per thread
 
 struct RopeParams {
     const void *q, *k;
@@ -50,6 +51,7 @@ struct RopeParams {
     const double *inv_freq;
     int64_t T, qs, ks, qos, kos;  // token strides in elements
     int Hq, Hk, d, rot;
+    int tokens;      // tokens of a CTA at a time
     int cols;        // columns of a head: kVec-wide rotated ones (pairs of them in the half layout), then copied ones
     int rot_cols;
     int lanes;       // columns taken side by side: min(cols, threads)
@@ -57,84 +59,121 @@ struct RopeParams {
     float mscale, sign;
 };
 
-// kVector: a column is 16 bytes; otherwise a single pair (rotated) or channel (copied).
+// What a thread holds of one row: kVector: a 16-byte column, or in the half layout the two columns of its pairs;
+// otherwise a single pair (rotated) or channel (copied).
+template <typename T, bool kInterleaved, bool kVector>
+struct Piece {
+    static constexpr int V = kVector ? Elem<T>::kVec : 1;
+    uint4 a, b;  // kVector
+    T x, y;      // not kVector
+
+    __device__ __forceinline__ void load(const RopeParams &p, const T *row, int col) {
+        const int half = p.rot / 2;
+        if (col >= p.rot_cols) {
+            const int i = p.rot + (col - p.rot_cols) * V;
+            if constexpr (kVector) a = *reinterpret_cast<const uint4 *>(row + i);
+            else x = row[i];
+        } else if constexpr (kVector) {
+            a = *reinterpret_cast<const uint4 *>(row + col * V);
+            if constexpr (!kInterleaved) b = *reinterpret_cast<const uint4 *>(row + half + col * V);
+        } else {
+            x = row[kInterleaved ? 2 * col : col];
+            y = row[kInterleaved ? 2 * col + 1 : col + half];
+        }
+    }
+    // c, s: the token's cosines and sines
+    __device__ __forceinline__ void store(const RopeParams &p, T *row, int col, const float *c, const float *s) const {
+        const int half = p.rot / 2;
+        if (col >= p.rot_cols) {
+            const int i = p.rot + (col - p.rot_cols) * V;
+            if constexpr (kVector) *reinterpret_cast<uint4 *>(row + i) = a;
+            else row[i] = x;
+        } else if constexpr (!kVector) {
+            const float u = Elem<T>::to_f(x), v = Elem<T>::to_f(y);
+            row[kInterleaved ? 2 * col : col] = Elem<T>::from_f(u * c[col] - v * s[col]);
+            row[kInterleaved ? 2 * col + 1 : col + half] = Elem<T>::from_f(u * s[col] + v * c[col]);
+        } else if constexpr (kInterleaved) {
+            float f[V], g[V];
+            unpack16(a, f);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float cc = c[col * (V / 2) + i], ss = s[col * (V / 2) + i];
+                g[2 * i] = f[2 * i] * cc - f[2 * i + 1] * ss;
+                g[2 * i + 1] = f[2 * i] * ss + f[2 * i + 1] * cc;
+            }
+            *reinterpret_cast<uint4 *>(row + col * V) = pack16(g);
+        } else {
+            float u[V], v[V], yu[V], yv[V];
+            unpack16(a, u);
+            unpack16(b, v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float cc = c[col * V + i], ss = s[col * V + i];
+                yu[i] = u[i] * cc - v[i] * ss;
+                yv[i] = u[i] * ss + v[i] * cc;
+            }
+            *reinterpret_cast<uint4 *>(row + col * V) = pack16(yu);
+            *reinterpret_cast<uint4 *>(row + half + col * V) = pack16(yv);
+        }
+    }
+};
+
 template <typename T, bool kInterleaved, bool kVector>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
     extern __shared__ char smem[];
-    constexpr int V = kVector ? Elem<T>::kVec : 1;
     const int half = p.rot / 2;
     uint64_t *turn = reinterpret_cast<uint64_t *>(smem);                // [half]
     float *cs = reinterpret_cast<float *>(smem + ((static_cast<size_t>(half) * 8 + 15) & ~static_cast<size_t>(15)));
-    float *sn = cs + kTokens * half;                                    // [kTokens][half] each
+    float *sn = cs + p.tokens * half;                                   // [tokens][half] each
     for (int j = threadIdx.x; j < half; j += kRopeThreads) {
         const double f = p.inv_freq[j] * 0.15915494309189533577;        // 1 / (2 pi)
         turn[j] = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
     }
     const int H = p.Hq + p.Hk;
-    const int col0 = threadIdx.x % p.lanes;
-    const int row0 = threadIdx.x / p.lanes;
-    const bool live = row0 < p.rows;
+    const int col0 = threadIdx.x % p.lanes, row0 = threadIdx.x / p.lanes + static_cast<int>(blockIdx.y) * p.rows;
+    const int step = p.rows * gridDim.y;
+    const bool live = threadIdx.x / p.lanes < p.rows;
     __syncthreads();
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < p.T; t0 += static_cast<int64_t>(gridDim.x) * kTokens) {
-        const int nt = static_cast<int>(p.T - t0 < kTokens ? p.T - t0 : kTokens);
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens; t0 < p.T; t0 += static_cast<int64_t>(gridDim.x) * p.tokens) {
+        const int nt = static_cast<int>(p.T - t0 < p.tokens ? p.T - t0 : p.tokens);
+        const int rows = live ? nt * H : 0;
+        // the i-th row from r on: its source, destination and token
+        auto src = [&](int r) -> const T * {
+            const int t = r / H, h = r - t * H;
+            return h < p.Hq ? static_cast<const T *>(p.q) + (t0 + t) * p.qs + static_cast<int64_t>(h) * p.d
+                            : static_cast<const T *>(p.k) + (t0 + t) * p.ks + static_cast<int64_t>(h - p.Hq) * p.d;
+        };
+        auto dst = [&](int r) -> T * {
+            const int t = r / H, h = r - t * H;
+            return h < p.Hq ? static_cast<T *>(p.q_out) + (t0 + t) * p.qos + static_cast<int64_t>(h) * p.d
+                            : static_cast<T *>(p.k_out) + (t0 + t) * p.kos + static_cast<int64_t>(h - p.Hq) * p.d;
+        };
+        Piece<T, kInterleaved, kVector> x[kUnroll];
+        auto load = [&](int r, int col) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (r + i * step < rows) x[i].load(p, src(r + i * step), col);
+        };
+        load(row0, col0);  // on its way while the sines are computed
         for (int e = threadIdx.x; e < nt * half; e += kRopeThreads) {
             const int t = e / half, j = e - t * half;
             const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + t])) * turn[j];
-            const float x = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578e-10f;  // half turns
+            const float h = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578e-10f;  // half turns
             float s, c;
-            sincospif(x, &s, &c);
+            sincospif(h, &s, &c);
             cs[e] = c * p.mscale;
             sn[e] = s * p.mscale * p.sign;
         }
         __syncthreads();
-        if (live) {
-            for (int r = row0 + static_cast<int>(blockIdx.y) * p.rows; r < nt * H; r += p.rows * gridDim.y) {
-                const int t = r / H, h = r - t * H;
-                const bool is_q = h < p.Hq;
-                const int64_t tok = t0 + t;
-                const T *x = is_q ? static_cast<const T *>(p.q) + tok * p.qs + static_cast<int64_t>(h) * p.d
-                                  : static_cast<const T *>(p.k) + tok * p.ks + static_cast<int64_t>(h - p.Hq) * p.d;
-                T *y = is_q ? static_cast<T *>(p.q_out) + tok * p.qos + static_cast<int64_t>(h) * p.d
-                            : static_cast<T *>(p.k_out) + tok * p.kos + static_cast<int64_t>(h - p.Hq) * p.d;
-                const float *c = cs + t * half, *s = sn + t * half;
-                for (int col = col0; col < p.cols; col += p.lanes) {
-                    if (col >= p.rot_cols) {
-                        const int i = p.rot + (col - p.rot_cols) * V;
-                        if constexpr (kVector)
-                            *reinterpret_cast<uint4 *>(y + i) = *reinterpret_cast<const uint4 *>(x + i);
-                        else
-                            y[i] = x[i];
-                    } else if constexpr (!kVector) {
-                        const int ia = kInterleaved ? 2 * col : col, ib = kInterleaved ? 2 * col + 1 : col + half;
-                        const float a = Elem<T>::to_f(x[ia]), b = Elem<T>::to_f(x[ib]);
-                        y[ia] = Elem<T>::from_f(a * c[col] - b * s[col]);
-                        y[ib] = Elem<T>::from_f(a * s[col] + b * c[col]);
-                    } else if constexpr (kInterleaved) {
-                        float f[V], g[V];
-                        unpack16(*reinterpret_cast<const uint4 *>(x + col * V), f);
-    #pragma unroll
-                        for (int i = 0; i < V / 2; ++i) {
-                            const float cc = c[col * (V / 2) + i], ss = s[col * (V / 2) + i];
-                            g[2 * i] = f[2 * i] * cc - f[2 * i + 1] * ss;
-                            g[2 * i + 1] = f[2 * i] * ss + f[2 * i + 1] * cc;
-                        }
-                        *reinterpret_cast<uint4 *>(y + col * V) = pack16(g);
-                    } else {
-                        float a[V], b[V], ya[V], yb[V];
-                        unpack16(*reinterpret_cast<const uint4 *>(x + col * V), a);
-                        unpack16(*reinterpret_cast<const uint4 *>(x + half + col * V), b);
-    #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float cc = c[col * V + i], ss = s[col * V + i];
-                            ya[i] = a[i] * cc - b[i] * ss;
-                            yb[i] = a[i] * ss + b[i] * cc;
-                        }
-                        *reinterpret_cast<uint4 *>(y + col * V) = pack16(ya);
-                        *reinterpret_cast<uint4 *>(y + half + col * V) = pack16(yb);
-                    }
+        for (int col = col0; col < p.cols; col += p.lanes)
+            for (int r = row0; r < rows; r += kUnroll * step) {
+                if (col != col0 || r != row0) load(r, col);
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) {
+                    const int at = r + i * step;
+                    if (at < rows) x[i].store(p, dst(at), col, cs + at / H * half, sn + at / H * half);
                 }
             }
-        }
         __syncthreads();
     }
 }
@@ -146,14 +185,16 @@ kda_status launch_rope(RopeParams p, bool interleaved, bool vector, cudaStream_t
     p.cols = p.rot_cols + (p.d - p.rot) / V;
     p.lanes = p.cols < kRopeThreads ? p.cols : kRopeThreads;
     p.rows = kRopeThreads / p.lanes;
-    const size_t smem = ((static_cast<size_t>(p.rot / 2) * 8 + 15) & ~static_cast<size_t>(15)) +
-                        static_cast<size_t>(kTokens) * p.rot * sizeof(float);
-    const int64_t groups = (p.T + kTokens - 1) / kTokens;
     const int64_t most = static_cast<int64_t>(spec::sm_count()) * 8;
     if (most <= 0) return KDA_ERR_CUDA;
-    const int64_t gx = groups < most ? groups : most;
-    // few tokens: their heads are spread over several CTAs
-    const int64_t steps = (static_cast<int64_t>(kTokens) * (p.Hq + p.Hk) + p.rows - 1) / p.rows;
+    // few tokens: fewer per CTA, and their heads spread over several CTAs
+    const int64_t share = p.T / most;
+    p.tokens = static_cast<int>(share < 1 ? 1 : share > kTokens ? kTokens : share);
+    const size_t smem = ((static_cast<size_t>(p.rot / 2) * 8 + 15) & ~static_cast<size_t>(15)) +
+                        static_cast<size_t>(p.tokens) * p.rot * sizeof(float);
+    const int64_t groups = (p.T + p.tokens - 1) / p.tokens;
+    const int64_t gx = groups < 0x7fffffffLL ? groups : 0x7fffffffLL;
+    const int64_t steps = (static_cast<int64_t>(p.tokens) * (p.Hq + p.Hk) + p.rows - 1) / p.rows;
     int64_t gy = most / gx < steps ? most / gx : steps;
     gy = gy < 1 ? 1 : gy > 64 ? 64 : gy;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
@@ -190,7 +231,7 @@ kda_status rope(const void *q, const void *k, kda_dtype dtype, const int32_t *po
     bool vector = aligned_to(q, 16) && aligned_to(q_out, 16) && qs % V == 0 && qos % V == 0 && rot % V == 0 &&
                   (interleaved || (rot / 2) % V == 0);
     if (Hk > 0) vector = vector && aligned_to(k, 16) && aligned_to(k_out, 16) && ks % V == 0 && kos % V == 0;
-    RopeParams p{q, k, q_out, k_out, positions, inv_freq, T, qs, ks, qos, kos, Hq, Hk, d, rot, 0, 0, 0, 0, mscale, sign};
+    RopeParams p{q, k, q_out, k_out, positions, inv_freq, T, qs, ks, qos, kos, Hq, Hk, d, rot, 0, 0, 0, 0, 0, mscale, sign};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == KDA_BF16 ? launch_rope<__nv_bfloat16>(p, interleaved != 0, vector, s)
                              : launch_rope<float>(p, interleaved != 0, vector, s);
