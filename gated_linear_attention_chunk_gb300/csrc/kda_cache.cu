@@ -1,9 +1,9 @@
 // Append of new rows to a paged cache: the keys and values of a prompt, or of the accepted nodes of a
 // drafted tree (through their row indices), to the rows after each sequence's context.
 //
-// A pure copy, bounded by its bytes (each row read and written once).  One warp per token, found
-// among the sequences by a 32-way search; its lanes take 16 bytes of the token's heads at a time, all
-// loads of a batch before the first store.
+// A pure copy, bounded by its bytes (each row read and written once).  A warp has a few consecutive tokens; their
+// sequence is found by a 32-way search, their rows and pages looked up by a lane each, and
+// then all lanes copy 16 bytes of a token's heads at a time, all loads of a step before the first store.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -11,6 +11,24 @@
 #include "kda_spec.cuh"
 
 namespace kda {
+namespace {
+
+__global__ void clear_kernel(uint32_t *words) {
+    spec::grid_go();
+    if (threadIdx.x < 2) words[threadIdx.x] = 0;
+}
+
+}  // namespace
+
+namespace spec {
+
+bool clear_words(void *workspace, cudaStream_t s) {
+    clear_kernel<<<1, 32, 0, s>>>(static_cast<uint32_t *>(workspace));
+    return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace spec
+
 namespace {
 
 using namespace spec;
@@ -26,9 +44,15 @@ struct AppendParams {
     int32_t *new_len;
     int64_t A_total, T_src, ks, vs;  // token strides in 16-byte units
     int N, Hkv;
+    int per;                         // tokens of a warp (at most 32)
     int kshift, vshift;              // log2 of a head's 16-byte units
     uint32_t *status;
 };
+
+__device__ __forceinline__ void raise(uint32_t *status, uint32_t err) {
+    grid_wait();  // the status word has been cleared
+    atomicOr(status, err);
+}
 
 // A sequence's place in the packed rows and its context, checked.
 struct AppendSeq {
@@ -43,54 +67,80 @@ __device__ __forceinline__ AppendSeq append_seq(const AppendParams &p, int n) {
     return s;
 }
 
-// `units` 16-byte units from a packed row to the heads of one cache row.
-__device__ __forceinline__ void copy_row(const char *src, char *dst, int64_t head_bytes, int units, int shift) {
-    const int lane = threadIdx.x & 31;
-    for (int u0 = lane; u0 < units; u0 += 32 * kAppendUnroll) {
-        uint4 x[kAppendUnroll];
+// The heads of a token's key and value rows, 16 bytes per lane and step, all loads of a step before its stores.
+struct CopySide {
+    const char *src;
+    char *dst;
+    int64_t head_bytes;
+    int units, shift;
+    __device__ __forceinline__ void load(uint4 (&x)[kAppendUnroll], int u0) const {
 #pragma unroll
         for (int i = 0; i < kAppendUnroll; ++i)
             if (u0 + 32 * i < units) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + u0 + 32 * i);
+    }
+    __device__ __forceinline__ void store(const uint4 (&x)[kAppendUnroll], int u0) const {
 #pragma unroll
         for (int i = 0; i < kAppendUnroll; ++i) {
             const int u = u0 + 32 * i;
-            if (u < units)
-                *reinterpret_cast<uint4 *>(dst + (u >> shift) * head_bytes + ((u & ((1 << shift) - 1)) << 4)) = x[i];
+            if (u < units) *reinterpret_cast<uint4 *>(dst + (u >> shift) * head_bytes + ((u & ((1 << shift) - 1)) << 4)) = x[i];
         }
     }
-}
+};
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int64_t es) {
     // new lengths, one thread per sequence
     const int64_t gid = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
     for (int64_t n = gid; n < p.N; n += static_cast<int64_t>(gridDim.x) * kAppendThreads) {
         const AppendSeq s = append_seq(p, static_cast<int>(n));
-        if (s.err) atomicOr(p.status, s.err);
+        if (s.err) raise(p.status, s.err);
         if (p.new_len) p.new_len[n] = static_cast<int32_t>(s.err ? s.ctx : s.ctx + s.last - s.first);
     }
     const int lane = threadIdx.x & 31;
     const int64_t most = p.cu[p.N];
     const int64_t total = most < p.A_total ? most : p.A_total;
-    for (int64_t j = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5); j < total;
-         j += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
-        const int n = warp_find([&](int i) { return p.cu[i]; }, p.N, j);
-        const AppendSeq s = append_seq(p, n);
-        if (s.err || j < s.first || j >= s.last) {
-            if (!s.err && lane == 0) atomicOr(p.status, DEV_ERR_SEQLENS);
-            continue;
+    for (int64_t j0 = (static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5)) * p.per; j0 < total;
+         j0 += static_cast<int64_t>(gridDim.x) * kAppendWarps * p.per) {
+        // lane i looks up token j0 + i: one chain of dependent loads for all of the warp's tokens
+        const int n0 = warp_find([&](int i) { return p.cu[i]; }, p.N, j0);
+        const int64_t j = j0 + lane;
+        int64_t row = -1, place_k = 0, place_v = 0;
+        if (lane < p.per && j < total) {
+            int n = n0;
+            while (n + 1 < p.N && p.cu[n + 1] <= j) ++n;
+            const AppendSeq s = append_seq(p, n);
+            if (s.err || j < s.first || j >= s.last) {
+                if (!s.err) raise(p.status, DEV_ERR_SEQLENS);
+            } else {
+                const int64_t r = p.rows ? static_cast<int64_t>(p.rows[j]) : j, at = s.ctx + j - s.first;
+                const int64_t page = p.c.table[static_cast<int64_t>(n) * p.c.table_stride + at / p.c.page_size];
+                const int64_t slot = at % p.c.page_size;
+                const bool row_ok = r >= 0 && r < p.T_src, page_ok = page >= 0 && page < p.c.num_pages;
+                if (row_ok && page_ok) {
+                    row = r;
+                    place_k = (page * p.c.kp + slot * p.c.kr) * es;
+                    place_v = (page * p.c.vp + slot * p.c.vr) * es;
+                } else {
+                    raise(p.status, row_ok ? DEV_ERR_PAGE : DEV_ERR_SLOT);
+                }
+            }
         }
-        const int64_t row = p.rows ? static_cast<int64_t>(p.rows[j]) : j;
-        const int64_t at = s.ctx + j - s.first;
-        const int64_t page = p.c.table[static_cast<int64_t>(n) * p.c.table_stride + at / p.c.page_size];
-        const int64_t slot = at % p.c.page_size;
-        const bool row_ok = row >= 0 && row < p.T_src, page_ok = page >= 0 && page < p.c.num_pages;
-        if (!row_ok || !page_ok) {
-            if (lane == 0) atomicOr(p.status, row_ok ? DEV_ERR_PAGE : DEV_ERR_SLOT);
-            continue;
+        __syncwarp();
+        for (int i = 0; i < p.per; ++i) {
+            const int64_t r = __shfl_sync(0xffffffffu, row, i);
+            const int64_t pk = __shfl_sync(0xffffffffu, place_k, i), pv = __shfl_sync(0xffffffffu, place_v, i);
+            if (r < 0) continue;
+            const CopySide k{p.k + r * p.ks * 16, p.c.k + pk, p.c.kh * es, p.Hkv << p.kshift, p.kshift};
+            const CopySide v{p.v + r * p.vs * 16, p.c.v + pv, p.c.vh * es, p.Hkv << p.vshift, p.vshift};
+            for (int u0 = lane; u0 < k.units || u0 < v.units; u0 += 32 * kAppendUnroll) {
+                uint4 x[kAppendUnroll], y[kAppendUnroll];
+                k.load(x, u0);
+                v.load(y, u0);
+                k.store(x, u0);
+                v.store(y, u0);
+            }
         }
-        copy_row(p.k + row * p.ks * 16, p.c.k + (page * p.c.kp + slot * p.c.kr) * es, p.c.kh * es, p.Hkv << p.kshift, p.kshift);
-        copy_row(p.v + row * p.vs * 16, p.c.v + (page * p.c.vp + slot * p.c.vr) * es, p.c.vh * es, p.Hkv << p.vshift, p.vshift);
     }
+    grid_wait();
 }
 
 }  // namespace
@@ -122,17 +172,20 @@ kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const
         return KDA_ERR_INVALID_ARGUMENT;
     if (new_len && new_len == cache->ctx_len) return KDA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (!clear_words(workspace, s)) return KDA_ERR_CUDA;
     if (N == 0) return KDA_OK;
     auto shift = [&](int d) { int b = 0; for (int u = d / vec; u > 1; u >>= 1) ++b; return b; };
     kda::AppendParams p{static_cast<const char *>(k), static_cast<const char *>(v), c, cu, rows, new_len, A_total, T_src,
-                        k_stride / vec, v_stride / vec, N, Hkv, shift(dk), shift(dv), static_cast<uint32_t *>(workspace)};
-    const int64_t work = A_total > N ? A_total : N;
-    const int64_t want = (work + kda::kAppendWarps - 1) / kda::kAppendWarps;
+                        k_stride / vec, v_stride / vec, N, Hkv, 1, shift(dk), shift(dv), static_cast<uint32_t *>(workspace)};
     const int64_t most = static_cast<int64_t>(sm_count()) * 8;
     if (most <= 0) return KDA_ERR_CUDA;
-    kda::append_kernel<<<static_cast<unsigned>(want < most ? want : most), kda::kAppendThreads, 0, s>>>(p, es);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    // few tokens: a warp each; many: up to 4 per warp, whose look-ups then wait for memory together
+    const int64_t share = A_total / (most * 4);
+    p.per = static_cast<int>(share < 1 ? 1 : share > 4 ? 4 : share);
+    const int64_t work = A_total / p.per + 1 > N / 32 ? A_total / p.per + 1 : N / 32 + 1;
+    const int64_t want = (work + kda::kAppendWarps - 1) / kda::kAppendWarps;
+    const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+    return launch_after(kda::append_kernel, grid, kda::kAppendThreads, 0, s, p, static_cast<int64_t>(es)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -115,6 +115,10 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // Lets the next grid in the stream begin (it waits for this one's end all the same).
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Clears the status word and the word behind it.  A kernel launched after it with the programmatic attribute begins once
+// everything before the clearing has ended; it waits (grid_wait) before it touches these words, and before it ends.
+bool clear_words(void *workspace, cudaStream_t s);
+
 // A page pool as the kernels see it (strides in elements).
 struct Pages {
     char *k, *v;

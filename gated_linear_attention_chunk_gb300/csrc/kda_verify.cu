@@ -181,7 +181,7 @@ __device__ __forceinline__ Pair from_lane(Pair x, int lane) {
 // Where a running sum passes a point: of one weight per lane, in lane order, the first lane whose sum, `before`
 // included, is above `point` (`before` becomes the sum ahead of it); otherwise hit is false, the last lane with mass or -1
 // is returned, and `before` becomes the sum of all.
-__device__ __forceinline__ int pass_point(Pair weight, double &before, double point, bool &hit) {
+__device__ __noinline__ int pass_point(Pair weight, double &before, double point, bool &hit) {
     const Pair upto = warp_scan(weight);
     const double sum = before + value(upto);
     const uint32_t over = __ballot_sync(0xffffffffu, weight.hi > 0.f && sum > point);
@@ -324,7 +324,10 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
             sh.nremoved = 0;
             sh.accepted = 0;
             is_last = false;
-            if (rank == 0 && err) atomicOr(p.status, err);
+            if (rank == 0 && err) {
+                grid_wait();   // the status word has been cleared
+                atomicOr(p.status, err);
+            }
         }
         accepted = (err || m == 0) ? 0ull : 1ull;
     }
@@ -336,6 +339,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     const bool publisher = rank == 0 && threadIdx.x == 32;
     auto publish = [&] {
         p.accepted[n] = sh.accepted;
+        grid_wait();           // the counter has been cleared
         __threadfence();
         is_last = atomicAdd(p.status + 1, 1u) == static_cast<uint32_t>(p.N) - 1;
         __threadfence();
@@ -513,6 +517,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
         __syncthreads();
         if (is_last && !packed && warp > 0) pack();
     }
+    grid_wait();
     cg_wait();  // no CTA leaves while another may still read its sums
 }
 
@@ -522,12 +527,14 @@ kda_status launch_verify(const VerifyParams &p, int cluster, cudaStream_t s) {
     cfg.gridDim = dim3(static_cast<unsigned>(p.N) * cluster);
     cfg.blockDim = dim3(kVerThreads);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // may begin beside the clearing of the status
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, verify_kernel<T, kDraft>, p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -563,7 +570,7 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
                             static_cast<const void *>(rows), static_cast<const void *>(next_token)})
         if (!aligned_to(ptr, 4)) return KDA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, 2 * sizeof(uint32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (!clear_words(workspace, s)) return KDA_ERR_CUDA;
     if (N == 0) {
         if (cudaMemsetAsync(cu_accept, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
         if (T > 0 && cudaMemsetAsync(rows, 0xff, static_cast<size_t>(T) * sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
