@@ -918,10 +918,13 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     size_t tc = 0;
     const int64_t rows = max_nodes * static_cast<int64_t>(Hq / Hkv);
     if (rows > kTileRows) {
-        const int64_t far = (max_ctx + kTcChunk - 1) / kTcChunk, some = (max_ctx + 1023) / 1024;
-        int64_t s = some < most ? some : most;
-        s = s > far ? s : far;
-        tc = static_cast<size_t>(T * (Hq / Hkv) / kTcRows + N) * Hkv * (s < 1 ? 1 : s) * 2;
+        // (fewer row groups make the number of parts that fill the GPU larger: one group has the most)
+        int s = 1;
+        for (int g = 1; g <= tc_groups_of(tc_tiles_of(static_cast<int>(rows))); ++g) {
+            const int x = tc_splits_of(max_ctx, Hkv, g);
+            if (x > s) s = x;
+        }
+        tc = static_cast<size_t>(T * (Hq / Hkv) / kTcRows + N) * Hkv * s * 2;
     }
     l.tc_ml = take(tc * kTcRows * sizeof(float2));
     l.tc_o = take(tc * kTcRows * dv * sizeof(float));
@@ -967,7 +970,7 @@ extern "C" {
 
 size_t kda_tree_attn_workspace_size(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
     if (N < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !kda::spec::dim_ok(dv) || max_nodes < 1 ||
-        max_nodes > KDA_MAX_TREE_NODES || max_ctx < 0)
+        max_nodes > KDA_MAX_TREE_NODES || max_ctx < 0 || max_ctx > 0x7fffffffLL)
         return 0;
     return kda::layout_of(N, T, Hq, Hkv, dv, max_nodes, max_ctx).total;
 }

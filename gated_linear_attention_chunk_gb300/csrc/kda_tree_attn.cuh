@@ -70,16 +70,19 @@ __host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, 
 }
 __host__ __device__ inline int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
 
-// The same for the tcgen05 kernel, whose units are pairs of row tiles (or one): at most kTcChunk keys, so that the second
-// pair of a sequence finds the first one's keys in L2.
-constexpr int kTcChunk = 4096;
+// The same for the tcgen05 kernel, whose units are pairs of row tiles (or one): the number that fills the GPU, or a
+// multiple of it, so that the units of a batch of such sequences share out evenly (32 parts in the place of 19 for four
+// sequences of 131,072 keys and 264 rows on 4 KV heads: 531 us against 430).
+constexpr int kTcChunk = 16384;
 __host__ __device__ inline int tc_tiles_of(int rows) { return (rows + kTcRows - 1) / kTcRows; }
 __host__ __device__ inline int tc_groups_of(int tiles) { return (tiles + 1) / 2; }
+__host__ __device__ inline int tc_splits_of(int64_t ctx, int Hkv, int groups) {
+    const int64_t some = (ctx + 1023) / 1024, most = most_splits(Hkv, groups);
+    const int64_t s = some < most ? some : most * ((ctx + most * kTcChunk - 1) / (most * kTcChunk));
+    return static_cast<int>(s < 1 ? 1 : s);
+}
 __host__ __device__ inline void tc_split_of(int ctx, int Hkv, int tiles, int *nsplit, int *chunk) {
-    int s = (ctx + 1023) / 1024;
-    const int most = most_splits(Hkv, tc_groups_of(tiles)), far = (ctx + kTcChunk - 1) / kTcChunk;
-    s = s < 1 ? 1 : s > most ? most : s;
-    if (s < far) s = far;
+    const int s = tc_splits_of(ctx, Hkv, tc_groups_of(tiles));
     int c = (ctx + s - 1) / s;
     c = (c + kTcKeys - 1) / kTcKeys * kTcKeys;
     if (c < kTcKeys) c = kTcKeys;
