@@ -334,9 +334,9 @@ struct Ring {
             cp16(dst + place<kUnits>(r0, i * kSide, u), base + u * 16 + x, x >= 0);
         }
     }
-    __device__ __forceinline__ void start(const AttnParams &p, int first, int last) {
+    __device__ __forceinline__ void start(const AttnParams &p, const Walk &from) {
         tile = 0;
-        w.start(p, first, last);
+        w = from;
 #pragma unroll
         for (int i = 0; i < kStages; ++i) {
             put(look(p), i & 1);
@@ -610,17 +610,31 @@ __device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat1
 // ---------------------------------------------------------------------------------------------------------------
 // fp32: the same walk with m16n8k8 products in three tf32 terms
 // ---------------------------------------------------------------------------------------------------------------
-// x = hi + lo + at most 2^-22 |x|, both with the 11 significant bits of tf32; a product is hi hi + hi lo + lo hi, which
+// x = hi + lo + at most 2^-23 |x|, both with the 11 significant bits of tf32; a product is hi hi + hi lo + lo hi, which
 // leaves about the rounding of an fp32 sum of this length, at a third of the tensor rate (and at that rate
-// this path is bound: fused multiply-adds took several times as long).  An infinity or NaN is all in hi, and 0 in `fin`, the hi of the two
-// cross terms, so that they add nothing to what it makes of the first one.
+// this path is bound: fused multiply-adds took several times as long).  hi is rounded to nearest, so that lo has either
+// sign and the lo lo left out does not add up (with a truncated hi the result was three times as far off); the largest
+// finite values round down.  An infinity or NaN is all in hi, and 0 in `fin`, the hi of the two cross terms, so that they
+// add nothing to what it makes of the first one.
 struct Split {
     uint32_t hi, fin, lo;
 };
+constexpr uint32_t kTf32 = 0xffffe000u;
+__device__ __forceinline__ Split split_any(float x) {
+    const uint32_t bits = __float_as_uint(x), size = bits & 0x7fffffffu;
+    const uint32_t near = (min(size + 0x1000u, 0x7f7fffffu) & kTf32) | (bits & 0x80000000u);
+    const bool ok = size < 0x7f800000u;
+    return {ok ? near : bits & kTf32, ok ? near : 0u, ok ? __float_as_uint(x - __uint_as_float(near)) & kTf32 : 0u};
+}
+// The same for values whose square is finite (as that of others is not, a sum of squares tells).
 __device__ __forceinline__ Split split(float x) {
-    const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
-    const bool ok = (hi & 0x7f800000u) != 0x7f800000u;
-    return {hi, ok ? hi : 0u, ok ? __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u : 0u};
+    const uint32_t hi = (__float_as_uint(x) + 0x1000u) & kTf32;
+    return {hi, hi, __float_as_uint(x - __uint_as_float(hi)) & kTf32};
+}
+template <bool kAny>
+__device__ __forceinline__ Split split_as(float x) {
+    if constexpr (kAny) return split_any(x);
+    else return split(x);
 }
 __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -662,6 +676,14 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
             for (int x = 0; x < 8; x += 4)
                 *reinterpret_cast<float4 *>(&qf[g][i][x]) = live[i] ? *reinterpret_cast<const float4 *>(src + 32 * g + x) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    float q_size = 0.f;  // sum of squares: finite unless a value is not, or far too large
+#pragma unroll
+    for (int g = 0; g < DK / 32; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) q_size = fmaf(qf[g][i][x], qf[g][i][x], q_size);
+    q_size = q_size < INFINITY ? 0.f : INFINITY;
     float o[DV / 8][4];  // fragment 4 g + q: columns 32 g + 8 j4 + q and + 4 of the two rows
 #pragma unroll
     for (int j = 0; j < DV / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -691,20 +713,33 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
                     const int row = key0 + j * 8 + quad, u = 8 * g + 2 * j4 + h;
                     *reinterpret_cast<float4 *>(kf[j]) = *reinterpret_cast<const float4 *>(ks + row * (R::kUnitsK * 16) + ((u ^ (row & 7)) << 4));
                 }
+                float size = q_size;
 #pragma unroll
-                for (int y = 0; y < 4; y += 2) {
-                    const Split a0 = split(qf[g][0][4 * h + y]), a1 = split(qf[g][1][4 * h + y]);
-                    const Split a2 = split(qf[g][0][4 * h + y + 1]), a3 = split(qf[g][1][4 * h + y + 1]);
-                    const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, af[4] = {a0.fin, a1.fin, a2.fin, a3.fin};
-                    const uint32_t al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const Split b0 = split(kf[j][y]), b1 = split(kf[j][y + 1]);
-                        mma1688(s[j], ah, b0.hi, b1.hi);
-                        mma1688(kApart ? x : s[j], af, b0.lo, b1.lo);
-                        mma1688(kApart ? x : s[j], al, b0.fin, b1.fin);
+                    for (int y = 0; y < 4; ++y) size = fmaf(kf[j][y], kf[j][y], size);
+                auto products = [&](auto any) {
+                    constexpr bool kAny = decltype(any)::value;
+#pragma unroll
+                    for (int y = 0; y < 4; y += 2) {
+                        // (split again for every tile: kept between them, the parts would not fit the registers)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) asm volatile("" : "+f"(qf[g][i][4 * h + y]), "+f"(qf[g][i][4 * h + y + 1]));
+                        const Split a0 = split_as<kAny>(qf[g][0][4 * h + y]), a1 = split_as<kAny>(qf[g][1][4 * h + y]);
+                        const Split a2 = split_as<kAny>(qf[g][0][4 * h + y + 1]), a3 = split_as<kAny>(qf[g][1][4 * h + y + 1]);
+                        const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, af[4] = {a0.fin, a1.fin, a2.fin, a3.fin};
+                        const uint32_t al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const Split b0 = split_as<kAny>(kf[j][y]), b1 = split_as<kAny>(kf[j][y + 1]);
+                            mma1688(s[j], ah, b0.hi, b1.hi);
+                            mma1688(kApart ? x : s[j], af, b0.lo, b1.lo);
+                            mma1688(kApart ? x : s[j], al, b0.fin, b1.fin);
+                        }
                     }
-                }
+                };
+                if (__any_sync(0xffffffffu, !(size < INFINITY))) products(std::true_type{});
+                else products(std::false_type{});
             }
         uint64_t sees[2] = {~0ull, ~0ull};
         if (drafted) {
@@ -752,9 +787,9 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
                 e[i] = exp2f(s[k][i] - top[i >> 1]);
                 sum[i >> 1] += e[i];
             }
+            // (weights are at most 1, or NaN, which their sum passes on to the whole row)
             const Split a0 = split(e[0]), a1 = split(e[2]), a2 = split(e[1]), a3 = split(e[3]);
-            const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, af[4] = {a0.fin, a1.fin, a2.fin, a3.fin};
-            const uint32_t al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
+            const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
             const int row = key0 + 8 * k + 2 * j4;
 #pragma unroll
             for (int g = 0; g < DV / 32; ++g) {
@@ -762,13 +797,21 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
                 const int u = 8 * g + quad;
                 *reinterpret_cast<float4 *>(v0) = *reinterpret_cast<const float4 *>(vs + row * (R::kUnitsV * 16) + ((u ^ (row & 7)) << 4));
                 *reinterpret_cast<float4 *>(v1) = *reinterpret_cast<const float4 *>(vs + (row + 1) * (R::kUnitsV * 16) + ((u ^ ((row + 1) & 7)) << 4));
+                float size = 0.f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const Split b0 = split(v0[q]), b1 = split(v1[q]);
-                    mma1688(o[4 * g + q], ah, b0.hi, b1.hi);
-                    mma1688(o[4 * g + q], af, b0.lo, b1.lo);
-                    mma1688(o[4 * g + q], al, b0.fin, b1.fin);
-                }
+                for (int q = 0; q < 4; ++q) size = fmaf(v0[q], v0[q], fmaf(v1[q], v1[q], size));
+                auto products = [&](auto any) {
+                    constexpr bool kAny = decltype(any)::value;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const Split b0 = split_as<kAny>(v0[q]), b1 = split_as<kAny>(v1[q]);
+                        mma1688(o[4 * g + q], ah, b0.hi, b1.hi);
+                        mma1688(o[4 * g + q], ah, b0.lo, b1.lo);
+                        mma1688(o[4 * g + q], al, b0.fin, b1.fin);
+                    }
+                };
+                if (__any_sync(0xffffffffu, !(size < INFINITY))) products(std::true_type{});
+                else products(std::false_type{});
             }
         }
         ring.end_tile(ahead);
@@ -825,7 +868,7 @@ __global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, 2) attn_kernel(cons
     ring.bad_seen = &bad_seen;
     Walk cw;
     cw.start(p, first, last);
-    ring.start(p, first, last);
+    ring.start(p, cw);
     std::conditional_t<sizeof(T) == 2, uint32_t[DK / 16][4], float[DK / 32][2][8]> qf;
     bool same = false;
     while (cw.unit < cw.end) {
