@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
                 if (err) atomicOr(&errors, err);
                 const int rows = s.nodes * p.G;
                 if (!err && rows > 0) {
-                    if (p.tc && rows > kTileRows) {
+                    if (p.tc && rows > kTcLeast) {
                         s.tiles = tc_tiles_of(rows);
                         tc_split_of(s.ctx, p.Hkv, s.tiles, &s.nsplit, &s.chunk);
                         units[1] = s.nsplit * s.tiles * p.Hkv;
@@ -244,7 +244,8 @@ template <typename T, int DK, int DV>
 struct Ring {
     static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
     static constexpr int kThreads = 128;
-    static constexpr int kStages = 3;
+    static constexpr int kStages = sizeof(T) == 2 ? 2 : 3;
+    static constexpr int kPerSm = sizeof(T) == 2 ? 3 : 2;  // CTAs (bf16 with three stages and two CTAs: 224 us for 204)
     static constexpr int kUnitsK = DK * static_cast<int>(sizeof(T)) / 16, kUnitsV = DV * static_cast<int>(sizeof(T)) / 16;
     static constexpr int kBytesK = kKeys * kUnitsK * 16, kBytesV = kKeys * kUnitsV * 16;
     static constexpr int kStage = kBytesK + kBytesV;
@@ -848,7 +849,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
 }
 
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, 2) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, Ring<T, DK, DV>::kPerSm) attn_kernel(const AttnParams p) {
     using R = Ring<T, DK, DV>;
     extern __shared__ __align__(128) char smem[];
     __shared__ TileRow rows[2][R::kKeys];
@@ -875,8 +876,7 @@ __global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, 2) attn_kernel(cons
         const int left = cw.nodes * p.G - cw.tile * kTileRows;
         if constexpr (sizeof(T) == 2) {
             if (left <= 16) unit_bf16<DK, DV, 1>(p, ring, cw, ml, qf, same);
-            else if (left <= 32) unit_bf16<DK, DV, 2>(p, ring, cw, ml, qf, same);
-            else unit_bf16<DK, DV, 4>(p, ring, cw, ml, qf, same);
+            else unit_bf16<DK, DV, 2>(p, ring, cw, ml, qf, same);  // (more rows: the tcgen05 kernel)
         } else {
             if (left <= 16) unit_f32<DK, DV, 1>(p, ring, cw, ml, qf, same);
             else if (left <= 32) unit_f32<DK, DV, 2>(p, ring, cw, ml, qf, same);
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
     const SeqInfo s = p.info[n];
     if (s.nsplit < 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
     const int parts = s.nsplit;
-    if (parts == 1 || (p.tc && s.nodes * p.G > kTileRows)) return;
+    if (parts == 1 || (p.tc && s.nodes * p.G > kTcLeast)) return;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row * p.max_splits + i].x);
 #pragma unroll
@@ -944,9 +944,7 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     AttnLayout l{};
     // a sequence of few rows has the most parts; G rows are the fewest
     l.max_tiles = tiles_of(max_nodes * (Hq / Hkv));
-    const int64_t by_len = (max_ctx + least_chunk(1, true) - 1) / least_chunk(1, true);
-    const int64_t most = most_splits(Hkv, 1);
-    l.max_splits = static_cast<int>(by_len < 1 ? 1 : by_len < most ? by_len : most);
+    l.max_splits = splits_of(max_ctx, least_chunk(1, true), Hkv, 1);
     size_t off = KDA_WS_HEADER_BYTES;
     auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
     l.info = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
@@ -960,7 +958,7 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     // the tcgen05 kernel's: every row tile (at most one not full per sequence) in each part, twice
     size_t tc = 0;
     const int64_t rows = max_nodes * static_cast<int64_t>(Hq / Hkv);
-    if (rows > kTileRows) {
+    if (rows > kTcLeast) {
         // (fewer row groups make the number of parts that fill the GPU larger: one group has the most)
         int s = 1;
         for (int g = 1; g <= tc_groups_of(tc_tiles_of(static_cast<int>(rows))); ++g) {
@@ -982,7 +980,7 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
     const int64_t seq_ctas = (static_cast<int64_t>(p.N) + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
     plan_kernel<<<static_cast<unsigned>(1 + seq_ctas), kPlanThreads, 0, s>>>(p);
     const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * (p.tc ? 1 : max_tiles);
-    const int64_t most = static_cast<int64_t>(sms) * 2;
+    const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? Ring<__nv_bfloat16, DK, DV>::kPerSm : Ring<float, DK, DV>::kPerSm);
     const dim3 grid(static_cast<unsigned>(units < most ? units : most));
     if (dtype == KDA_BF16) {
         using R = Ring<__nv_bfloat16, DK, DV>;
@@ -1058,7 +1056,7 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     p.info = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info);
     p.info_tc = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info_tc);
     p.wide = dtype == KDA_F32;
-    p.tc = dtype == KDA_BF16 && max_nodes * p.G > kda::attn::kTileRows;
+    p.tc = dtype == KDA_BF16 && max_nodes * p.G > kda::attn::kTcLeast;
     p.bad = reinterpret_cast<uint32_t *>(ws + l.bad);
     p.seq_of = reinterpret_cast<int32_t *>(ws + l.seq_of);
     p.sees = reinterpret_cast<uint64_t *>(ws + l.sees);

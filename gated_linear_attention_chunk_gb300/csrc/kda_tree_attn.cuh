@@ -14,6 +14,7 @@ namespace attn {
 using namespace spec;
 
 constexpr int kTileRows = 64;    // query rows of a unit of the register kernels
+constexpr int kTcLeast = 32;     // bf16 sequences of more rows per KV head go to the tcgen05 kernel
 constexpr int kTcRows = 128;     // query rows of a tcgen05 tile
 constexpr int kTcKeys = 128;     // keys of a tile there
 
@@ -33,7 +34,7 @@ struct AttnParams {
     int64_t T, qs, ks, vs;       // token strides in elements
     int N, Hq, Hkv, G, max_nodes, max_splits;
     bool wide;                   // fp32
-    int tc;                      // sequences of more than kTileRows rows go to the tcgen05 kernel
+    int tc;                      // sequences of more than kTcLeast rows go to the tcgen05 kernel
     float scale;
     uint32_t *status;
     SeqInfo *info, *info_tc;     // [N + 1] each; entry N holds the total in unit0
@@ -46,22 +47,28 @@ struct AttnParams {
     float2 *tc_ml;               // [part][kTcRows]
 };
 
-// How a sequence is cut: parts of at least 256 keys (more for many rows, whose partial results would outweigh the
-// keys they save), as many as give the sequence alone about one unit per SM, whatever else is in the batch.
+// How a sequence is cut, whatever else is in the batch: parts of at least least_chunk keys (a part's partial result, rows x dv
+// fp32 written and read again, has to stay small beside its keys, and so have the few microseconds that a part takes to begin and
+// end: with 256 keys in the place of 384 a batch of 128 contexts of 2048 took 238 us for 223, with 512 it took 219, but one
+// context of 1025 took 1.5 us longer), as many as give the sequence alone about one unit per SM; long contexts in parts of at
+// least 1024 keys up to three units per SM, one per resident CTA, which makes the units of a batch share out more evenly.
 constexpr int kFillUnits = 152;
-__host__ __device__ inline int most_splits(int Hkv, int tiles) {
+__host__ __device__ inline int most_splits(int Hkv, int tiles, int per_sm = 1) {
     const int per = Hkv * tiles;
-    return per >= kFillUnits ? 1 : (kFillUnits + per - 1) / per;
+    return per >= per_sm * kFillUnits ? 1 : (per_sm * kFillUnits + per - 1) / per;
 }
 __host__ __device__ inline int least_chunk(int rows, bool wide) {
     if (wide) return rows <= 32 ? 128 : rows <= 64 ? 4 * rows : 256;
-    return rows <= 16 ? 384 : rows <= 64 ? 8 * rows : 1024;
+    return rows <= 16 ? 384 : 512;
+}
+__host__ __device__ inline int splits_of(int64_t ctx, int least, int Hkv, int tiles) {
+    const int64_t some = (ctx + least - 1) / least, one = most_splits(Hkv, tiles);
+    const int64_t many = (ctx + 1023) / 1024, three = most_splits(Hkv, tiles, 3);
+    const int64_t s = some < one ? some : one, t = many < three ? many : three;
+    return static_cast<int>(s > t ? (s < 1 ? 1 : s) : (t < 1 ? 1 : t));
 }
 __host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, bool wide, int *nsplit, int *chunk) {
-    const int least = least_chunk(rows, wide);
-    int s = (ctx + least - 1) / least;
-    const int most = most_splits(Hkv, tiles);
-    s = s < 1 ? 1 : s > most ? most : s;
+    const int s = splits_of(ctx, least_chunk(rows, wide), Hkv, tiles);
     int c = (ctx + s - 1) / s;
     c = (c + 63) / 64 * 64;
     if (c < 64) c = 64;
@@ -73,11 +80,11 @@ __host__ __device__ inline int tiles_of(int rows) { return (rows + kTileRows - 1
 // The same for the tcgen05 kernel, whose units are pairs of row tiles (or one): the number that fills the GPU, or a
 // multiple of it, so that the units of a batch of such sequences share out evenly (32 parts in the place of 19 for four
 // sequences of 131,072 keys and 264 rows on 4 KV heads: 531 us against 430).
-constexpr int kTcChunk = 16384;
+constexpr int kTcChunk = 16384, kTcShort = 1024;
 __host__ __device__ inline int tc_tiles_of(int rows) { return (rows + kTcRows - 1) / kTcRows; }
 __host__ __device__ inline int tc_groups_of(int tiles) { return (tiles + 1) / 2; }
 __host__ __device__ inline int tc_splits_of(int64_t ctx, int Hkv, int groups) {
-    const int64_t some = (ctx + 1023) / 1024, most = most_splits(Hkv, groups);
+    const int64_t some = (ctx + kTcShort - 1) / kTcShort, most = most_splits(Hkv, groups);
     const int64_t s = some < most ? some : most * ((ctx + most * kTcChunk - 1) / (most * kTcChunk));
     return static_cast<int>(s < 1 ? 1 : s);
 }
