@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
                     } else {
                         s.tiles = tiles_of(rows);
                         split_of(s.ctx, rows, p.Hkv, s.tiles, p.wide, &s.nsplit, &s.chunk);
-                        units[0] = s.nsplit * s.tiles * p.Hkv;
+                        units[0] = s.nsplit * s.tiles * (p.Hkv / heads_of(rows, p.Hkv, p.wide));
                     }
                 }
             }
@@ -179,6 +179,7 @@ struct Walk {
     int unit, end;                      // units left: [unit, end)
     int n, head, tile, split;           // of the unit
     int ctx, nodes, t0, nsplit, chunk, tiles, next0;  // of the sequence; next0: the first unit after it
+    int heads;                          // KV heads of a unit (1 or 4); `head` counts groups of them
     int key, key_end;                   // context keys left in the unit
     int node, node_end;                 // drafted keys left in the unit
 
@@ -200,6 +201,7 @@ struct Walk {
         const int4 b = __ldg(reinterpret_cast<const int4 *>(p.info + n) + 1);
         ctx = a.x; nodes = a.y; t0 = a.z; nsplit = b.x; chunk = b.y; tiles = b.z;
         next0 = next;
+        heads = heads_of(nodes * p.G, p.Hkv, p.wide);
         const int u = unit - a.w, ht = u / nsplit;
         split = u - ht * nsplit;
         head = ht / tiles;
@@ -263,30 +265,32 @@ struct Ring {
         TileRow r{-1, -1};
         kbase = nullptr;
         if (w.unit >= w.end) return r;
-        const int j = threadIdx.x;
+        // a unit of four heads has a quarter of the tile for each
+        const int per = w.heads == 4 ? kKeys / 4 : kKeys, j = threadIdx.x % per, h = threadIdx.x / per;
+        const bool mine = threadIdx.x < kKeys;
         if (w.key < w.key_end) {
-            kbase = p.c.k + w.head * p.c.kh * es;
-            vbase = p.c.v + w.head * p.c.vh * es;
-            if (j < kKeys && w.key + j < w.key_end) {
+            kbase = p.c.k + w.head * w.heads * p.c.kh * es;
+            vbase = p.c.v + w.head * w.heads * p.c.vh * es;
+            if (mine && w.key + j < w.key_end) {
                 const int at = w.key + j, pg = at / p.c.page_size, slot = at - pg * p.c.page_size;
                 const int page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
                 if (page >= 0 && page < p.c.num_pages) {
-                    r = TileRow{(page * p.c.kp + slot * p.c.kr) * es, (page * p.c.vp + slot * p.c.vr) * es};
+                    r = TileRow{(page * p.c.kp + slot * p.c.kr + h * p.c.kh) * es, (page * p.c.vp + slot * p.c.vr + h * p.c.vh) * es};
                 } else {
                     atomicOr(p.bad + w.n, static_cast<uint32_t>(DEV_ERR_PAGE));
                     atomicOr(p.status, static_cast<uint32_t>(DEV_ERR_PAGE));
                     *bad_seen = 1;
                 }
             }
-            w.key += kKeys;
+            w.key += per;
         } else {
-            kbase = static_cast<const char *>(p.k) + static_cast<int64_t>(w.head) * DK * es;
-            vbase = static_cast<const char *>(p.v) + static_cast<int64_t>(w.head) * DV * es;
-            if (j < kKeys && w.node + j < w.node_end) {
+            kbase = static_cast<const char *>(p.k) + static_cast<int64_t>(w.head) * w.heads * DK * es;
+            vbase = static_cast<const char *>(p.v) + static_cast<int64_t>(w.head) * w.heads * DV * es;
+            if (mine && w.node + j < w.node_end) {
                 const int64_t t = w.t0 + w.node + j;
-                r = TileRow{t * p.ks * es, t * p.vs * es};
+                r = TileRow{(t * p.ks + h * DK) * es, (t * p.vs + h * DV) * es};
             }
-            w.node += kKeys;
+            w.node += per;
         }
         if (w.unit_done()) w.next_unit(p);
         return r;
@@ -647,13 +651,16 @@ __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], u
 // The order in which an instruction's k index runs over channels or keys is free as long as both operands agree: a lane takes
 // eight consecutive channels of every 32 (two 16-byte reads without bank conflicts), and the weights' accumulator fragment
 // is the next product's operand as it is.
-template <int DK, int DV, int RW>
+template <int DK, int DV, int RW, bool kHeads>
 __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV> &ring, Walk &cw, float2 (*ml)[16],
                                          float (&qf)[DK / 32][2][8], bool same_rows) {
     using R = Ring<float, DK, DV>;
-    constexpr int KW = R::kThreads / 32 / RW, NT = R::kKeys / 8 / KW;
+    constexpr int KT = R::kThreads / 32 / RW, NT = R::kKeys / 8 / KT;
+    constexpr int KW = kHeads ? 1 : KT;
+    constexpr int kStep = kHeads ? R::kKeys / 4 : R::kKeys;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rg = warp % RW, kg = warp / RW, key0 = kg * (R::kKeys / KW);
+    const int rg = warp % RW, kg = kHeads ? 0 : warp / RW, row0 = warp / RW * (R::kKeys / KT), key0 = kHeads ? 0 : row0;
+    const int head = kHeads ? cw.head * 4 + warp : cw.head;
     const int quad = lane >> 2, j4 = lane & 3;
     const int n = cw.n, t0 = cw.t0, split_no = cw.split, nsplit = cw.nsplit, rows = cw.nodes * p.G;
     const uint32_t flag = __ldcg(p.bad + n);
@@ -665,7 +672,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
         const int r = cw.tile * kTileRows + rg * 16 + quad + 8 * i;
         live[i] = r < rows;
         node[i] = live[i] ? r / p.G : 0;
-        hq[i] = cw.head * p.G + (live[i] ? r - node[i] * p.G : 0);
+        hq[i] = head * p.G + (live[i] ? r - node[i] * p.G : 0);
     }
     if (!same_rows)  // channels 32 g + 8 j4 + 0..7 of the two rows
 #pragma unroll
@@ -694,7 +701,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
         const bool drafted = cw.key >= cw.key_end;
         const int first = drafted ? cw.node : 0;
         const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;
-        if (drafted) cw.node += R::kKeys; else cw.key += R::kKeys;
+        if (drafted) cw.node += kStep; else cw.key += kStep;
         const TileRow ahead = ring.begin_tile(p);
         const char *ks = ring.stage(), *vs = ks + R::kBytesK;
         // hi hi, and the cross terms apart where one column of keys alone would leave the products waiting for one another
@@ -711,7 +718,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
                 float kf[NT][4];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const int row = key0 + j * 8 + quad, u = 8 * g + 2 * j4 + h;
+                    const int row = row0 + j * 8 + quad, u = 8 * g + 2 * j4 + h;
                     *reinterpret_cast<float4 *>(kf[j]) = *reinterpret_cast<const float4 *>(ks + row * (R::kUnitsK * 16) + ((u ^ (row & 7)) << 4));
                 }
                 float size = q_size;
@@ -791,7 +798,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
             // (weights are at most 1, or NaN, which their sum passes on to the whole row)
             const Split a0 = split(e[0]), a1 = split(e[2]), a2 = split(e[1]), a3 = split(e[3]);
             const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
-            const int row = key0 + 8 * k + 2 * j4;
+            const int row = row0 + 8 * k + 2 * j4;
 #pragma unroll
             for (int g = 0; g < DV / 32; ++g) {
                 float v0[4], v1[4];  // columns 32 g + 4 quad + 0..3 of the two keys
@@ -817,7 +824,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
         }
         ring.end_tile(ahead);
     }
-    join_warps<R::kThreads / 32, RW, DV>(ring.scratch(), ml, o, mx, sum);
+    join_warps<R::kThreads / 32, kHeads ? R::kThreads / 32 : RW, DV>(ring.scratch(), ml, o, mx, sum);
     const bool ok = may_write(p, n, flag, ring.bad_seen);
     if (flag && threadIdx.x == 0) atomicOr(p.status, flag);
     constexpr int NP = DV / 8 / KW;
@@ -878,9 +885,10 @@ __global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, Ring<T, DK, DV>::kP
             if (left <= 16) unit_bf16<DK, DV, 1>(p, ring, cw, ml, qf, same);
             else unit_bf16<DK, DV, 2>(p, ring, cw, ml, qf, same);  // (more rows: the tcgen05 kernel)
         } else {
-            if (left <= 16) unit_f32<DK, DV, 1>(p, ring, cw, ml, qf, same);
-            else if (left <= 32) unit_f32<DK, DV, 2>(p, ring, cw, ml, qf, same);
-            else unit_f32<DK, DV, 4>(p, ring, cw, ml, qf, same);
+            if (cw.heads == 4) unit_f32<DK, DV, 1, true>(p, ring, cw, ml, qf, same);
+            else if (left <= 16) unit_f32<DK, DV, 1, false>(p, ring, cw, ml, qf, same);
+            else if (left <= 32) unit_f32<DK, DV, 2, false>(p, ring, cw, ml, qf, same);
+            else unit_f32<DK, DV, 4, false>(p, ring, cw, ml, qf, same);
         }
         same = cw.split + 1 < cw.nsplit;
         cw.next_unit(p);
@@ -888,14 +896,16 @@ __global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, Ring<T, DK, DV>::kP
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// The parts of a row joined in order: one warp per (node, query head), a lane DV / 32 columns
+// The parts of a row (node, query head) joined: four sums of every fourth part, added in order.  kWarps = 1: a warp has all
+// four; 4: a warp each, where there are few rows (one warp per row took 28 us for 256 rows of 114 parts).  A lane has DV / 32 columns.
 // ---------------------------------------------------------------------------------------------------------------
-template <typename T, int DV>
+template <typename T, int DV, int kWarps>
 __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams p) {
-    constexpr int VL = DV / 32;
+    constexpr int VL = DV / 32, kSums = 4 / kWarps;  // sums of a warp
+    __shared__ float share[kWarps == 4 ? 4 : 1][VL + 1][32];
     grid_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 32) + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = kWarps == 4 ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 32) + warp;
     if (row >= p.T * p.Hq) return;
     const int64_t t = row / p.Hq;
     // (a packed node beyond the last sequence has no entry: whatever is read there does not contain it)
@@ -905,30 +915,61 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
     if (s.nsplit < 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
     const int parts = s.nsplit;
     if (parts == 1 || (p.tc && s.nodes * p.G > kTcLeast)) return;
+    const float2 *ml = p.part_ml + row * p.max_splits;
     float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[row * p.max_splits + i].x);
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[i].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[VL] = {};
+    float l[kSums] = {}, o[kSums][VL] = {};
+    const float *src = p.part_o + row * p.max_splits * DV + lane * VL;
+    const int first = kWarps == 4 ? warp : 0;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const int64_t at = row * p.max_splits + i;
-        const float2 ml = p.part_ml[at];
-        const float f = exp2f(ml.x - base);
-        l = fmaf(f, ml.y, l);
+    for (int i0 = first; i0 < parts; i0 += 4)
 #pragma unroll
-        for (int x = 0; x < VL; x += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(p.part_o + at * DV + lane * VL + x);
-            o[x] = fmaf(f, v.x, o[x]);
-            o[x + 1] = fmaf(f, v.y, o[x + 1]);
+        for (int c = 0; c < kSums; ++c) {
+            const int i = i0 + c;
+            if (i < parts) {
+                const float2 part = ml[i];
+                const float f = exp2f(part.x - base);
+                l[c] = fmaf(f, part.y, l[c]);
+#pragma unroll
+                for (int x = 0; x < VL; x += 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + static_cast<int64_t>(i) * DV + x);
+                    o[c][x] = fmaf(f, v.x, o[c][x]);
+                    o[c][x + 1] = fmaf(f, v.y, o[c][x + 1]);
+                }
+            }
         }
+    float sum, out[VL];
+    if constexpr (kWarps == 4) {
+        auto &all = share;
+#pragma unroll
+        for (int x = 0; x < VL; ++x) all[warp][x][lane] = o[0][x];
+        all[warp][VL][lane] = l[0];
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int x = 0; x < VL; ++x) out[x] = (all[0][x][lane] + all[1][x][lane]) + (all[2][x][lane] + all[3][x][lane]);
+        sum = (all[0][VL][lane] + all[1][VL][lane]) + (all[2][VL][lane] + all[3][VL][lane]);
+    } else {
+#pragma unroll
+        for (int x = 0; x < VL; ++x) out[x] = (o[0][x] + o[1][x]) + (o[2][x] + o[3][x]);
+        sum = (l[0] + l[1]) + (l[2] + l[3]);
     }
-    const float inv = 1.f / l;
+    const float inv = 1.f / sum;
     T *to = static_cast<T *>(p.o) + row * DV + lane * VL;
 #pragma unroll
-    for (int x = 0; x < VL; ++x) to[x] = Elem<T>::from_f(o[x] * inv);
-    if (p.lse && lane == 0) p.lse[row] = (m + log2f(l)) * kLn2;
+    for (int x = 0; x < VL; ++x) to[x] = Elem<T>::from_f(out[x] * inv);
+    if (p.lse && lane == 0) p.lse[row] = (m + log2f(sum)) * kLn2;
+}
+
+template <typename T, int DV>
+cudaError_t launch_combine(const AttnParams &p, cudaStream_t s) {
+    const int64_t rows = p.T * p.Hq;
+    if (rows <= 4096) return launch_after(combine_kernel<T, DV, 4>, dim3(static_cast<unsigned>(rows)), kAttnThreads, 0, s, p);
+    constexpr int kPer = kAttnThreads / 32;
+    return launch_after(combine_kernel<T, DV, 1>, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)), kAttnThreads, 0, s, p);
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -944,7 +985,7 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     AttnLayout l{};
     // a sequence of few rows has the most parts; G rows are the fewest
     l.max_tiles = tiles_of(max_nodes * (Hq / Hkv));
-    l.max_splits = splits_of(max_ctx, least_chunk(1, true), Hkv, 1);
+    l.max_splits = splits_of(max_ctx, 128, Hkv % 4 == 0 ? Hkv / 4 : Hkv, 1);  // (no sequence has smaller parts)
     size_t off = KDA_WS_HEADER_BYTES;
     auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
     l.info = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
@@ -994,13 +1035,8 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
         if (!smem_opt_in<attn_kernel<float, DK, DV>>(smem)) return KDA_ERR_CUDA;
         if (launch_after(attn_kernel<float, DK, DV>, grid, R::kThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
     }
-    if (p.max_splits > 1) {
-        const int64_t rows = p.T * p.Hq;
-        const unsigned cg = static_cast<unsigned>((rows + kAttnThreads / 32 - 1) / (kAttnThreads / 32));
-        const cudaError_t e = dtype == KDA_BF16 ? launch_after(combine_kernel<__nv_bfloat16, DV>, dim3(cg), kAttnThreads, 0, s, p)
-                                                : launch_after(combine_kernel<float, DV>, dim3(cg), kAttnThreads, 0, s, p);
-        if (e != cudaSuccess) return KDA_ERR_CUDA;
-    }
+    if (p.max_splits > 1 && (dtype == KDA_BF16 ? launch_combine<__nv_bfloat16, DV>(p, s) : launch_combine<float, DV>(p, s)) != cudaSuccess)
+        return KDA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -1022,7 +1058,7 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
                          void *o, float *lse, void *workspace, size_t ws_bytes, void *stream) {
     using namespace kda::spec;
     if (!dtype_ok(dtype) || !dim_ok(dk) || !dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
-    if (N < 0 || N > (1 << 20) || T < 0 || T > 0x7fffffffLL || Hq <= 0 || Hkv <= 0 || Hq > 4096 || Hq % Hkv)
+    if (N < 0 || N > (1 << 20) || T < 0 || T > 0x7fffffffLL || Hq <= 0 || Hkv <= 0 || Hq > 4096 || Hq % Hkv || T * Hq > 0x7fffffffLL)
         return KDA_ERR_INVALID_ARGUMENT;
     if (max_nodes < 1 || max_nodes > KDA_MAX_TREE_NODES || T > static_cast<int64_t>(N) * max_nodes) return KDA_ERR_INVALID_ARGUMENT;
     Pages c;

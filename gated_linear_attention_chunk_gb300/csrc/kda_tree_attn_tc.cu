@@ -606,11 +606,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     if (warp == kSoftmaxWarps + kLoadWarps) tmem_dealloc(tmem, 512);
 }
 
-// The parts of a row tile joined in order: a thread per row, kCombCols columns of it.
+// The parts of a row tile joined, kCombCols columns of it: four threads per row take every fourth part each, and their sums
+// are added in order.
 constexpr int kCombCols = 8;
 
 template <int DV>
-__global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(4 * kTcRows) combine_tc_kernel(const AttnParams p) {
+    __shared__ float share[3][kCombCols + 1][kTcRows];
     grid_wait();
     const int n = blockIdx.x, max_tiles = gridDim.y / p.Hkv;
     const int head = blockIdx.y / max_tiles, tile = blockIdx.y - head * max_tiles, c0 = blockIdx.z * kCombCols;
@@ -618,42 +620,53 @@ __global__ void __launch_bounds__(kTcRows) combine_tc_kernel(const AttnParams p)
     if (p.info_tc[n + 1].unit0 == s.unit0 || tile >= s.tiles) return;
     const bool alone = (tile | 1) >= s.tiles;
     if ((!alone && s.nsplit == 1) || p.bad[n]) return;
-    const int row = threadIdx.x, r = tile * kTcRows + row, parts = alone ? 2 * s.nsplit : s.nsplit;
-    if (r >= s.nodes * p.G) return;
+    const int row = threadIdx.x % kTcRows, chain = threadIdx.x / kTcRows, r = tile * kTcRows + row;
+    const int parts = alone ? 2 * s.nsplit : s.nsplit;
+    const bool live = r < s.nodes * p.G;
     const int64_t id0 = s.unit0 + static_cast<int64_t>(head) * s.nsplit * s.tiles + tile;
     auto part = [&](int i) { return alone ? tc_part(id0 + static_cast<int64_t>(i >> 1) * s.tiles, i & 1) : tc_part(id0 + static_cast<int64_t>(i) * s.tiles, 0); };
     float m = -INFINITY;
+    if (live) {
 #pragma unroll 8
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, p.tc_ml[part(i) * kTcRows + row].x);
+        for (int i = 0; i < parts; ++i) m = fmaxf(m, p.tc_ml[part(i) * kTcRows + row].x);
+    }
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[kCombCols] = {};
+    if (live) {
 #pragma unroll 8
-    for (int i = 0; i < parts; ++i) {
-        const float2 ml = p.tc_ml[part(i) * kTcRows + row];
-        const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
-        const bool empty = ml.y == 0.f;  // no keys: its sums were not written
-        const float f = exp2f(ml.x - base);
-        l = fmaf(f, ml.y, l);
+        for (int i = chain; i < parts; i += 4) {
+            const float2 ml = p.tc_ml[part(i) * kTcRows + row];
+            const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
+            const bool empty = ml.y == 0.f;  // no keys: its sums were not written
+            const float f = exp2f(ml.x - base);
+            l = fmaf(f, ml.y, l);
 #pragma unroll
-        for (int j = 0; j < kCombCols / 4; ++j) {
-            const float4 v = src[j * kTcRows];
-            o[4 * j] = fmaf(f, empty ? 0.f : v.x, o[4 * j]);
-            o[4 * j + 1] = fmaf(f, empty ? 0.f : v.y, o[4 * j + 1]);
-            o[4 * j + 2] = fmaf(f, empty ? 0.f : v.z, o[4 * j + 2]);
-            o[4 * j + 3] = fmaf(f, empty ? 0.f : v.w, o[4 * j + 3]);
+            for (int j = 0; j < kCombCols / 4; ++j) {
+                const float4 v = src[j * kTcRows];
+                o[4 * j] = fmaf(f, empty ? 0.f : v.x, o[4 * j]);
+                o[4 * j + 1] = fmaf(f, empty ? 0.f : v.y, o[4 * j + 1]);
+                o[4 * j + 2] = fmaf(f, empty ? 0.f : v.z, o[4 * j + 2]);
+                o[4 * j + 3] = fmaf(f, empty ? 0.f : v.w, o[4 * j + 3]);
+            }
         }
     }
+    if (chain > 0) {
+#pragma unroll
+        for (int x = 0; x < kCombCols; ++x) share[chain - 1][x][row] = o[x];
+        share[chain - 1][kCombCols][row] = l;
+    }
+    __syncthreads();
+    if (chain > 0 || !live) return;
+#pragma unroll
+    for (int x = 0; x < kCombCols; ++x) o[x] = (o[x] + share[0][x][row]) + (share[1][x][row] + share[2][x][row]);
+    l = (l + share[0][kCombCols][row]) + (share[1][kCombCols][row] + share[2][kCombCols][row]);
     const float inv = 1.f / l;
     const int node = r / p.G;
     const int64_t out = static_cast<int64_t>(s.t0 + node) * p.Hq + head * p.G + r - node * p.G;
-    uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + c0);
+    uint32_t k[4];
 #pragma unroll
-    for (int i = 0; i < kCombCols / 8; ++i) {
-        uint32_t k[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = pack_bf16x2(o[8 * i + 2 * j] * inv, o[8 * i + 2 * j + 1] * inv);
-        to[i] = make_uint4(k[0], k[1], k[2], k[3]);
-    }
+    for (int j = 0; j < 4; ++j) k[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + c0) = make_uint4(k[0], k[1], k[2], k[3]);
     if (p.lse && c0 == 0) p.lse[out] = (m + log2f(l)) * kLn2;
 }
 
@@ -664,7 +677,7 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
     const cudaError_t e = launch_after(attn_tc_kernel<DK, DV>, dim3(sms), kTcThreads, bytes, s, p);
     if (e != cudaSuccess) return e;
     const dim3 grid(p.N, p.Hkv * tc_tiles_of(p.max_nodes * p.G), DV / kCombCols);
-    return launch_after(combine_tc_kernel<DV>, grid, kTcRows, 0, s, p);
+    return launch_after(combine_tc_kernel<DV>, grid, 4 * kTcRows, 0, s, p);
 }
 
 }  // namespace
