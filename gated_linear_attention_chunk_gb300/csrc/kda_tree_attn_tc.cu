@@ -606,13 +606,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     if (warp == kSoftmaxWarps + kLoadWarps) tmem_dealloc(tmem, 512);
 }
 
-// The parts of a row tile joined, kCombCols columns of it: four threads per row take every fourth part each, and their sums
-// are added in order.
+// The parts of a row tile joined, kCombCols columns of it: four sums of every fourth part, added in order.  kWays = 4: a
+// thread for each of them, where there are few tiles; 1: one thread for all.
 constexpr int kCombCols = 8;
 
-template <int DV>
-__global__ void __launch_bounds__(4 * kTcRows) combine_tc_kernel(const AttnParams p) {
-    __shared__ float share[3][kCombCols + 1][kTcRows];
+template <int DV, int kWays>
+__global__ void __launch_bounds__(kWays * kTcRows) combine_tc_kernel(const AttnParams p) {
+    constexpr int kSums = 4 / kWays;
+    __shared__ float share[kWays == 4 ? 3 : 1][kCombCols + 1][kWays == 4 ? kTcRows : 1];
     grid_wait();
     const int n = blockIdx.x, max_tiles = gridDim.y / p.Hkv;
     const int head = blockIdx.y / max_tiles, tile = blockIdx.y - head * max_tiles, c0 = blockIdx.z * kCombCols;
@@ -631,43 +632,55 @@ __global__ void __launch_bounds__(4 * kTcRows) combine_tc_kernel(const AttnParam
         for (int i = 0; i < parts; ++i) m = fmaxf(m, p.tc_ml[part(i) * kTcRows + row].x);
     }
     const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[kCombCols] = {};
+    float l[kSums] = {}, o[kSums][kCombCols] = {};
     if (live) {
-#pragma unroll 8
-        for (int i = chain; i < parts; i += 4) {
-            const float2 ml = p.tc_ml[part(i) * kTcRows + row];
-            const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
-            const bool empty = ml.y == 0.f;  // no keys: its sums were not written
-            const float f = exp2f(ml.x - base);
-            l = fmaf(f, ml.y, l);
+#pragma unroll(kWays == 4 ? 8 : 2)
+        for (int i0 = chain; i0 < parts; i0 += 4)
 #pragma unroll
-            for (int j = 0; j < kCombCols / 4; ++j) {
-                const float4 v = src[j * kTcRows];
-                o[4 * j] = fmaf(f, empty ? 0.f : v.x, o[4 * j]);
-                o[4 * j + 1] = fmaf(f, empty ? 0.f : v.y, o[4 * j + 1]);
-                o[4 * j + 2] = fmaf(f, empty ? 0.f : v.z, o[4 * j + 2]);
-                o[4 * j + 3] = fmaf(f, empty ? 0.f : v.w, o[4 * j + 3]);
+            for (int y = 0; y < kSums; ++y) {
+                const int i = i0 + y;
+                if (i >= parts) break;
+                const float2 ml = p.tc_ml[part(i) * kTcRows + row];
+                const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
+                const bool empty = ml.y == 0.f;  // no keys: its sums were not written
+                const float f = exp2f(ml.x - base);
+                l[y] = fmaf(f, ml.y, l[y]);
+#pragma unroll
+                for (int j = 0; j < kCombCols / 4; ++j) {
+                    const float4 v = src[j * kTcRows];
+                    o[y][4 * j] = fmaf(f, empty ? 0.f : v.x, o[y][4 * j]);
+                    o[y][4 * j + 1] = fmaf(f, empty ? 0.f : v.y, o[y][4 * j + 1]);
+                    o[y][4 * j + 2] = fmaf(f, empty ? 0.f : v.z, o[y][4 * j + 2]);
+                    o[y][4 * j + 3] = fmaf(f, empty ? 0.f : v.w, o[y][4 * j + 3]);
+                }
             }
+    }
+    float sum, out_o[kCombCols];
+    if constexpr (kWays == 4) {
+        if (chain > 0) {
+#pragma unroll
+            for (int x = 0; x < kCombCols; ++x) share[chain - 1][x][row] = o[0][x];
+            share[chain - 1][kCombCols][row] = l[0];
         }
-    }
-    if (chain > 0) {
+        __syncthreads();
+        if (chain > 0) return;
 #pragma unroll
-        for (int x = 0; x < kCombCols; ++x) share[chain - 1][x][row] = o[x];
-        share[chain - 1][kCombCols][row] = l;
-    }
-    __syncthreads();
-    if (chain > 0 || !live) return;
+        for (int x = 0; x < kCombCols; ++x) out_o[x] = (o[0][x] + share[0][x][row]) + (share[1][x][row] + share[2][x][row]);
+        sum = (l[0] + share[0][kCombCols][row]) + (share[1][kCombCols][row] + share[2][kCombCols][row]);
+    } else {
 #pragma unroll
-    for (int x = 0; x < kCombCols; ++x) o[x] = (o[x] + share[0][x][row]) + (share[1][x][row] + share[2][x][row]);
-    l = (l + share[0][kCombCols][row]) + (share[1][kCombCols][row] + share[2][kCombCols][row]);
-    const float inv = 1.f / l;
+        for (int x = 0; x < kCombCols; ++x) out_o[x] = (o[0][x] + o[1][x]) + (o[2][x] + o[3][x]);
+        sum = (l[0] + l[1]) + (l[2] + l[3]);
+    }
+    if (!live) return;
+    const float inv = 1.f / sum;
     const int node = r / p.G;
     const int64_t out = static_cast<int64_t>(s.t0 + node) * p.Hq + head * p.G + r - node * p.G;
     uint32_t k[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+    for (int j = 0; j < 4; ++j) k[j] = pack_bf16x2(out_o[2 * j] * inv, out_o[2 * j + 1] * inv);
     *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + out * DV + c0) = make_uint4(k[0], k[1], k[2], k[3]);
-    if (p.lse && c0 == 0) p.lse[out] = (m + log2f(l)) * kLn2;
+    if (p.lse && c0 == 0) p.lse[out] = (m + log2f(sum)) * kLn2;
 }
 
 template <int DK, int DV>
@@ -677,7 +690,8 @@ cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
     const cudaError_t e = launch_after(attn_tc_kernel<DK, DV>, dim3(sms), kTcThreads, bytes, s, p);
     if (e != cudaSuccess) return e;
     const dim3 grid(p.N, p.Hkv * tc_tiles_of(p.max_nodes * p.G), DV / kCombCols);
-    return launch_after(combine_tc_kernel<DV>, grid, 4 * kTcRows, 0, s, p);
+    if (static_cast<int64_t>(grid.x) * grid.y * grid.z <= 2048) return launch_after(combine_tc_kernel<DV, 4>, grid, 4 * kTcRows, 0, s, p);
+    return launch_after(combine_tc_kernel<DV, 1>, grid, kTcRows, 0, s, p);
 }
 
 }  // namespace
