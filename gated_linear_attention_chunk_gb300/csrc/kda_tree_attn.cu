@@ -704,13 +704,9 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
         if (drafted) cw.node += kStep; else cw.key += kStep;
         const TileRow ahead = ring.begin_tile(p);
         const char *ks = ring.stage(), *vs = ks + R::kBytesK;
-        // hi hi, and the cross terms apart where one column of keys alone would leave the products waiting for one another
-        float s[NT][4], x[4];
-        constexpr bool kApart = NT == 1;
+        float s[NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = x[e] = 0.f;
+        for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
         for (int g = 0; g < DK / 32; ++g)
 #pragma unroll
@@ -726,24 +722,40 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) size = fmaf(kf[j][y], kf[j][y], size);
+                // The tensor cores cut sums off instead of rounding them: sixteen channels are summed there, the small terms first,
+                // and what comes out is added with rounding (one sum through was three times as far off).
                 auto products = [&](auto any) {
                     constexpr bool kAny = decltype(any)::value;
+                    // (split again for every tile: kept between them, the parts would not fit the registers)
 #pragma unroll
-                    for (int y = 0; y < 4; y += 2) {
-                        // (split again for every tile: kept between them, the parts would not fit the registers)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) asm volatile("" : "+f"(qf[g][i][4 * h + y]), "+f"(qf[g][i][4 * h + y + 1]));
-                        const Split a0 = split_as<kAny>(qf[g][0][4 * h + y]), a1 = split_as<kAny>(qf[g][1][4 * h + y]);
-                        const Split a2 = split_as<kAny>(qf[g][0][4 * h + y + 1]), a3 = split_as<kAny>(qf[g][1][4 * h + y + 1]);
-                        const uint32_t ah[4] = {a0.hi, a1.hi, a2.hi, a3.hi}, af[4] = {a0.fin, a1.fin, a2.fin, a3.fin};
-                        const uint32_t al[4] = {a0.lo, a1.lo, a2.lo, a3.lo};
+                        for (int y = 0; y < 4; ++y) asm volatile("" : "+f"(qf[g][i][4 * h + y]));
+                    Split a[2][4];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const Split b0 = split_as<kAny>(kf[j][y]), b1 = split_as<kAny>(kf[j][y + 1]);
-                            mma1688(s[j], ah, b0.hi, b1.hi);
-                            mma1688(kApart ? x : s[j], af, b0.lo, b1.lo);
-                            mma1688(kApart ? x : s[j], al, b0.fin, b1.fin);
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[y][e] = split_as<kAny>(qf[g][e & 1][4 * h + 2 * y + (e >> 1)]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                        Split b[2][2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            b[y][0] = split_as<kAny>(kf[j][2 * y]);
+                            b[y][1] = split_as<kAny>(kf[j][2 * y + 1]);
+                            const uint32_t af[4] = {a[y][0].fin, a[y][1].fin, a[y][2].fin, a[y][3].fin};
+                            const uint32_t al[4] = {a[y][0].lo, a[y][1].lo, a[y][2].lo, a[y][3].lo};
+                            mma1688(t, af, b[y][0].lo, b[y][1].lo);
+                            mma1688(t, al, b[y][0].fin, b[y][1].fin);
                         }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t ah[4] = {a[y][0].hi, a[y][1].hi, a[y][2].hi, a[y][3].hi};
+                            mma1688(t, ah, b[y][0].hi, b[y][1].hi);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[j][e] += t[e];
                     }
                 };
                 if (__any_sync(0xffffffffu, !(size < INFINITY))) products(std::true_type{});
@@ -760,7 +772,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = key0 + j * 8 + 2 * j4 + (e & 1);
-                float t = (kApart ? s[j][e] + x[e] : s[j][e]) * c;
+                float t = s[j][e] * c;
                 if (key >= count || !((sees[e >> 1] >> key) & 1)) t = -INFINITY;
                 s[j][e] = t;
                 top[e >> 1] = fmaxf(top[e >> 1], t);
@@ -813,9 +825,12 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const Split b0 = split_as<kAny>(v0[q]), b1 = split_as<kAny>(v1[q]);
-                        mma1688(o[4 * g + q], ah, b0.hi, b1.hi);
-                        mma1688(o[4 * g + q], ah, b0.lo, b1.lo);
-                        mma1688(o[4 * g + q], al, b0.fin, b1.fin);
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma1688(t, ah, b0.lo, b1.lo);
+                        mma1688(t, al, b0.fin, b1.fin);
+                        mma1688(t, ah, b0.hi, b1.hi);
+#pragma unroll
+                        for (int e2 = 0; e2 < 4; ++e2) o[4 * g + q][e2] += t[e2];
                     }
                 };
                 if (__any_sync(0xffffffffu, !(size < INFINITY))) products(std::true_type{});
