@@ -14,6 +14,13 @@
 // combine_kernel joins them in part order.  Everything a unit does depends on its own sequence alone,
 // so a sequence's bits do not depend on the batch.
 //
+// Bounded by the bytes of the cache: 128 sequences of 1 to 4 nodes over 1 to 4,096 keys (8 KV heads, bf16) take 204 us, 5.3 TB/s; 16 rows
+// over 131,072 keys 188 us, 5.7 TB/s.  The four warps of a CTA take a quarter of a tile's 64 keys each (half, on two row
+// groups) and are joined through shared memory at the end of a part; three CTAs of two stages per SM cover one another's part ends
+// (two CTAs of three stages: 224 us).  From 33 rows on (bf16) the tcgen05 kernel takes over: mma.sync falls behind the
+// loads there (40 rows over 131,072 keys: 358 us, there 250).  fp32 is bound by the rate of mma.sync in tf32: 40 us for seven
+// sequences of 1 to 13 nodes over 1 to 4,099 keys.
+//
 // plan_kernel, one launch before: checks the lengths, lists the sequences with their first unit, and
 // turns the parents into ancestor masks (one 64-bit word per node, by pointer doubling).
 #include <cuda_bf16.h>
@@ -995,6 +1002,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct AttnLayout {
     size_t info, info_tc, bad, seq_of, sees, part_ml, part_o, tc_ml, tc_o, total;
     int max_splits, max_tiles;
+    int64_t units;               // at most so many in either list (tcgen05: row tiles times parts)
 };
 AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
     AttnLayout l{};
@@ -1013,6 +1021,7 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     l.part_o = take(parts * dv * sizeof(float));
     // the tcgen05 kernel's: every row tile (at most one not full per sequence) in each part, twice
     size_t tc = 0;
+    l.units = static_cast<int64_t>(N) * Hkv * l.max_splits * l.max_tiles;
     const int64_t rows = max_nodes * static_cast<int64_t>(Hq / Hkv);
     if (rows > kTcLeast) {
         // (fewer row groups make the number of parts that fill the GPU larger: one group has the most)
@@ -1021,7 +1030,9 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
             const int x = tc_splits_of(max_ctx, Hkv, g);
             if (x > s) s = x;
         }
-        tc = static_cast<size_t>(T * (Hq / Hkv) / kTcRows + N) * Hkv * s * 2;
+        const int64_t tiles = (T * (Hq / Hkv) / kTcRows + N) * Hkv * s;
+        if (tiles > l.units) l.units = tiles;
+        tc = static_cast<size_t>(tiles) * 2;
     }
     l.tc_ml = take(tc * kTcRows * sizeof(float2));
     l.tc_o = take(tc * kTcRows * dv * sizeof(float));
@@ -1095,7 +1106,7 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4))
         return KDA_ERR_INVALID_ARGUMENT;
     const kda::AttnLayout l = kda::layout_of(N, T, Hq, Hkv, dv, max_nodes, max_ctx);
-    if (static_cast<int64_t>(N) * Hkv * l.max_splits * l.max_tiles > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
+    if (l.units > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0 || T == 0) return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);

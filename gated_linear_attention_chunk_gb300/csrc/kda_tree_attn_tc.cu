@@ -18,6 +18,10 @@
 // filled with zeros.  The ring holds the tiles in the order in which they are consumed:
 // K_0 .. K_{L-1}, V_0, K_L, V_1, K_{L+1}, .. with L = 1 for a pair and 2 for a tile alone.
 //
+// Four sequences of 32 nodes over 131,072 keys (8 heads on each of 4 KV heads: a pair of tiles): 273 us, 1.0 PFLOP/s.  A pair's
+// step of 2 x 128 x 128 scores takes 3.4k clocks, the chain of one stream: maximum 0.6k, exponentials 1.0k (16 per clock and
+// SM), PV 0.45k, QK 0.5k and the hand-offs.  A tile alone is bound by the loads: 250 us, 4.3 TB/s.
+//
 // Every wait is bounded (2 s): a role that gives up raises the abort flag, which ends all the others' waits; the MMAs
 // issued so far are drained and the TMEM is freed.
 #include <cuda_bf16.h>

@@ -429,8 +429,9 @@ typedef struct kda_paged_kv {
  *   k, v   [T, Hkv, dk], [T, Hkv, dv]: the nodes' own keys and values, not in the cache
  *   o      [T, Hq, dv] dtype, packed;  lse [T, Hq] fp32 or NULL: log sum exp(scale q.k)
  *   max_nodes  the largest tree of the batch (1..KDA_MAX_TREE_NODES); a larger one is
- *          reported as KDA_ERR_BAD_SEQLENS
- * dk, dv each 64 or 128.  Scores, softmax and sums are fp32; for bf16 the weights are
+ *          reported as KDA_ERR_BAD_SEQLENS.  T <= N * max_nodes; packed nodes from
+ *          cu_nodes[N] on are not read, and their outputs not written.
+ * dk, dv each 64 or 128; page_size * max_pages < 2^31.  Scores, softmax and sums are fp32; for bf16 the weights are
  * rounded to bf16 before they meet the values (fp32 inputs: products in three tf32 terms, about 22 bits).
  * Long contexts are cut into parts that run concurrently and are joined in a fixed
  * order; the cut goes by a sequence's own length and tree, so its bits do not depend

@@ -125,6 +125,43 @@ def test_batch_invariance_and_repeatability(kda, dtype):
 
 
 @pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+@pytest.mark.parametrize("nodes", [2, 20])  # 16 and 160 query rows per KV head
+def test_batch_size_changes_no_bits(kda, dtype, nodes):
+    """A sequence of many parts alone, and among so many others that the parts are joined by the other kernels."""
+    sizes, ctx = [nodes] + [64] * 9, [9000] + [3] * 9
+    whole = _case(sizes, ctx, 8, 4, 128, 128, 64, dtype, True, seed=11)
+    o, lse, _ = _run(kda, whole)
+    alone = dict(whole, cu=ref.offsets([nodes]), ctx=whole["ctx"][:1], table=whole["table"][:1])
+    for key in ("q", "k", "v", "parent"):
+        alone[key] = whole[key][:nodes]
+    a, b, _ = _run(kda, alone, max_nodes=nodes)
+    assert torch.equal(a, o[:nodes]) and torch.equal(b, lse[:nodes])
+    _check(alone, a, b)
+
+
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+def test_infinite_value_in_sight(kda, dtype):
+    c = _case([3], [100], 2, 4, 64, 64, 16, dtype, False, seed=2)
+    page, slot = int(c["table"][0, 3]), 5
+    c["vp"][page, slot, 1, 7] = float("inf")
+    o, _, _ = _run(kda, c)
+    assert bool(torch.isposinf(o[:, 2:4, 7]).all())
+    o[:, 2:4, 7] = 0
+    assert bool(torch.isfinite(o).all())
+
+
+def test_padded_nodes_are_left_alone(kda):
+    c = _case([3, 4], [70, 40], 4, 2, 128, 128, 16, ref.BF16, True, seed=7)
+    want = _run(kda, c)
+    padded = dict(c)
+    for key in ("q", "k", "v", "parent"):
+        padded[key] = torch.cat([c[key], c[key][:1].expand(3, *c[key].shape[1:])])
+    o, lse, status = _marked(kda, padded)
+    assert status == kda.KDA_OK and torch.equal(o[:7], want[0]) and torch.equal(lse[:7], want[1])
+    assert bool((o[7:] == 7).all()) and bool((lse[7:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
 def test_strides_and_axis_orders(kda, dtype):
     """q, k, v inside one fused projection; heads before rows in the pools; K and V interleaved in one pool."""
     c = _case([6, 3], [200, 90], 4, 2, 128, 128, 16, dtype, True, seed=5)
