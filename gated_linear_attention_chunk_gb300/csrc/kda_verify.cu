@@ -15,7 +15,8 @@
 // holds its point again.  So a sequence costs about one reading of one row (two with draft rows),
 // which bounds it: the rest is the latency of the walk's dependent loads.  128 chains of 4 nodes over 131,072 tokens, fp32: 44 us,
 // of them 21.7 in the pass (6.2 TB/s); one tree of 6 nodes over 32,001: 12.3 us a call,
-// 16.4 where a sibling is tried after a refusal (a pass more).  Four CTAs of 256 threads per SM keep all sequences resident (one of 512 took 100 us, eight per sequence in two rounds 54, two per sequence 48.5).
+// 16.4 where a sibling is tried after a refusal (a pass more).  Four CTAs of 256 threads per SM keep all sequences
+// resident (one of 512 took 100 us, eight per sequence in two rounds 54, two per sequence 48.5).
 //
 // Precision: the answers are whole numbers, so a rounding shows only next to a border, where a flat
 // distribution over 10^5 tokens has one every 10^-5.  p - A q is carried as an unevaluated fp32 pair with
