@@ -241,10 +241,14 @@ struct Walk {
     }
 };
 
-// A key row of a tile: byte offsets of its K and V rows from the tile's bases; negative: no such row (zeros).
+// A key row of a tile: byte offsets of its K and V rows from the tile's bases (multiples of 16), each with bit 0 set where there is
+// no such row (zeros; the copy of no bytes still names an aligned address, the base's).
 struct __align__(16) TileRow {
     int64_t k, v;
 };
+constexpr TileRow kNoRow{1, 1};
+__device__ __forceinline__ bool row_there(int64_t off) { return (off & 1) == 0; }
+__device__ __forceinline__ int64_t row_offset(int64_t off) { return off & ~static_cast<int64_t>(1); }
 
 // The ring of key / value tiles.  A tile is kKeys rows of K, then kKeys rows of V; the 16-byte
 // units of a row are permuted by its low three row bits, so that both a column of eight rows and a row are read
@@ -269,7 +273,7 @@ struct Ring {
     // Rows of the walk's tile; moves the walk past it.  Every thread takes part, threads < kKeys have a row.
     __device__ __forceinline__ TileRow look(const AttnParams &p) {
         constexpr int64_t es = sizeof(T);
-        TileRow r{-1, -1};
+        TileRow r = kNoRow;
         kbase = nullptr;
         if (w.unit >= w.end) return r;
         // a unit of four heads has a quarter of the tile for each
@@ -324,10 +328,10 @@ struct Ring {
 #pragma unroll
                 for (int i = 0; i < kKeys / kSide; ++i) {
                     const TileRow x = tr[r0 + i * kSide];
-                    const bool there = x.k >= 0;
+                    const bool there = row_there(x.k);
                     const uint32_t to = dst + place<kUnitsK>(r0, i * kSide, u);
-                    cp16(to, ks + x.k, there);
-                    cp16(to + kBytesK, vs + x.v, there);
+                    cp16(to, ks + row_offset(x.k), there);
+                    cp16(to + kBytesK, vs + row_offset(x.v), there);
                 }
             } else {
                 copy<kUnitsK>(dst, &tr->k, kbase);
@@ -343,7 +347,7 @@ struct Ring {
 #pragma unroll
         for (int i = 0; i < kKeys / kSide; ++i) {
             const int64_t x = off[2 * (r0 + i * kSide)];
-            cp16(dst + place<kUnits>(r0, i * kSide, u), base + u * 16 + x, x >= 0);
+            cp16(dst + place<kUnits>(r0, i * kSide, u), base + u * 16 + row_offset(x), row_there(x));
         }
     }
     __device__ __forceinline__ void start(const AttnParams &p, const Walk &from) {
