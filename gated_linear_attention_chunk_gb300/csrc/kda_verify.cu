@@ -258,7 +258,7 @@ __device__ __forceinline__ uint64_t children(const int (&par)[2], int node) {
     return (static_cast<uint64_t>(__ballot_sync(0xffffffffu, par[1] == node)) << 32) | __ballot_sync(0xffffffffu, par[0] == node);
 }
 
-// The cluster barrier in two halves.
+// The cluster barrier in two halves, each run by converged warps (__syncwarp before it).
 __device__ __forceinline__ void cg_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cg_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     }
 
     // ---- the sequence's outputs; the last sequence to finish packs them all
+    __syncwarp();
     cg_arrive();
     if (rank == 0 && threadIdx.x == 0) p.next_token[n] = token;
     if (publisher && !told) publish();
@@ -521,6 +522,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
         if (is_last && !packed && warp > 0) pack();
     }
     grid_wait();
+    __syncwarp();
     cg_wait();  // no CTA leaves while another may still read its sums
 }
 
