@@ -38,12 +38,14 @@ using namespace attn;
 
 constexpr int kAttnThreads = 128;
 
-__device__ __forceinline__ uint32_t seq_check(const AttnParams &p, int n, int *t0, int *m, int *ctx) {
+// `before`: the largest of cu[0 .. n - 1].  A sequence that begins below it shares nodes with an earlier one: the masks and the
+// room for partial results hold each packed node once.
+__device__ __forceinline__ uint32_t seq_check(const AttnParams &p, int n, int before, int *t0, int *m, int *ctx) {
     const int64_t a = p.cu[n], b = p.cu[n + 1], c = p.c.ctx_len[n];
     *t0 = static_cast<int>(a);
     *m = static_cast<int>(b - a);
     *ctx = static_cast<int>(c);
-    if (a < 0 || a > b || b > p.T || b - a > p.max_nodes || (n == 0 && a != 0)) return DEV_ERR_SEQLENS;
+    if (a < 0 || a > b || b > p.T || b - a > p.max_nodes || (n == 0 && a != 0) || a < before) return DEV_ERR_SEQLENS;
     if (c < 0 || c > static_cast<int64_t>(p.c.max_pages) * p.c.page_size) return DEV_ERR_PAGE;
     return 0;
 }
@@ -57,19 +59,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
     if (blockIdx.x == 0) {
         // both lists at once: units of the register kernels, row tiles of the tcgen05 kernel
         __shared__ int warp_tot[2][kPlanThreads / 32];
-        __shared__ int base_units[2];
+        __shared__ int warp_top[kPlanThreads / 32];
+        __shared__ int base_units[2], base_top;
         __shared__ uint32_t errors;
         if (threadIdx.x == 0) {
             base_units[0] = base_units[1] = 0;
+            base_top = INT32_MIN;
             errors = 0;
         }
         __syncthreads();
         for (int base = 0; base < p.N; base += kPlanThreads) {
             const int n = base + threadIdx.x;
+            // the running maximum of cu ahead of this sequence
+            int top = n < p.N ? p.cu[n] : INT32_MIN;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, top, o);
+                if (lane >= o) top = max(top, y);
+            }
+            if (lane == 31) warp_top[warp] = top;
+            int before = __shfl_up_sync(0xffffffffu, top, 1);
+            __syncthreads();
+            before = lane == 0 ? base_top : max(before, base_top);
+            for (int w = 0; w < warp; ++w) before = max(before, warp_top[w]);
             SeqInfo s{};
             int units[2] = {0, 0};
             if (n < p.N) {
-                const uint32_t err = seq_check(p, n, &s.t0, &s.nodes, &s.ctx);
+                const uint32_t err = seq_check(p, n, before, &s.t0, &s.nodes, &s.ctx);
                 if (err) atomicOr(&errors, err);
                 const int rows = s.nodes * p.G;
                 if (!err && rows > 0) {
@@ -115,6 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
             if (threadIdx.x == kPlanThreads - 1) {
                 base_units[0] = off[0] + upto[0];
                 base_units[1] = off[1] + upto[1];
+                base_top = max(before, top);
             }
             __syncthreads();
         }
@@ -130,10 +147,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
         }
         return;
     }
-    const int n = (blockIdx.x - 1) * (kPlanThreads / 32) + warp;
+    const int n0 = (blockIdx.x - 1) * (kPlanThreads / 32), n = n0 + warp;
+    int before = lane < warp && n0 + lane < p.N ? p.cu[n0 + lane] : INT32_MIN;
+    if (n0 > 0) {  // (the same for the whole CTA)
+        __shared__ int warp_top[kPlanThreads / 32];
+        int top = INT32_MIN;
+        for (int i = threadIdx.x; i < n0; i += kPlanThreads) top = max(top, p.cu[i]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) warp_top[warp] = top;
+        __syncthreads();
+        if (lane < kPlanThreads / 32) before = max(before, warp_top[lane]);
+    }
+    before = __reduce_max_sync(0xffffffffu, before);
     if (n >= p.N) return;
     int t0, m, ctx;
-    const bool ok = seq_check(p, n, &t0, &m, &ctx) == 0;
+    const bool ok = seq_check(p, n, before, &t0, &m, &ctx) == 0;
     if (!ok) m = 0;
     uint64_t mask[2];
     int up[2];

@@ -372,7 +372,10 @@ kda_status kda_replay_conv(float *state_pool, int64_t num_slots, const int32_t *
  * that follows the committed context (already sampled).  parent[i] is the local
  * index of a node's parent, 0 <= parent[i] < i (the root's entry is not read);
  * parent NULL means chains, parent[i] = i - 1.  cu_nodes [N+1] int32 on the device:
- * cu_nodes[0] = 0, non-decreasing, cu_nodes[N] <= the number of packed nodes.
+ * cu_nodes[0] = 0, non-decreasing, cu_nodes[N] <= the number of packed nodes.  Where it
+ * is not, a sequence whose own two entries are out of range or decrease, and (in
+ * kda_tree_attn) one that begins before an earlier entry, is reported as
+ * KDA_ERR_BAD_SEQLENS and left out; the others are worked on.
  */
 #define KDA_MAX_TREE_NODES 64
 
