@@ -15,17 +15,30 @@
 namespace kda {
 namespace {
 
-__global__ void clear_kernel(uint32_t *words) {
+// Words 0 and 1 become 0; word 2 says whether cu falls somewhere.  If it does, begins_low[n] (where given) says of each
+// sequence whether it begins below an earlier entry, that is, shares packed rows with another one.
+__global__ void check_kernel(uint32_t *words, const int32_t *cu, int N, uint64_t *begins_low) {
     spec::grid_go();
-    if (threadIdx.x < 2) words[threadIdx.x] = 0;
+    bool falls = false;
+    for (int i = threadIdx.x; i < N; i += blockDim.x) falls |= cu[i + 1] < cu[i];
+    falls = __syncthreads_or(falls);
+    if (threadIdx.x < 3) words[threadIdx.x] = threadIdx.x == 2 && falls ? 1u : 0u;
+    if (!falls || !begins_low) return;
+    __shared__ spec::RunningMax run;
+    run.begin();
+    for (int base = 0; base < N; base += blockDim.x) {
+        const int n = base + threadIdx.x, first = n < N ? cu[n] : INT32_MIN;
+        const int before = run.next(first, base / static_cast<int>(blockDim.x));
+        if (n < N) begins_low[n] = first < before;
+    }
 }
 
 }  // namespace
 
 namespace spec {
 
-bool clear_words(void *workspace, cudaStream_t s) {
-    clear_kernel<<<1, 32, 0, s>>>(static_cast<uint32_t *>(workspace));
+bool check_lengths(void *workspace, const int32_t *cu, int N, uint64_t *begins_low, cudaStream_t s) {
+    check_kernel<<<1, N > 2048 ? 1024 : 256, 0, s>>>(static_cast<uint32_t *>(workspace), cu, N, begins_low);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -89,7 +102,84 @@ struct CopySide {
     }
 };
 
+__device__ __forceinline__ CopySide key_side(const AppendParams &p, int64_t row, int64_t place, int64_t es) {
+    return CopySide{p.k + row * p.ks * 16, p.c.k + place, p.c.kh * es, p.Hkv << p.kshift, p.kshift};
+}
+__device__ __forceinline__ CopySide value_side(const AppendParams &p, int64_t row, int64_t place, int64_t es) {
+    return CopySide{p.v + row * p.vs * 16, p.c.v + place, p.c.vh * es, p.Hkv << p.vshift, p.vshift};
+}
+
+// Source row and place of token j of sequence n (row -1: not to be written), from a sequence without errors.
+__device__ __forceinline__ int64_t append_place(const AppendParams &p, const AppendSeq &s, int n, int64_t j, int64_t es, int64_t *place_k,
+                                                int64_t *place_v) {
+    const int64_t r = p.rows ? static_cast<int64_t>(p.rows[j]) : j, at = s.ctx + j - s.first;
+    const int64_t page = p.c.table[static_cast<int64_t>(n) * p.c.table_stride + at / p.c.page_size];
+    const int64_t slot = at % p.c.page_size;
+    const bool row_ok = r >= 0 && r < p.T_src, page_ok = page >= 0 && page < p.c.num_pages;
+    if (!row_ok || !page_ok) {
+        raise(p.status, row_ok ? DEV_ERR_PAGE : DEV_ERR_SLOT);
+        return -1;
+    }
+    *place_k = (page * p.c.kp + slot * p.c.kr) * es;
+    *place_v = (page * p.c.vp + slot * p.c.vr) * es;
+    return r;
+}
+
+// The whole call for a cu that falls somewhere: every CTA walks the sequences with the running maximum of cu and copies, a warp
+// per sequence, those of its own number.  A sequence that begins below an earlier entry is a bad one.
+__device__ __noinline__ void append_malformed(const AppendParams &p, int64_t es) {
+    __shared__ RunningMax run;
+    const int lane = threadIdx.x & 31;
+    run.begin();
+    for (int base = 0; base < p.N; base += kAppendThreads) {
+        const int n = base + threadIdx.x;
+        const int before = run.next(n < p.N ? p.cu[n] : INT32_MIN, base / kAppendThreads);
+        AppendSeq mine{0, 0, 0, DEV_ERR_SEQLENS};
+        if (n < p.N) {
+            mine = append_seq(p, n);
+            if (mine.first < before) mine.err = DEV_ERR_SEQLENS;
+            if (blockIdx.x == 0) {
+                if (mine.err) raise(p.status, mine.err);
+                if (p.new_len) p.new_len[n] = static_cast<int32_t>(mine.err ? mine.ctx : mine.ctx + mine.last - mine.first);
+            }
+        }
+        const int n0 = base + static_cast<int>(threadIdx.x) - lane;
+        for (int l = 0; l < 32 && n0 + l < p.N; ++l) {
+            const AppendSeq s{__shfl_sync(0xffffffffu, mine.first, l), __shfl_sync(0xffffffffu, mine.last, l),
+                              __shfl_sync(0xffffffffu, mine.ctx, l), __shfl_sync(0xffffffffu, mine.err, l)};
+            if (s.err || (n0 + l) % gridDim.x != blockIdx.x) continue;
+            for (int64_t j = s.first; j < s.last; ++j) {
+                int64_t place_k = 0, place_v = 0;
+                const int64_t r = append_place(p, s, n0 + l, j, es, &place_k, &place_v);
+                if (r < 0) continue;
+                const CopySide k = key_side(p, r, place_k, es), v = value_side(p, r, place_v, es);
+                for (int u0 = lane; u0 < k.units || u0 < v.units; u0 += 32 * kAppendUnroll) {
+                    uint4 x[kAppendUnroll];
+                    k.load(x, u0);
+                    k.store(x, u0);
+                    v.load(x, u0);
+                    v.store(x, u0);
+                }
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int64_t es) {
+    // A few lengths are looked over here, more of them by the kernel ahead.
+    bool falls;
+    if (p.N <= kAppendThreads) {
+        const int i = threadIdx.x;
+        falls = __syncthreads_or(i < p.N && p.cu[i + 1] < p.cu[i]);
+    } else {
+        grid_wait();
+        falls = __ldcg(p.status + 2) != 0;
+    }
+    if (falls) {
+        append_malformed(p, es);
+        grid_wait();
+        return;
+    }
     // new lengths, one thread per sequence
     const int64_t gid = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
     for (int64_t n = gid; n < p.N; n += static_cast<int64_t>(gridDim.x) * kAppendThreads) {
@@ -113,17 +203,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             if (s.err || j < s.first || j >= s.last) {
                 if (!s.err) raise(p.status, DEV_ERR_SEQLENS);
             } else {
-                const int64_t r = p.rows ? static_cast<int64_t>(p.rows[j]) : j, at = s.ctx + j - s.first;
-                const int64_t page = p.c.table[static_cast<int64_t>(n) * p.c.table_stride + at / p.c.page_size];
-                const int64_t slot = at % p.c.page_size;
-                const bool row_ok = r >= 0 && r < p.T_src, page_ok = page >= 0 && page < p.c.num_pages;
-                if (row_ok && page_ok) {
-                    row = r;
-                    place_k = (page * p.c.kp + slot * p.c.kr) * es;
-                    place_v = (page * p.c.vp + slot * p.c.vr) * es;
-                } else {
-                    raise(p.status, row_ok ? DEV_ERR_PAGE : DEV_ERR_SLOT);
-                }
+                row = append_place(p, s, n, j, es, &place_k, &place_v);
             }
         }
         __syncwarp();
@@ -131,8 +211,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             const int64_t r = __shfl_sync(0xffffffffu, row, i);
             const int64_t pk = __shfl_sync(0xffffffffu, place_k, i), pv = __shfl_sync(0xffffffffu, place_v, i);
             if (r < 0) continue;
-            const CopySide k{p.k + r * p.ks * 16, p.c.k + pk, p.c.kh * es, p.Hkv << p.kshift, p.kshift};
-            const CopySide v{p.v + r * p.vs * 16, p.c.v + pv, p.c.vh * es, p.Hkv << p.vshift, p.vshift};
+            const CopySide k = key_side(p, r, pk, es), v = value_side(p, r, pv, es);
             for (int u0 = lane; u0 < k.units || u0 < v.units; u0 += 32 * kAppendUnroll) {
                 uint4 x[kAppendUnroll], y[kAppendUnroll];
                 k.load(x, u0);
@@ -156,7 +235,7 @@ kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const
                             size_t ws_bytes, void *stream) {
     using namespace kda::spec;
     if (!dtype_ok(dtype) || !dim_ok(dk) || !dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
-    if (N < 0 || A_total < 0 || T_src < 0 || Hkv <= 0 || Hkv > 4096) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || N > 0x7fffffff - 1024 || A_total < 0 || T_src < 0 || Hkv <= 0 || Hkv > 4096) return KDA_ERR_INVALID_ARGUMENT;
     if (!workspace || !aligned_to(workspace, 16) || ws_bytes < KDA_WS_HEADER_BYTES) return KDA_ERR_WORKSPACE;
     Pages c;
     kda_status st = check_pages(cache, dtype, N, &c);
@@ -174,7 +253,7 @@ kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const
         return KDA_ERR_INVALID_ARGUMENT;
     if (new_len && new_len == cache->ctx_len) return KDA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!clear_words(workspace, s)) return KDA_ERR_CUDA;
+    if (!check_lengths(workspace, cu, N, nullptr, s)) return KDA_ERR_CUDA;
     if (N == 0) return KDA_OK;
     auto shift = [&](int d) { int b = 0; for (int u = d / vec; u > 1; u >>= 1) ++b; return b; };
     kda::AppendParams p{static_cast<const char *>(k), static_cast<const char *>(v), c, cu, rows, new_len, A_total, T_src,

@@ -115,9 +115,37 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // Lets the next grid in the stream begin (it waits for this one's end all the same).
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Clears the status word and the word behind it.  A kernel launched after it with the programmatic attribute begins once
-// everything before the clearing has ended; it waits (grid_wait) before it touches these words, and before it ends.
-bool clear_words(void *workspace, cudaStream_t s);
+// Clears the status word and the word behind it, and looks cu over: word 2 becomes 1 if it falls somewhere, else 0.  If it falls,
+// begins_low[n] (N entries, or null) says whether sequence n begins below an earlier entry.  A kernel launched after it with the
+// programmatic attribute begins once everything before this call has ended; it waits (grid_wait) before it touches these words,
+// and before it ends.
+bool check_lengths(void *workspace, const int32_t *cu, int N, uint64_t *begins_low, cudaStream_t s);
+
+// In shared memory: the maximum of all values that lower-numbered threads gave, and that all threads gave in earlier rounds.  For
+// whole CTAs of whole warps.
+struct RunningMax {
+    int warp_top[2][32], base[2];
+    __device__ __forceinline__ void begin() {
+        if (threadIdx.x == 0) base[0] = INT32_MIN;
+        __syncthreads();
+    }
+    __device__ __forceinline__ int next(int x, int round) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = round & 1;
+        int top = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, top, o);
+            if (lane >= o) top = max(top, y);
+        }
+        if (lane == 31) warp_top[b][warp] = top;
+        int before = __shfl_up_sync(0xffffffffu, top, 1);
+        __syncthreads();
+        before = lane == 0 ? base[b] : max(before, base[b]);
+        for (int w = 0; w < warp; ++w) before = max(before, warp_top[b][w]);
+        if (threadIdx.x == blockDim.x - 1) base[b ^ 1] = max(before, x);
+        return before;
+    }
+};
 
 // A page pool as the kernels see it (strides in elements).
 struct Pages {

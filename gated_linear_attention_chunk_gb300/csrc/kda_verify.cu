@@ -52,8 +52,8 @@ struct VerifyParams {
     int N, V;
     int nseg, seg_steps;     // segments of a row, kSegUnit-element steps of a segment
     int32_t *cu_accept, *rows, *next_token;
-    uint32_t *status;        // [0] status word, [1] ticket of finished sequences
-    uint64_t *accepted;      // [N] accepted nodes as bits
+    uint32_t *status;        // [0] status word, [1] ticket of finished sequences, [2] cu falls somewhere
+    uint64_t *accepted;      // [N] accepted nodes as bits; if cu falls, before that whether the sequence begins below an earlier entry
 };
 
 // Unevaluated sum of two floats, hi + lo.
@@ -275,7 +275,7 @@ struct Shared {
     double A, R, total;
     int32_t removed[kMaxNodes];
     uint64_t accepted;
-    int nremoved, cur, step, use_q;
+    int nremoved, cur, step, use_q, begins_low;
 };
 
 template <typename T, bool kDraft>
@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
             sh.step = (err || m == 0) ? kDone : kPassResidual;
             sh.nremoved = 0;
             sh.accepted = 0;
+            sh.begins_low = 0;
             is_last = false;
             if (rank == 0 && err) {
                 grid_wait();   // the status word has been cleared
@@ -341,8 +342,12 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     // publishes the accepted nodes and counts the sequence off: as soon as the walk has ended, beside the draw's pass
     const bool publisher = rank == 0 && threadIdx.x == 32;
     auto publish = [&] {
-        p.accepted[n] = sh.accepted;
-        grid_wait();           // the counter has been cleared
+        grid_wait();           // the counter has been cleared, the lengths have been checked
+        if (__ldcg(p.status + 2) && __ldcg(p.accepted + n)) {
+            sh.begins_low = 1;
+            atomicOr(p.status, DEV_ERR_SEQLENS);
+        }
+        p.accepted[n] = sh.begins_low ? 0ull : sh.accepted;
         __threadfence();
         is_last = atomicAdd(p.status + 1, 1u) == static_cast<uint32_t>(p.N) - 1;
         __threadfence();
@@ -374,10 +379,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
                 all += warp_tot[w];
             }
             if (i < p.N) {
-                // (overlapping ranges of a bad cu_nodes could count more than T nodes)
-                p.cu_accept[i + 1] = off + upto < p.T ? off + upto : static_cast<int32_t>(p.T);
+                p.cu_accept[i + 1] = off + upto;  // (good sequences share no nodes: at most T)
                 uint64_t b = bits;
-                for (int at = off + upto - mine; b && at < p.T; b &= b - 1, ++at)
+                for (int at = off + upto - mine; b; b &= b - 1, ++at)
                     p.rows[at] = static_cast<int32_t>(first) + __ffsll(static_cast<long long>(b)) - 1;
             }
             base_count = all;
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const VerifyPara
     // ---- the sequence's outputs; the last sequence to finish packs them all
     __syncwarp();
     cg_arrive();
-    if (rank == 0 && threadIdx.x == 0) p.next_token[n] = token;
+    if (rank == 0 && threadIdx.x == 0) p.next_token[n] = sh.begins_low ? -1 : token;  // (not published yet: no token anyway)
     if (publisher && !told) publish();
     if (rank == 0) {
         __syncthreads();
@@ -575,7 +579,8 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
                             static_cast<const void *>(rows), static_cast<const void *>(next_token)})
         if (!aligned_to(ptr, 4)) return KDA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!clear_words(workspace, s)) return KDA_ERR_CUDA;
+    uint64_t *accepted = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + KDA_WS_HEADER_BYTES);
+    if (!check_lengths(workspace, cu_nodes, N, accepted, s)) return KDA_ERR_CUDA;
     if (N == 0) {
         if (cudaMemsetAsync(cu_accept, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
         if (T > 0 && cudaMemsetAsync(rows, 0xff, static_cast<size_t>(T) * sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
@@ -586,7 +591,7 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
     p.u_accept = u_accept; p.u_sample = u_sample; p.T = T; p.ts = target_stride; p.ds = draft_stride;
     p.N = N; p.V = V; p.cu_accept = cu_accept; p.rows = rows; p.next_token = next_token;
     p.status = static_cast<uint32_t *>(workspace);
-    p.accepted = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + KDA_WS_HEADER_BYTES);
+    p.accepted = accepted;
     // a row may start up to 7 elements after a 16-byte boundary
     const int64_t steps = (static_cast<int64_t>(V) + 7 + kda::kSegUnit - 1) / kda::kSegUnit;
     p.seg_steps = static_cast<int>((steps + kda::kMaxSegs - 1) / kda::kMaxSegs);

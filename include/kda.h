@@ -373,9 +373,9 @@ kda_status kda_replay_conv(float *state_pool, int64_t num_slots, const int32_t *
  * index of a node's parent, 0 <= parent[i] < i (the root's entry is not read);
  * parent NULL means chains, parent[i] = i - 1.  cu_nodes [N+1] int32 on the device:
  * cu_nodes[0] = 0, non-decreasing, cu_nodes[N] <= the number of packed nodes.  Where it
- * is not, a sequence whose own two entries are out of range or decrease, and (in
- * kda_tree_attn) one that begins before an earlier entry, is reported as
- * KDA_ERR_BAD_SEQLENS and left out; the others are worked on.
+ * is not, a sequence whose own two entries are out of range or decrease, or that
+ * begins before an earlier entry, is reported as KDA_ERR_BAD_SEQLENS and left out;
+ * the others are worked on.
  */
 #define KDA_MAX_TREE_NODES 64
 
@@ -455,10 +455,11 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
  * drafted tree.  cu [N+1] as cu_nodes above; A_total >= cu[N] is the number of rows
  * given (the rest are not read).  k, v: T_src rows, strides as for kda_tree_attn.
  *   new_len  [N] int32 or NULL: ctx_len[n] + cu[n+1] - cu[n]; must not be ctx_len itself
- * Device errors: BAD_SEQLENS; BAD_PAGE (a sequence that does not fit its block table
- * keeps its length and writes nothing; a row whose page is outside the pool is not
- * written); BAD_SLOT (rows[j] outside [0, T_src): not written).  Two rows must not
- * name the same place.  workspace: >= KDA_WS_HEADER_BYTES.
+ * Device errors: BAD_SEQLENS, and BAD_PAGE for a sequence that does not fit its block
+ * table: such a sequence keeps its length and writes nothing.  BAD_PAGE for a row whose
+ * page is outside the pool and BAD_SLOT for rows[j] outside [0, T_src): that row is not
+ * written, but the others are and new_len counts it, so after these two errors the
+ * length covers a row that was never stored.  Two rows must not name the same place.  workspace: >= KDA_WS_HEADER_BYTES.
  */
 kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
                             const int32_t *cu, const int32_t *rows, int N, int64_t A_total, int64_t T_src, int Hkv,
