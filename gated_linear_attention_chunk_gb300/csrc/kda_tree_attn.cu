@@ -220,7 +220,7 @@ struct Walk {
 
     __device__ __forceinline__ void begin_unit() {
         key = split * chunk;
-        key_end = key + chunk < ctx ? key + chunk : ctx;
+        key_end = ctx - key < chunk ? ctx : key + chunk;  // (a context may end right below 2^31: nothing is added to a key past it)
         node = 0;
         node_end = split == nsplit - 1 ? nodes : 0;
     }
@@ -310,7 +310,7 @@ struct Ring {
         if (w.key < w.key_end) {
             kbase = p.c.k + w.head * w.heads * p.c.kh * es;
             vbase = p.c.v + w.head * w.heads * p.c.vh * es;
-            if (mine && w.key + j < w.key_end) {
+            if (mine && j < w.key_end - w.key) {
                 const int at = w.key + j, pg = at / p.c.page_size, slot = at - pg * p.c.page_size;
                 const int page = __ldg(p.c.table + static_cast<int64_t>(w.n) * p.c.table_stride + pg);
                 if (page >= 0 && page < p.c.num_pages) {
@@ -321,7 +321,7 @@ struct Ring {
                     *bad_seen = 1;
                 }
             }
-            w.key += per;
+            w.key = w.key_end - w.key < per ? w.key_end : w.key + per;
         } else {
             kbase = static_cast<const char *>(p.k) + static_cast<int64_t>(w.head) * w.heads * DK * es;
             vbase = static_cast<const char *>(p.v) + static_cast<int64_t>(w.head) * w.heads * DV * es;
@@ -538,7 +538,7 @@ __device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat1
         const bool drafted = cw.key >= cw.key_end;
         const int first = drafted ? cw.node : 0;
         const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;  // keys from here on
-        if (drafted) cw.node += R::kKeys; else cw.key += R::kKeys;
+        if (drafted) cw.node += R::kKeys; else cw.key = count < R::kKeys ? cw.key_end : cw.key + R::kKeys;
         const TileRow ahead = ring.begin_tile(p);
         const uint32_t ks = ptx::smem_u32(ring.stage()), vs = ks + R::kBytesK;
         // scores of 16 rows x NT * 8 keys
@@ -740,7 +740,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
         const bool drafted = cw.key >= cw.key_end;
         const int first = drafted ? cw.node : 0;
         const int count = drafted ? cw.node_end - cw.node : cw.key_end - cw.key;
-        if (drafted) cw.node += kStep; else cw.key += kStep;
+        if (drafted) cw.node += kStep; else cw.key = count < kStep ? cw.key_end : cw.key + kStep;
         const TileRow ahead = ring.begin_tile(p);
         const char *ks = ring.stage(), *vs = ks + R::kBytesK;
         float s[NT][4];

@@ -72,14 +72,16 @@ __host__ __device__ inline int splits_of(int64_t ctx, int least, int Hkv, int ti
     const int64_t s = some < one ? some : one, t = many < three ? many : three;
     return static_cast<int>(s > t ? (s < 1 ? 1 : s) : (t < 1 ? 1 : t));
 }
+// Keys of each of s parts, a multiple of `unit` (but for one part of a context that ends right below 2^31).
+__host__ __device__ inline int chunk_of(int ctx, int s, int unit) {
+    const int c = ctx > 0 ? (ctx - 1) / s + 1 : 1;
+    return c > 0x7fffffff - unit ? 0x7fffffff : (c + unit - 1) / unit * unit;
+}
 __host__ __device__ inline void split_of(int ctx, int rows, int Hkv, int tiles, bool wide, int *nsplit, int *chunk) {
     const int heads = heads_of(rows, Hkv, wide);
     const int s = splits_of(ctx, least_chunk(rows, wide, heads), Hkv / heads, tiles);
-    int c = (ctx + s - 1) / s;
-    c = (c + 63) / 64 * 64;
-    if (c < 64) c = 64;
-    *chunk = c;
-    *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
+    *chunk = chunk_of(ctx, s, 64);
+    *nsplit = ctx > 0 ? (ctx - 1) / *chunk + 1 : 1;
 }
 __host__ __device__ inline int tiles_of(int rows) { return (rows + kTileRows - 1) / kTileRows; }
 
@@ -96,11 +98,8 @@ __host__ __device__ inline int tc_splits_of(int64_t ctx, int Hkv, int groups) {
 }
 __host__ __device__ inline void tc_split_of(int ctx, int Hkv, int tiles, int *nsplit, int *chunk) {
     const int s = tc_splits_of(ctx, Hkv, tc_groups_of(tiles));
-    int c = (ctx + s - 1) / s;
-    c = (c + kTcKeys - 1) / kTcKeys * kTcKeys;
-    if (c < kTcKeys) c = kTcKeys;
-    *chunk = c;
-    *nsplit = ctx > 0 ? (ctx + c - 1) / c : 1;
+    *chunk = chunk_of(ctx, s, kTcKeys);
+    *nsplit = ctx > 0 ? (ctx - 1) / *chunk + 1 : 1;
 }
 
 // Partial results of the tcgen05 kernel, by the row tile's number in info_tc's order; a tile alone leaves two per part.

@@ -89,3 +89,19 @@ def test_overlapping_trees_stay_inside_the_workspace(kda):
     assert status == kda.KDA_ERR_BAD_SEQLENS
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert bool((whole[need:] == 0xa5).all())
+
+
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+@pytest.mark.parametrize("ctx", [2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 70])
+def test_context_right_below_the_limit(kda, dtype, ctx):
+    """One cache row read 2^31 - 1 times (a row stride of zero): equal scores, so o is the value and lse the score plus the
+    logarithm of the number of keys.  A part left out would change that by 2e-3; 456 parts of exact counts are summed with rounding."""
+    Hkv, d = 1, 64
+    row = lambda x: torch.full((1, 1, Hkv, d), x, dtype=dtype, device="cuda").expand(1, ctx, Hkv, d)  # noqa: E731
+    q, k, v = (torch.full((1, 1, d), x, dtype=dtype, device="cuda") for x in (0.5, 0.25, 2.0))
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(kda.kda_tree_attn_workspace_size(1, 1, 1, Hkv, d, 1, ctx), dtype=torch.uint8, device="cuda")
+    o, lse = kda.kda_tree_attn(q, k, v, row(0.25), row(2.0), ints(0).view(1, 1), ints(ctx), ints(0, 1), max_nodes=1, workspace=ws)
+    assert kda.kda_device_status(ws) == kda.KDA_OK
+    assert np.abs(ref.np64(lse) - (1.0 + np.log(ctx + 1.0))).max() <= 456 * 2.0 ** -24 + 22 * 2.0 ** -22
+    assert np.abs(ref.np64(o) - 2.0).max() <= 2.0 * (912 * 2.0 ** -24 + ref.HALF_STEP[dtype])
