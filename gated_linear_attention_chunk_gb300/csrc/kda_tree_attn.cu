@@ -52,8 +52,10 @@ __device__ __forceinline__ uint32_t seq_check(const AttnParams &p, int n, int be
 
 constexpr int kPlanThreads = 256;
 
-// CTA 0: the list of sequences and units, and the status word.  The others, a warp per sequence: masks.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) {
+// CTA 0: the list of sequences and units, and the status word.  The next seq_ctas, a warp per sequence: masks.  The others, a warp
+// per packed node: the finite copy of its values.
+template <typename T>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p, int seq_ctas, int dv) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_go();
     if (blockIdx.x == 0) {
@@ -145,6 +147,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p) 
             }
             *p.status = errors;
         }
+        return;
+    }
+    if (blockIdx.x > seq_ctas) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x - 1 - seq_ctas) * (kPlanThreads / 32) + warp;
+        if (t >= p.T) return;
+        if (t >= p.cu[p.N]) {  // not to be read, unless cu falls and an earlier sequence has the node
+            int top = 0;
+            for (int i = lane; i < p.N; i += 32) top = max(top, p.cu[i]);
+            if (t >= __reduce_max_sync(0xffffffffu, top)) return;
+        }
+        const int units = p.Hkv * dv / Elem<T>::kVec;
+        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.given_v) + t * p.given_vs);
+        uint4 *to = reinterpret_cast<uint4 *>(const_cast<void *>(p.v)) + t * units;
+        bool odd = false;
+#pragma unroll 4
+        for (int u = lane; u < units; u += 32) to[u] = finite_only<T>(from[u], odd);
+        odd = __any_sync(0xffffffffu, odd);
+        if (lane == 0) p.odd[t] = odd;
         return;
     }
     const int n0 = (blockIdx.x - 1) * (kPlanThreads / 32), n = n0 + warp;
@@ -950,7 +970,7 @@ __global__ void __launch_bounds__(Ring<T, DK, DV>::kThreads, Ring<T, DK, DV>::kP
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// The parts of a row (node, query head) joined: four sums of every fourth part, added in order.  kWarps = 1: a warp has all
+// The last kernel: the parts of a row (node, query head) joined, and what its nodes' values that are not finite add to it.  Joined: four sums of every fourth part, added in order.  kWarps = 1: a warp has all
 // four; 4: a warp each, where there are few rows (one warp per row took 28 us for 256 rows of 114 parts).  A lane has DV / 32 columns.
 // ---------------------------------------------------------------------------------------------------------------
 template <typename T, int DV, int kWarps>
@@ -967,8 +987,36 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
     if (n < 0 || n >= p.N) return;
     const SeqInfo s = p.info[n];
     if (s.nsplit < 1 || t < s.t0 || t >= s.t0 + s.nodes || p.bad[n]) return;
+    uint64_t odd = 0;  // nodes that the row sees and whose values are not all finite
+    if (p.odd) {
+        const uint64_t sees = p.sees[t];
+        const bool low = ((sees >> lane) & 1) && p.odd[s.t0 + lane], high = ((sees >> (lane + 32)) & 1) && p.odd[s.t0 + lane + 32];
+        odd = (static_cast<uint64_t>(__ballot_sync(0xffffffffu, high)) << 32) | __ballot_sync(0xffffffffu, low);
+    }
+    T *to = static_cast<T *>(p.o) + row * DV + lane * VL;
+    auto add_odd = [&](float (&x)[VL]) {
+        const int64_t column = (row - t * p.Hq) / p.G * DV + lane * VL;
+        for (; odd; odd &= odd - 1) {
+            const T *src = static_cast<const T *>(p.given_v) + (s.t0 + __ffsll(static_cast<long long>(odd)) - 1) * p.given_vs + column;
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+                const float v = Elem<T>::to_f(src[i]);
+                if (!(fabsf(v) < INFINITY)) x[i] += v;
+            }
+        }
+    };
     const int parts = s.nsplit;
-    if (parts == 1 || (p.tc && s.nodes * p.G > kTcLeast)) return;
+    if (parts == 1 || (p.tc && s.nodes * p.G > kTcLeast)) {  // complete but for those
+        if (odd && (kWarps == 1 || warp == 0)) {
+            float x[VL];
+#pragma unroll
+            for (int i = 0; i < VL; ++i) x[i] = Elem<T>::to_f(to[i]);
+            add_odd(x);
+#pragma unroll
+            for (int i = 0; i < VL; ++i) to[i] = Elem<T>::from_f(x[i]);
+        }
+        return;
+    }
     const float2 *ml = p.part_ml + row * p.max_splits;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[i].x);
@@ -1012,9 +1060,11 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
         sum = (l[0] + l[1]) + (l[2] + l[3]);
     }
     const float inv = 1.f / sum;
-    T *to = static_cast<T *>(p.o) + row * DV + lane * VL;
 #pragma unroll
-    for (int x = 0; x < VL; ++x) to[x] = Elem<T>::from_f(out[x] * inv);
+    for (int x = 0; x < VL; ++x) out[x] *= inv;
+    if (odd) add_odd(out);
+#pragma unroll
+    for (int x = 0; x < VL; ++x) to[x] = Elem<T>::from_f(out[x]);
     if (p.lse && lane == 0) p.lse[row] = (m + log2f(sum)) * kLn2;
 }
 
@@ -1032,7 +1082,7 @@ cudaError_t launch_combine(const AttnParams &p, cudaStream_t s) {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct AttnLayout {
-    size_t info, info_tc, bad, seq_of, sees, part_ml, part_o, tc_ml, tc_o, total;
+    size_t info, info_tc, bad, seq_of, sees, odd, copy_v, part_ml, part_o, tc_ml, tc_o, total;
     int max_splits, max_tiles;
     int64_t units;               // at most so many in either list (tcgen05: row tiles times parts)
 };
@@ -1048,6 +1098,8 @@ AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, i
     l.bad = take(static_cast<size_t>(N) * 4);
     l.seq_of = take(static_cast<size_t>(T) * 4);
     l.sees = take(static_cast<size_t>(T) * 8);
+    l.odd = take(static_cast<size_t>(T) * 4);
+    l.copy_v = take(max_nodes > 1 ? static_cast<size_t>(T) * Hkv * dv * sizeof(float) : 0);
     const size_t parts = l.max_splits > 1 ? static_cast<size_t>(T) * Hq * l.max_splits : 0;
     l.part_ml = take(parts * sizeof(float2));
     l.part_o = take(parts * dv * sizeof(float));
@@ -1077,7 +1129,10 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
     const int sms = sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
     const int64_t seq_ctas = (static_cast<int64_t>(p.N) + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
-    plan_kernel<<<static_cast<unsigned>(1 + seq_ctas), kPlanThreads, 0, s>>>(p);
+    const int64_t node_ctas = p.odd ? (p.T + kPlanThreads / 32 - 1) / (kPlanThreads / 32) : 0;
+    const unsigned plan_ctas = static_cast<unsigned>(1 + seq_ctas + node_ctas);
+    if (dtype == KDA_BF16) plan_kernel<__nv_bfloat16><<<plan_ctas, kPlanThreads, 0, s>>>(p, static_cast<int>(seq_ctas), DV);
+    else plan_kernel<float><<<plan_ctas, kPlanThreads, 0, s>>>(p, static_cast<int>(seq_ctas), DV);
     const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * (p.tc ? 1 : max_tiles);
     const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? Ring<__nv_bfloat16, DK, DV>::kPerSm : Ring<float, DK, DV>::kPerSm);
     const dim3 grid(static_cast<unsigned>(units < most ? units : most));
@@ -1093,7 +1148,7 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
         if (!smem_opt_in<attn_kernel<float, DK, DV>>(smem)) return KDA_ERR_CUDA;
         if (launch_after(attn_kernel<float, DK, DV>, grid, R::kThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
     }
-    if (p.max_splits > 1 && (dtype == KDA_BF16 ? launch_combine<__nv_bfloat16, DV>(p, s) : launch_combine<float, DV>(p, s)) != cudaSuccess)
+    if ((p.max_splits > 1 || p.odd) && (dtype == KDA_BF16 ? launch_combine<__nv_bfloat16, DV>(p, s) : launch_combine<float, DV>(p, s)) != cudaSuccess)
         return KDA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -1154,6 +1209,13 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     p.bad = reinterpret_cast<uint32_t *>(ws + l.bad);
     p.seq_of = reinterpret_cast<int32_t *>(ws + l.seq_of);
     p.sees = reinterpret_cast<uint64_t *>(ws + l.sees);
+    if (max_nodes > 1) {
+        p.given_v = v;
+        p.given_vs = v_stride;
+        p.v = ws + l.copy_v;
+        p.vs = static_cast<int64_t>(Hkv) * dv;
+        p.odd = reinterpret_cast<int32_t *>(ws + l.odd);
+    }
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
     p.tc_ml = reinterpret_cast<float2 *>(ws + l.tc_ml);

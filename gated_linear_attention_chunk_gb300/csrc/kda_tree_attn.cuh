@@ -26,7 +26,7 @@ struct __align__(16) SeqInfo {
 };
 
 struct AttnParams {
-    const void *q, *k, *v;
+    const void *q, *k, *v;       // v: the drafted nodes' values, in a batch of trees the finite copy of them
     void *o;
     float *lse;
     Pages c;
@@ -41,6 +41,12 @@ struct AttnParams {
     uint32_t *bad;               // [N] a page or a parent of the sequence is not valid
     int32_t *seq_of;             // [T] sequence of a packed node
     uint64_t *sees;              // [T] ancestors of a packed node, itself included
+    // Trees of more than one node: a tile holds drafted values that some of its rows do not see, and a weight of zero does not take an
+    // infinity or NaN out of a product.  So the tiles are made of a copy with zeros in the place of such values (v, vs), and
+    // combine_kernel, the last one, adds them to the rows that do see them.
+    const void *given_v;
+    int64_t given_vs;
+    int32_t *odd;                // [T] a packed node has such values; null in a batch of single nodes, which has no copy
     float *part_o;               // [T, Hq, max_splits, dv]
     float2 *part_ml;             // [T, Hq, max_splits] maximum (base 2) and sum
     float *tc_o;                 // tcgen05 kernel's parts: [part][dv / 4][kTcRows] of 4 columns
@@ -112,6 +118,20 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 16 bytes of T without what is not finite; `odd` becomes true if there was such a value.
+template <typename T>
+__device__ __forceinline__ uint4 finite_only(uint4 x, bool &odd) {
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool high = (w[i] & 0x7f800000u) == 0x7f800000u, low = sizeof(T) == 2 && (w[i] & 0x7f80u) == 0x7f80u;
+        odd |= high || low;
+        if (high) w[i] = sizeof(T) == 2 ? w[i] & 0xffffu : 0u;
+        if (low) w[i] &= 0xffff0000u;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

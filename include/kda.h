@@ -436,6 +436,7 @@ typedef struct kda_paged_kv {
  *          cu_nodes[N] on are not read, and their outputs not written.
  * dk, dv each 64 or 128; page_size * max_pages < 2^31.  Scores, softmax and sums are fp32; for bf16 the weights are
  * rounded to bf16 before they meet the values (fp32 inputs: products in three tf32 terms, about 22 bits).
+ * A node's infinities and NaN reach the rows that see the node, and no others.
  * Long contexts are cut into parts that run concurrently and are joined in a fixed
  * order; the cut goes by a sequence's own length and tree, so its bits do not depend
  * on the batch.  A sequence with a device error (BAD_SEQLENS, BAD_PAGE, BAD_TREE)

@@ -105,3 +105,66 @@ def test_context_right_below_the_limit(kda, dtype, ctx):
     assert kda.kda_device_status(ws) == kda.KDA_OK
     assert np.abs(ref.np64(lse) - (1.0 + np.log(ctx + 1.0))).max() <= 456 * 2.0 ** -24 + 22 * 2.0 ** -22
     assert np.abs(ref.np64(o) - 2.0).max() <= 2.0 * (912 * 2.0 ** -24 + ref.HALF_STEP[dtype])
+
+
+ODD = [  # nodes, contexts, G, Hkv, dk, dv: the register kernels' row groups, four heads per CTA (fp32), one and several row tiles, parts
+    ([6], [0], 1, 1, 64, 64),
+    ([5, 9, 1], [70, 1400, 3], 2, 4, 64, 128),
+    ([13, 4], [900, 33], 2, 3, 128, 64),
+    ([40, 7], [200, 2100], 1, 2, 128, 128),
+    ([64, 11], [1300, 5], 8, 1, 128, 128),
+    ([33], [5000], 8, 2, 64, 64),
+]
+
+
+@pytest.mark.parametrize("shape", ODD, ids=range(len(ODD)))
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+def test_values_that_a_row_does_not_see(kda, shape, dtype):
+    """Infinities and NaN in a drafted node's key and value: rows that do not see the node are what they are without them, rows that
+    do have the infinity, or NaN, in that column (a key of NaN makes all of the row NaN)."""
+    c = _case(*shape, 16, dtype, True, seed=len(shape[0]))
+    nodes, _, G, Hkv, _, dv = shape
+    cu = c["cu"].tolist()
+    want_o, want_lse, status = _run(kda, c)
+    assert status == kda.KDA_OK
+    _check(c, want_o, want_lse)
+    f = dict(c, k=c["k"].clone(), v=c["v"].clone())
+    want_o, want_lse = want_o.cpu(), want_lse.cpu()
+    n = int(np.argmax(nodes))
+    sees = ref.ancestors([-1] + c["parent"][cu[n] + 1:cu[n + 1]].tolist())
+    marks = [(nodes[n] - 1, 0, 3, float("inf")), (nodes[n] - 2, Hkv - 1, dv - 1, -float("inf")), (1, Hkv - 1, 0, float("nan")),
+             (nodes[n] // 2, 0, 9, float("inf")), (2, 0, 9, -float("inf"))]
+    for node, head, column, x in marks:
+        f["v"][cu[n] + node, head, column] = x
+    lost = nodes[n] - 1
+    f["k"][cu[n] + lost, Hkv - 1] = float("nan")
+    for i in range(nodes[n]):
+        for head in range(Hkv):
+            for column in range(dv):
+                xs = [x for node, h, col, x in marks if h == head and col == column and sees[i, node]]
+                if xs:
+                    want_o[cu[n] + i, head * G:(head + 1) * G, column] = sum(xs)  # (both infinities: NaN)
+            if head == Hkv - 1 and sees[i, lost]:
+                want_o[cu[n] + i, head * G:(head + 1) * G] = float("nan")
+                want_lse[cu[n] + i, head * G:(head + 1) * G] = float("nan")
+    o, lse, status = _run(kda, f)
+    assert status == kda.KDA_OK
+    assert torch.equal(torch.nan_to_num(o.cpu(), nan=77.0, posinf=88.0, neginf=99.0),
+                       torch.nan_to_num(want_o, nan=77.0, posinf=88.0, neginf=99.0))
+    assert torch.equal(torch.nan_to_num(lse.cpu(), nan=77.0), torch.nan_to_num(want_lse, nan=77.0))
+
+
+@pytest.mark.parametrize("dtype,nodes,G", [(ref.BF16, 4, 2), (ref.BF16, 40, 4), (ref.F32, 7, 2)])
+def test_a_drafted_branch_changes_nothing_before_it(kda, dtype, nodes, G):
+    """A chain's last node is all NaN: the nodes before it, and the other sequences, keep their bits."""
+    c = _case([3, nodes, 2], [100, 300, 0], G, 4, 128, 128, 16, dtype, False, seed=6)
+    want_o, want_lse, _ = _run(kda, c)
+    last = 3 + nodes - 1
+    f = dict(c, **{key: c[key].clone() for key in "qkv"})
+    for key in "qkv":
+        f[key][last] = float("nan")
+    o, lse, status = _run(kda, f)
+    assert status == kda.KDA_OK
+    keep = [i for i in range(nodes + 5) if i != last]
+    assert torch.equal(o[keep], want_o[keep]) and torch.equal(lse[keep], want_lse[keep])
+    assert bool(o[last].isnan().all()) and bool(lse[last].isnan().all())
