@@ -59,13 +59,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_go();
     if (blockIdx.x == 0) {
-        // both lists at once: units of the register kernels, row tiles of the tcgen05 kernel
-        __shared__ int warp_tot[2][kPlanThreads / 32];
+        // both lists at once: units of the register kernels, row tiles of the tcgen05 kernel; and the rows of partial results
+        __shared__ int warp_tot[3][kPlanThreads / 32];
         __shared__ int warp_top[kPlanThreads / 32];
-        __shared__ int base_units[2], base_top;
+        __shared__ int base_units[3], base_top;
         __shared__ uint32_t errors;
         if (threadIdx.x == 0) {
-            base_units[0] = base_units[1] = 0;
+            base_units[0] = base_units[1] = base_units[2] = 0;
             base_top = INT32_MIN;
             errors = 0;
         }
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p, 
             before = lane == 0 ? base_top : max(before, base_top);
             for (int w = 0; w < warp; ++w) before = max(before, warp_top[w]);
             SeqInfo s{};
-            int units[2] = {0, 0};
+            int units[3] = {0, 0, 0};
             if (n < p.N) {
                 const uint32_t err = seq_check(p, n, before, &s.t0, &s.nodes, &s.ctx);
                 if (err) atomicOr(&errors, err);
@@ -100,28 +100,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p, 
                         split_of(s.ctx, rows, p.Hkv, s.tiles, p.wide, &s.nsplit, &s.chunk);
                         units[0] = s.nsplit * s.tiles * (p.Hkv / heads_of(rows, p.Hkv, p.wide));
                     }
+                    units[2] = static_cast<int>(part_rows(p.tc, s.nodes, p.Hq, p.Hkv, s.nsplit));
                 }
             }
-            int upto[2] = {units[0], units[1]};
+            int upto[3] = {units[0], units[1], units[2]};
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y0 = __shfl_up_sync(0xffffffffu, upto[0], o), y1 = __shfl_up_sync(0xffffffffu, upto[1], o);
-                if (lane >= o) {
-                    upto[0] += y0;
-                    upto[1] += y1;
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto[x], o);
+                    if (lane >= o) upto[x] += y;
                 }
-            }
             if (lane == 31) {
-                warp_tot[0][warp] = upto[0];
-                warp_tot[1][warp] = upto[1];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) warp_tot[x][warp] = upto[x];
             }
             __syncthreads();
-            int off[2] = {base_units[0], base_units[1]};
-            for (int w = 0; w < warp; ++w) {
-                off[0] += warp_tot[0][w];
-                off[1] += warp_tot[1][w];
-            }
+            int off[3] = {base_units[0], base_units[1], base_units[2]};
+            for (int w = 0; w < warp; ++w)
+#pragma unroll
+                for (int x = 0; x < 3; ++x) off[x] += warp_tot[x][w];
             if (n < p.N) {
+                s.part0 = off[2] + upto[2] - units[2];
                 s.unit0 = off[0] + upto[0] - units[0];
                 p.info[n] = s;
                 if (p.tc) {
@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnParams p, 
             }
             __syncthreads();
             if (threadIdx.x == kPlanThreads - 1) {
-                base_units[0] = off[0] + upto[0];
-                base_units[1] = off[1] + upto[1];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) base_units[x] = off[x] + upto[x];
                 base_top = max(before, top);
             }
             __syncthreads();
@@ -658,7 +658,7 @@ __device__ __forceinline__ void unit_bf16(const AttnParams &p, Ring<__nv_bfloat1
                 }
             if (p.lse && first_lane) p.lse[row] = (mx[i] + log2f(sum[i])) * kLn2;
         } else {
-            const int64_t at = row * p.max_splits + split;
+            const int64_t at = __ldg(&p.info[n].part0) + (row - static_cast<int64_t>(t0) * p.Hq) * nsplit + split;
             float2 *to = reinterpret_cast<float2 *>(p.part_o + at * DV + two);
 #pragma unroll
             for (int part = 0; part < KW; ++part)
@@ -907,7 +907,7 @@ __device__ __forceinline__ void unit_f32(const AttnParams &p, Ring<float, DK, DV
         if (!live[i] || !ok) continue;
         const int64_t row = static_cast<int64_t>(t0 + node[i]) * p.Hq + hq[i];
         const bool whole = nsplit == 1;
-        const int64_t at = row * p.max_splits + split_no;
+        const int64_t at = whole ? 0 : __ldg(&p.info[n].part0) + (row - static_cast<int64_t>(t0) * p.Hq) * nsplit + split_no;
         const float f = whole ? 1.f / sum[i] : 1.f;
         float *to = (whole ? static_cast<float *>(p.o) + row * DV : p.part_o + at * DV) + 8 * j4;
 #pragma unroll
@@ -1017,14 +1017,15 @@ __global__ void __launch_bounds__(kAttnThreads) combine_kernel(const AttnParams 
         }
         return;
     }
-    const float2 *ml = p.part_ml + row * p.max_splits;
+    const int64_t part0 = s.part0 + (row - static_cast<int64_t>(s.t0) * p.Hq) * parts;
+    const float2 *ml = p.part_ml + part0;
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[i].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float base = m == -INFINITY ? 0.f : m;
     float l[kSums] = {}, o[kSums][VL] = {};
-    const float *src = p.part_o + row * p.max_splits * DV + lane * VL;
+    const float *src = p.part_o + part0 * DV + lane * VL;
     const int first = kWarps == 4 ? warp : 0;
 #pragma unroll 4
     for (int i0 = first; i0 < parts; i0 += 4)
@@ -1082,50 +1083,71 @@ cudaError_t launch_combine(const AttnParams &p, cudaStream_t s) {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct AttnLayout {
-    size_t info, info_tc, bad, seq_of, sees, odd, copy_v, part_ml, part_o, tc_ml, tc_o, total;
-    int max_splits, max_tiles;
+    size_t info, info_tc, bad, seq_of, sees, odd, copy_v, part_ml, part_o, total;
+    int max_nodes;               // of a tree that T nodes can hold
+    bool tc, parts;              // some tree is for the tcgen05 kernel; some sequence can have more than one part
     int64_t units;               // at most so many in either list (tcgen05: row tiles times parts)
+    int64_t part_rows;           // at most so many rows of partial results
 };
-AttnLayout layout_of(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
+// The most that any batch of N trees of T nodes in all can ask for, each over a context of up to max_ctx rows.
+AttnLayout layout_of(kda_dtype dtype, int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
     AttnLayout l{};
-    // a sequence of few rows has the most parts; G rows are the fewest
-    l.max_tiles = tiles_of(max_nodes * (Hq / Hkv));
-    l.max_splits = splits_of(max_ctx, 128, Hkv % 4 == 0 ? Hkv / 4 : Hkv, 1);  // (no sequence has smaller parts)
+    const bool wide = dtype == KDA_F32;
+    const int G = Hq / Hkv;
+    if (max_nodes > T) max_nodes = static_cast<int>(T < 1 ? 1 : T);
+    l.max_nodes = max_nodes;
+    l.tc = !wide && max_nodes * G > kTcLeast;
+    // By a tree's size: its rows of partial results (a cut has no more parts over a shorter context).
+    int64_t rows_of[KDA_MAX_TREE_NODES + 1] = {}, most_units = 0;
+    int least = 1, best = 1;     // the largest tree of the register kernels; the one of most rows per node
+    for (int m = 1; m <= max_nodes; ++m) {
+        const int rows = m * G;
+        int splits;
+        int64_t units;
+        if (!wide && rows > kTcLeast) {
+            splits = tc_splits_of(max_ctx, Hkv, tc_groups_of(tc_tiles_of(rows)));
+            units = static_cast<int64_t>(splits) * tc_tiles_of(rows) * Hkv;
+        } else {
+            const int heads = heads_of(rows, Hkv, wide);
+            splits = splits_of(max_ctx, least_chunk(rows, wide, heads), Hkv / heads, tiles_of(rows));
+            units = static_cast<int64_t>(splits) * tiles_of(rows) * (Hkv / heads);
+            least = m;
+        }
+        l.parts |= splits > 1;
+        rows_of[m] = part_rows(l.tc, m, Hq, Hkv, splits);
+        if (units > most_units) most_units = units;
+        if (rows_of[m] * best > rows_of[best] * m) best = m;
+    }
+    l.units = most_units * N;
+    // For any price of a node, no batch has more rows than the price of all nodes and, for each tree, what the best size has over it.
+    l.part_rows = INT64_MAX;
+    const int next = least < max_nodes ? least + 1 : least;
+    const int64_t prices[] = {0, (rows_of[best] + best - 1) / best, (rows_of[least] + least - 1) / least, (rows_of[next] + next - 1) / next,
+                              (rows_of[max_nodes] + max_nodes - 1) / max_nodes};
+    for (const int64_t price : prices) {
+        int64_t over = 0;
+        for (int m = 1; m <= max_nodes; ++m)
+            if (rows_of[m] - price * m > over) over = rows_of[m] - price * m;
+        const int64_t rows = price * T + over * N;
+        if (rows < l.part_rows) l.part_rows = rows;
+    }
     size_t off = KDA_WS_HEADER_BYTES;
     auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
     l.info = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
-    l.info_tc = take((static_cast<size_t>(N) + 1) * sizeof(SeqInfo));
+    l.info_tc = take(l.tc ? (static_cast<size_t>(N) + 1) * sizeof(SeqInfo) : 0);
     l.bad = take(static_cast<size_t>(N) * 4);
     l.seq_of = take(static_cast<size_t>(T) * 4);
     l.sees = take(static_cast<size_t>(T) * 8);
     l.odd = take(static_cast<size_t>(T) * 4);
     l.copy_v = take(max_nodes > 1 ? static_cast<size_t>(T) * Hkv * dv * sizeof(float) : 0);
-    const size_t parts = l.max_splits > 1 ? static_cast<size_t>(T) * Hq * l.max_splits : 0;
-    l.part_ml = take(parts * sizeof(float2));
-    l.part_o = take(parts * dv * sizeof(float));
-    // the tcgen05 kernel's: every row tile (at most one not full per sequence) in each part, twice
-    size_t tc = 0;
-    l.units = static_cast<int64_t>(N) * Hkv * l.max_splits * l.max_tiles;
-    const int64_t rows = max_nodes * static_cast<int64_t>(Hq / Hkv);
-    if (rows > kTcLeast) {
-        // (fewer row groups make the number of parts that fill the GPU larger: one group has the most)
-        int s = 1;
-        for (int g = 1; g <= tc_groups_of(tc_tiles_of(static_cast<int>(rows))); ++g) {
-            const int x = tc_splits_of(max_ctx, Hkv, g);
-            if (x > s) s = x;
-        }
-        const int64_t tiles = (T * (Hq / Hkv) / kTcRows + N) * Hkv * s;
-        if (tiles > l.units) l.units = tiles;
-        tc = static_cast<size_t>(tiles) * 2;
-    }
-    l.tc_ml = take(tc * kTcRows * sizeof(float2));
-    l.tc_o = take(tc * kTcRows * dv * sizeof(float));
+    l.part_ml = take(static_cast<size_t>(l.part_rows) * sizeof(float2));
+    l.part_o = take(static_cast<size_t>(l.part_rows) * dv * sizeof(float));
     l.total = off;
     return l;
 }
 
 template <int DK, int DV>
-kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cudaStream_t s) {
+kda_status launch_attn(const AttnParams &p, kda_dtype dtype, const AttnLayout &l, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
     const int64_t seq_ctas = (static_cast<int64_t>(p.N) + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
@@ -1133,9 +1155,8 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
     const unsigned plan_ctas = static_cast<unsigned>(1 + seq_ctas + node_ctas);
     if (dtype == KDA_BF16) plan_kernel<__nv_bfloat16><<<plan_ctas, kPlanThreads, 0, s>>>(p, static_cast<int>(seq_ctas), DV);
     else plan_kernel<float><<<plan_ctas, kPlanThreads, 0, s>>>(p, static_cast<int>(seq_ctas), DV);
-    const int64_t units = static_cast<int64_t>(p.N) * p.Hkv * p.max_splits * (p.tc ? 1 : max_tiles);
     const int64_t most = static_cast<int64_t>(sms) * (dtype == KDA_BF16 ? Ring<__nv_bfloat16, DK, DV>::kPerSm : Ring<float, DK, DV>::kPerSm);
-    const dim3 grid(static_cast<unsigned>(units < most ? units : most));
+    const dim3 grid(static_cast<unsigned>(l.units < most ? l.units : most));
     if (dtype == KDA_BF16) {
         using R = Ring<__nv_bfloat16, DK, DV>;
         constexpr int smem = R::kStages * R::kStage;
@@ -1148,7 +1169,7 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
         if (!smem_opt_in<attn_kernel<float, DK, DV>>(smem)) return KDA_ERR_CUDA;
         if (launch_after(attn_kernel<float, DK, DV>, grid, R::kThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
     }
-    if ((p.max_splits > 1 || p.odd) && (dtype == KDA_BF16 ? launch_combine<__nv_bfloat16, DV>(p, s) : launch_combine<float, DV>(p, s)) != cudaSuccess)
+    if ((l.parts || p.odd) && (dtype == KDA_BF16 ? launch_combine<__nv_bfloat16, DV>(p, s) : launch_combine<float, DV>(p, s)) != cudaSuccess)
         return KDA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -1158,11 +1179,17 @@ kda_status launch_attn(const AttnParams &p, kda_dtype dtype, int max_tiles, cuda
 
 extern "C" {
 
-size_t kda_tree_attn_workspace_size(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
-    if (N < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !kda::spec::dim_ok(dv) || max_nodes < 1 ||
+size_t kda_tree_attn_workspace_size_for(kda_dtype dtype, int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
+    if (!kda::spec::dtype_ok(dtype) || N < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !kda::spec::dim_ok(dv) || max_nodes < 1 ||
         max_nodes > KDA_MAX_TREE_NODES || max_ctx < 0 || max_ctx > 0x7fffffffLL)
         return 0;
-    return kda::layout_of(N, T, Hq, Hkv, dv, max_nodes, max_ctx).total;
+    return kda::layout_of(dtype, N, T, Hq, Hkv, dv, max_nodes, max_ctx).total;
+}
+
+size_t kda_tree_attn_workspace_size(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx) {
+    const size_t a = kda_tree_attn_workspace_size_for(KDA_BF16, N, T, Hq, Hkv, dv, max_nodes, max_ctx);
+    const size_t b = kda_tree_attn_workspace_size_for(KDA_F32, N, T, Hq, Hkv, dv, max_nodes, max_ctx);
+    return a > b ? a : b;
 }
 
 kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
@@ -1178,9 +1205,8 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     kda_status st = check_pages(cache, dtype, N, &c);
     if (st != KDA_OK) return st;
     const int64_t max_ctx = static_cast<int64_t>(c.page_size) * c.max_pages;
-    if (!workspace || !aligned_to(workspace, 16) ||
-        ws_bytes < kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx))
-        return KDA_ERR_WORKSPACE;
+    const kda::AttnLayout l = kda::layout_of(dtype, N, T, Hq, Hkv, dv, max_nodes, max_ctx);
+    if (!workspace || !aligned_to(workspace, 16) || ws_bytes < l.total) return KDA_ERR_WORKSPACE;
     const int64_t vec = 16 / static_cast<int64_t>(elem_size(dtype));
     if (!q_stride) q_stride = static_cast<int64_t>(Hq) * dk;
     if (!k_stride) k_stride = static_cast<int64_t>(Hkv) * dk;
@@ -1192,24 +1218,23 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     if (T > 0 && (!q || !k || !v || !o)) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(o, 16) || !aligned_to(lse, 4))
         return KDA_ERR_INVALID_ARGUMENT;
-    const kda::AttnLayout l = kda::layout_of(N, T, Hq, Hkv, dv, max_nodes, max_ctx);
-    if (l.units > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
+    if (l.units > 0x7fffffffLL || l.part_rows > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0 || T == 0) return cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     kda::attn::AttnParams p{};
     p.q = q; p.k = k; p.v = v; p.o = o; p.lse = lse; p.c = c; p.cu = cu_nodes; p.parent = parent;
     p.T = T; p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
-    p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.max_nodes = max_nodes; p.max_splits = l.max_splits; p.scale = scale;
+    p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.max_nodes = l.max_nodes; p.scale = scale;
     p.status = reinterpret_cast<uint32_t *>(ws);
     p.info = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info);
     p.info_tc = reinterpret_cast<kda::attn::SeqInfo *>(ws + l.info_tc);
     p.wide = dtype == KDA_F32;
-    p.tc = dtype == KDA_BF16 && max_nodes * p.G > kda::attn::kTcLeast;
+    p.tc = l.tc;
     p.bad = reinterpret_cast<uint32_t *>(ws + l.bad);
     p.seq_of = reinterpret_cast<int32_t *>(ws + l.seq_of);
     p.sees = reinterpret_cast<uint64_t *>(ws + l.sees);
-    if (max_nodes > 1) {
+    if (l.max_nodes > 1) {
         p.given_v = v;
         p.given_vs = v_stride;
         p.v = ws + l.copy_v;
@@ -1218,10 +1243,8 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
     }
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
-    p.tc_ml = reinterpret_cast<float2 *>(ws + l.tc_ml);
-    p.tc_o = reinterpret_cast<float *>(ws + l.tc_o);
-    if (dk == 128) return dv == 128 ? kda::launch_attn<128, 128>(p, dtype, l.max_tiles, s) : kda::launch_attn<128, 64>(p, dtype, l.max_tiles, s);
-    return dv == 128 ? kda::launch_attn<64, 128>(p, dtype, l.max_tiles, s) : kda::launch_attn<64, 64>(p, dtype, l.max_tiles, s);
+    if (dk == 128) return dv == 128 ? kda::launch_attn<128, 128>(p, dtype, l, s) : kda::launch_attn<128, 64>(p, dtype, l, s);
+    return dv == 128 ? kda::launch_attn<64, 128>(p, dtype, l, s) : kda::launch_attn<64, 64>(p, dtype, l, s);
 }
 
 }  // extern "C"

@@ -22,7 +22,8 @@ constexpr int kTcKeys = 128;     // keys of a tile there
 // sequence has units in one of the two lists).
 struct __align__(16) SeqInfo {
     int ctx, nodes, t0, unit0;   // context, nodes, first packed node; units (tcgen05: row tiles) before it
-    int nsplit, chunk, tiles, pad;
+    int nsplit, chunk, tiles;
+    int part0;                   // its first row of partial results
 };
 
 struct AttnParams {
@@ -32,7 +33,7 @@ struct AttnParams {
     Pages c;
     const int32_t *cu, *parent;
     int64_t T, qs, ks, vs;       // token strides in elements
-    int N, Hq, Hkv, G, max_nodes, max_splits;
+    int N, Hq, Hkv, G, max_nodes;
     bool wide;                   // fp32
     int tc;                      // sequences of more than kTcLeast rows go to the tcgen05 kernel
     float scale;
@@ -47,10 +48,8 @@ struct AttnParams {
     const void *given_v;
     int64_t given_vs;
     int32_t *odd;                // [T] a packed node has such values; null in a batch of single nodes, which has no copy
-    float *part_o;               // [T, Hq, max_splits, dv]
-    float2 *part_ml;             // [T, Hq, max_splits] maximum (base 2) and sum
-    float *tc_o;                 // tcgen05 kernel's parts: [part][dv / 4][kTcRows] of 4 columns
-    float2 *tc_ml;               // [part][kTcRows]
+    float *part_o;               // partial results, dv columns a row: [node, Hq, part] of a sequence, or tc_part's tiles
+    float2 *part_ml;             // and their maximum (base 2) and sum
 };
 
 // How a sequence is cut, whatever else is in the batch: parts of at least least_chunk keys (a part's partial result, rows x dv
@@ -108,8 +107,27 @@ __host__ __device__ inline void tc_split_of(int ctx, int Hkv, int tiles, int *ns
     *nsplit = ctx > 0 ? (ctx - 1) / *chunk + 1 : 1;
 }
 
-// Partial results of the tcgen05 kernel, by the row tile's number in info_tc's order; a tile alone leaves two per part.
-__host__ __device__ inline int64_t tc_part(int64_t tile, int stream) { return 2 * tile + stream; }
+// Partial results are numbered by the plan: a sequence has as many rows of them as its own cut asks for.  The tcgen05 kernel's lie by
+// KV head, row tile and part, [dv / 4][pitch] of 4 columns each; a tile alone leaves two per part, a pair of one part none.
+__host__ __device__ inline int tc_pitch(int rows, int tile) {
+    const int left = rows - tile * kTcRows;
+    return left >= kTcRows ? kTcRows : (left + 7) / 8 * 8;
+}
+__host__ __device__ inline int tc_part_rows(int rows, int tiles, int nsplit) {  // of one KV head
+    const int paired = nsplit > 1 ? nsplit : 0;
+    return (tiles - 1) * kTcRows * paired + tc_pitch(rows, tiles - 1) * (tiles & 1 ? 2 * nsplit : paired);
+}
+__device__ __forceinline__ int64_t tc_part(int part0, int rows, int tiles, int nsplit, int head, int tile, int split, int stream) {
+    const bool alone = (tile | 1) >= tiles;  // the last of an odd number: those before it are pairs
+    return part0 + static_cast<int64_t>(head) * tc_part_rows(rows, tiles, nsplit) + tile * kTcRows * (nsplit > 1 ? nsplit : 0) +
+           (alone ? 2 * split + stream : split) * tc_pitch(rows, tile);
+}
+// Rows of partial results of a sequence of `nodes` nodes in nsplit parts.
+__host__ __device__ inline int64_t part_rows(bool tc, int nodes, int Hq, int Hkv, int nsplit) {
+    const int rows = nodes * (Hq / Hkv);
+    if (tc && rows > kTcLeast) return static_cast<int64_t>(Hkv) * tc_part_rows(rows, tc_tiles_of(rows), nsplit);
+    return nsplit > 1 ? static_cast<int64_t>(nodes) * Hq * nsplit : 0;
+}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool there) {
     const int n = there ? 16 : 0;  // 0: nothing is read and the 16 bytes become zeros

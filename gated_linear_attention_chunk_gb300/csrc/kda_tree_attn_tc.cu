@@ -517,7 +517,8 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
         const bool ok = live && !err;
         const int64_t out = static_cast<int64_t>(w.t0 + node) * p.Hq + hq;
         const bool whole = w.pair && w.nsplit == 1;
-        const int64_t part = tc_part(w.first + (static_cast<int64_t>(w.head) * w.nsplit + w.split) * w.tiles + tile, w.pair ? 0 : s);
+        const int64_t part = whole ? 0 : tc_part(__ldg(&p.info_tc[w.n].part0), rows, w.tiles, w.nsplit, w.head, tile, w.split, s);
+        const int pitch = tc_pitch(rows, tile);
         if (any) {
             const float f = whole ? 1.f / sum : 1.f;
 #pragma unroll
@@ -536,15 +537,15 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
                         dst[i] = make_uint4(k[0], k[1], k[2], k[3]);
                     }
                 } else if (live && !whole) {  // [DV / 4][row]: a warp's stores are consecutive
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.tc_o) + (part * (DV / 4) + x / 4) * kTcRows + row;
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o) + part * (DV / 4) + (x / 4) * pitch + row;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i * kTcRows] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) dst[i * pitch] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
             tc_fence_before();
             mbar_arrive(&c.o_empty[s]);
         }
-        if (live && !whole) p.tc_ml[part * kTcRows + row] = make_float2(ref, sum);
+        if (live && !whole) p.part_ml[part + row] = make_float2(ref, sum);
         else if (ok && p.lse) p.lse[out] = (ref + log2f(sum)) * kLn2;
         w.next(p);
     }
@@ -628,12 +629,14 @@ __global__ void __launch_bounds__(kWays * kTcRows) combine_tc_kernel(const AttnP
     const int row = threadIdx.x % kTcRows, chain = threadIdx.x / kTcRows, r = tile * kTcRows + row;
     const int parts = alone ? 2 * s.nsplit : s.nsplit;
     const bool live = r < s.nodes * p.G;
-    const int64_t id0 = s.unit0 + static_cast<int64_t>(head) * s.nsplit * s.tiles + tile;
-    auto part = [&](int i) { return alone ? tc_part(id0 + static_cast<int64_t>(i >> 1) * s.tiles, i & 1) : tc_part(id0 + static_cast<int64_t>(i) * s.tiles, 0); };
+    const int rows = s.nodes * p.G, pitch = tc_pitch(rows, tile);
+    const int64_t part0 = tc_part(s.part0, rows, s.tiles, s.nsplit, head, tile, 0, 0);
+    const float2 *all_ml = p.part_ml + part0 + row;
+    const float4 *all_o = reinterpret_cast<const float4 *>(p.part_o) + part0 * (DV / 4) + c0 / 4 * pitch + row;
     float m = -INFINITY;
     if (live) {
 #pragma unroll 8
-        for (int i = 0; i < parts; ++i) m = fmaxf(m, p.tc_ml[part(i) * kTcRows + row].x);
+        for (int i = 0; i < parts; ++i) m = fmaxf(m, all_ml[static_cast<int64_t>(i) * pitch].x);
     }
     const float base = m == -INFINITY ? 0.f : m;
     float l[kSums] = {}, o[kSums][kCombCols] = {};
@@ -644,14 +647,14 @@ __global__ void __launch_bounds__(kWays * kTcRows) combine_tc_kernel(const AttnP
             for (int y = 0; y < kSums; ++y) {
                 const int i = i0 + y;
                 if (i >= parts) break;
-                const float2 ml = p.tc_ml[part(i) * kTcRows + row];
-                const float4 *src = reinterpret_cast<const float4 *>(p.tc_o) + (part(i) * (DV / 4) + c0 / 4) * kTcRows + row;
+                const float2 ml = all_ml[static_cast<int64_t>(i) * pitch];
+                const float4 *src = all_o + static_cast<int64_t>(i) * pitch * (DV / 4);
                 const bool empty = ml.y == 0.f;  // no keys: its sums were not written
                 const float f = exp2f(ml.x - base);
                 l[y] = fmaf(f, ml.y, l[y]);
 #pragma unroll
                 for (int j = 0; j < kCombCols / 4; ++j) {
-                    const float4 v = src[j * kTcRows];
+                    const float4 v = src[j * pitch];
                     o[y][4 * j] = fmaf(f, empty ? 0.f : v.x, o[y][4 * j]);
                     o[y][4 * j + 1] = fmaf(f, empty ? 0.f : v.y, o[y][4 * j + 1]);
                     o[y][4 * j + 2] = fmaf(f, empty ? 0.f : v.z, o[y][4 * j + 2]);

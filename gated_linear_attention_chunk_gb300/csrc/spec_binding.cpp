@@ -240,7 +240,7 @@ PyObject *tree_attn(PyObject *const *a) {
     at::Tensor lse;
     if (!absent(a[12])) lse = given(a[12], "lse", at::kFloat, {T, Hq});
     else if (truth(a[13])) lse = fresh({T, Hq}, at::kFloat, q);
-    const size_t need = absent(a[14]) ? kda_tree_attn_workspace_size(small(c.N, "N"), T, small(Hq, "Hq"), small(Hkv, "Hkv"), small(dv, "dv"),
+    const size_t need = absent(a[14]) ? kda_tree_attn_workspace_size_for(dt, small(c.N, "N"), T, small(Hq, "Hq"), small(Hkv, "Hkv"), small(dv, "dv"),
                                                                      max_nodes, c.max_ctx) : 0;
     const Workspace ws(a[14], need, q);
     check(kda_tree_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, &c.c, cu, parent, small(c.N, "N"), T, small(Hq, "Hq"),

@@ -86,6 +86,7 @@ _SIGS = {
     "kda_rope_bwd": (_int, [_vp, _vp, _int, _vp, _vp, _i64, _int, _int, _int, _int, _i64, _i64, _int, ctypes.c_float,
                             _vp, _vp, _i64, _i64, _vp]),
     "kda_tree_attn_workspace_size": (ctypes.c_size_t, [_int, _i64, _int, _int, _int, _int, _i64]),
+    "kda_tree_attn_workspace_size_for": (ctypes.c_size_t, [_int, _int, _i64, _int, _int, _int, _int, _i64]),
     "kda_tree_attn": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _int, _int, _int, _int, _i64, _i64, _i64,
                              _int, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "kda_cache_append": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _i64, _int, _int, _int, _i64, _i64, _vp, _vp,

@@ -96,9 +96,15 @@ def kda_rope_bwd(d_q_out, d_k_out, positions, inv_freq, interleaved: bool = Fals
     return _spec.rope(*args) if stream is None else _on(stream, _spec.rope, *args)
 
 
-def kda_tree_attn_workspace_size(N: int, T: int, Hq: int, Hkv: int, dv: int, max_nodes: int, max_ctx: int) -> int:
-    """Workspace of ``kda_tree_attn`` in bytes (0 for invalid arguments); max_ctx = block-table columns x page size."""
-    return int(_kda.load_library().kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx))
+def kda_tree_attn_workspace_size(N: int, T: int, Hq: int, Hkv: int, dv: int, max_nodes: int, max_ctx: int,
+                                 dtype: Optional[torch.dtype] = None) -> int:
+    """Workspace of ``kda_tree_attn`` in bytes (0 for invalid arguments); max_ctx = block-table columns x page size.
+    ``dtype`` bf16 or fp32: what that type needs; None: enough for either."""
+    lib = _kda.load_library()
+    if dtype is None:
+        return int(lib.kda_tree_attn_workspace_size(N, T, Hq, Hkv, dv, max_nodes, max_ctx))
+    code = {torch.bfloat16: _kda.KDA_BF16, torch.float32: _kda.KDA_F32}.get(dtype, -1)
+    return int(lib.kda_tree_attn_workspace_size_for(code, N, T, Hq, Hkv, dv, max_nodes, max_ctx))
 
 
 def kda_tree_attn(q, k, v, k_pages, v_pages, block_table, ctx_len, cu_nodes, parent=None, scale: Optional[float] = None,

@@ -443,6 +443,9 @@ typedef struct kda_paged_kv {
  * writes nothing.
  */
 size_t kda_tree_attn_workspace_size(int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes, int64_t max_ctx);
+/* The same for one type (bf16's is the smaller where trees are small). */
+size_t kda_tree_attn_workspace_size_for(kda_dtype dtype, int N, int64_t T, int Hq, int Hkv, int dv, int max_nodes,
+                                        int64_t max_ctx);
 
 kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
                          const int32_t *cu_nodes, const int32_t *parent, int N, int64_t T, int Hq, int Hkv, int dk,

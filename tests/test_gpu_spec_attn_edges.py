@@ -168,3 +168,24 @@ def test_a_drafted_branch_changes_nothing_before_it(kda, dtype, nodes, G):
     keep = [i for i in range(nodes + 5) if i != last]
     assert torch.equal(o[keep], want_o[keep]) and torch.equal(lse[keep], want_lse[keep])
     assert bool(o[last].isnan().all()) and bool(lse[last].isnan().all())
+
+
+def _sizes(rng, N, most):
+    return [int(rng.integers(1, most + 1)) if rng.random() < 0.5 else int(rng.choice([1, most])) for _ in range(N)]
+
+
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+@pytest.mark.parametrize("N,most,G,Hkv,longest", [(1, 1, 1, 1, 9000), (9, 4, 4, 8, 9000), (5, 64, 8, 4, 20000), (40, 9, 8, 1, 3000), (6, 33, 5, 3, 9000)])
+def test_partial_results_stay_inside_the_workspace(kda, dtype, N, most, G, Hkv, longest):
+    """Batches of every mixture of tree sizes over contexts as long as their block tables allow, in a workspace of exactly the size
+    that is asked for, with a marked region behind it."""
+    rng = np.random.default_rng(N)
+    nodes = _sizes(rng, N, most)
+    c = _case(nodes, [longest if rng.random() < 0.8 else int(rng.integers(0, longest)) for _ in nodes], G, Hkv, 64, 64, 128, dtype, True, seed=N)
+    width = c["table"].shape[1] * 128
+    need = kda.kda_tree_attn_workspace_size(N, sum(nodes), G * Hkv, Hkv, 64, most, width, dtype=dtype)
+    assert need <= kda.kda_tree_attn_workspace_size(N, sum(nodes), G * Hkv, Hkv, 64, most, width)
+    whole = torch.full((need + (1 << 20),), 0xa5, dtype=torch.uint8, device="cuda")
+    o, lse, status = _run(kda, c, workspace=whole[:need], max_nodes=most)
+    assert status == kda.KDA_OK and bool((whole[need:] == 0xa5).all())
+    _check(c, o, lse)
