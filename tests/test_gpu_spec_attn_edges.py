@@ -189,3 +189,135 @@ def test_partial_results_stay_inside_the_workspace(kda, dtype, N, most, G, Hkv, 
     o, lse, status = _run(kda, c, workspace=whole[:need], max_nodes=most)
     assert status == kda.KDA_OK and bool((whole[need:] == 0xa5).all())
     _check(c, o, lse)
+
+
+# ---- the tcgen05 kernel's special cases (bf16, more than 32 rows per KV head), beside sequences of the register kernels ----------
+
+WIDE = dict(nodes=[3, 9, 2, 33], G=16, Hkv=2)  # 48, 144, 32 and 528 rows: a tile alone, a pair, the register kernel, pairs and one over
+
+
+def _wide(ctx, dk, dv, page=16, tree=True, seed=0, sharp=1.0):
+    return _case(WIDE["nodes"], ctx, WIDE["G"], WIDE["Hkv"], dk, dv, page, ref.BF16, tree, seed=seed, sharp=sharp)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 64), (64, 128)])
+@pytest.mark.parametrize("scale,sharp", [(None, 12.0), (-0.05, 4.0), (0.0, 1.0)])
+def test_wide_sharp_scores_and_scales(kda, dk, dv, scale, sharp):
+    c = _wide([333, 70, 1500, 2900], dk, dv, seed=4, sharp=sharp)
+    c["scale"] = dk ** -0.5 if scale is None else scale
+    o, lse, status = _run(kda, c)
+    assert status == kda.KDA_OK
+    _check(c, o, lse)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_wide_maximum_that_keeps_rising(kda, sign):
+    """Scores that grow along the context by hundreds, so that the reference is left behind tile after tile; and that fall."""
+    c = _wide([1000, 2000, 300, 700], 128, 128, page=64, seed=8)
+    c["q"] = (c["q"].abs() + 0.5).to(ref.BF16)
+    for n, length in enumerate(c["ctx"].tolist()):
+        at = torch.arange(length)
+        ramp = sign * torch.linspace(-3, 3, length)[:, None, None]
+        page, slot = c["table"][n].long()[at // 64], at % 64
+        c["kp"][page, slot] = (0.1 * c["kp"][page, slot].float() + ramp).to(ref.BF16)
+    o, lse, status = _run(kda, c)
+    assert status == kda.KDA_OK
+    _check(c, o, lse)
+
+
+@pytest.mark.parametrize("ctx1", [40, 1400, 6000])  # one part and several
+def test_wide_device_errors_write_nothing(kda, ctx1):
+    good = _wide([70, ctx1, 33, 500], 128, 128, seed=7)
+    want = _run(kda, good)
+    assert want[2] == kda.KDA_OK
+    for code, key, at, value in ((kda.KDA_ERR_BAD_PAGE, "table", (1, 1), -1), (kda.KDA_ERR_BAD_PAGE, "table", (1, (ctx1 - 1) // 16), good["kp"].shape[0]),
+                                 (kda.KDA_ERR_BAD_PAGE, "ctx", 1, -1), (kda.KDA_ERR_BAD_PAGE, "ctx", 1, 1 << 20),
+                                 (kda.KDA_ERR_BAD_TREE, "parent", 5, 2), (kda.KDA_ERR_BAD_TREE, "parent", 11, -1)):
+        f = dict(good)
+        f[key] = good[key].clone()
+        f[key][at] = value
+        o, lse, status = _marked(kda, f)
+        assert status == code
+        assert bool((o[3:12] == 7).all()) and bool((lse[3:12] == 7).all())
+        for a, b in ((o, want[0]), (lse, want[1])):
+            assert torch.equal(a[:3], b[:3]) and torch.equal(a[12:], b[12:])
+    assert _run(kda, good)[2] == kda.KDA_OK
+
+
+def test_wide_strides_and_axis_orders(kda):
+    """q, k, v inside one fused projection; heads before rows in the pools; K and V in one pool; a wider block table."""
+    c = _wide([200, 90, 1000, 10], 128, 128, seed=5)
+    o, lse, _ = _run(kda, c)
+    T, Hq, Hkv = c["q"].shape[0], 32, 2
+    fused = torch.cat([c[x].reshape(T, -1) for x in "qkv"], 1).cuda()
+    f = dict(c)
+    f["q"] = fused[:, :Hq * 128].view(T, Hq, 128)
+    f["k"], f["v"] = (fused[:, (Hq + i * Hkv) * 128:(Hq + (i + 1) * Hkv) * 128].view(T, Hkv, 128) for i in range(2))
+    pool = torch.stack([c["kp"], c["vp"]], 1).permute(0, 1, 3, 2, 4).contiguous().cuda()  # [pages, 2, Hkv, page, d]
+    f["kp"], f["vp"] = pool[:, 0].transpose(1, 2), pool[:, 1].transpose(1, 2)
+    table = torch.full((4, c["table"].shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+    table[:, :c["table"].shape[1]] = c["table"].cuda()
+    f["table"] = table[:, :c["table"].shape[1]]
+    o2, lse2, status = _run(kda, f)
+    assert status == kda.KDA_OK and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_wide_offsets_past_32_bits(kda):
+    page, Hkv, d = 16, 2, 128
+    stride = 2 ** 31 // 64 + 4096  # elements per page
+    pool = torch.empty(66 * stride, dtype=ref.BF16, device="cuda")
+    pages = pool.as_strided((66, page, Hkv, d), (stride, Hkv * d, d, 1))
+    c = _case([3], [100], 16, Hkv, d, d, page, ref.BF16, True, seed=6)
+    f = dict(c)
+    far = torch.tensor([[65, 0, 64, 1, 63, 2, 62]], dtype=torch.int32)
+    for key, at in (("kp", 0), ("vp", page * Hkv * d)):
+        view = pool[at:].as_strided(pages.shape, pages.stride()) if at else pages
+        view[far[0].long().cuda()] = c[key][c["table"][0].long()].cuda()
+        f[key] = view
+    f["table"] = far
+    o, lse, status = _run(kda, f)
+    assert status == kda.KDA_OK
+    want = _run(kda, c)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("ctx", [100, 3000])
+def test_wide_infinities_and_nan_in_sight(kda, ctx):
+    """What a row sees counts: an infinite value in its column, a key of -inf scores not at all, a key of NaN in that head."""
+    c = _case([3], [ctx], 16, 2, 64, 64, 16, ref.BF16, False, seed=2)
+    c["q"] = c["q"].abs() + 0.1
+    page, slot = int(c["table"][0, 3]), 5
+    f = dict(c, vp=c["vp"].clone(), kp=c["kp"].clone())
+    f["vp"][page, slot, 1, 7] = float("inf")
+    o, _, _ = _run(kda, f)
+    assert bool(torch.isposinf(o[:, 16:, 7]).all())
+    o[:, 16:, 7] = 0
+    assert bool(torch.isfinite(o).all())
+    f = dict(c, kp=c["kp"].clone())
+    f["kp"][page, slot, 0] = -float("inf")
+    o, lse, _ = _run(kda, f)
+    f["kp"][page, slot, 0] = -1e30  # the same weight: none
+    _check(f, o, lse)
+    f["kp"][page, slot, 0] = float("nan")
+    o, lse, _ = _run(kda, f)
+    assert bool(o[:, :16].isnan().all()) and bool(lse[:, :16].isnan().all()) and not bool(o[:, 16:].isnan().any())
+
+
+@pytest.mark.parametrize("dtype,G", [(ref.BF16, 1), (ref.BF16, 12), (ref.F32, 2)])
+def test_large_batches(kda, dtype, G):
+    """More sequences than the plan takes in one round, empty ones among them, trees of every kernel."""
+    rng = np.random.default_rng(3)
+    N = 700
+    nodes = [int(x) for x in rng.choice([0, 1, 2, 3, 9], N)]
+    ctx = [int(x) for x in rng.integers(0, 300, N)]
+    c = _case(nodes, ctx, G, 1, 64, 64, 16, dtype, True, seed=9)
+    o, lse, status = _run(kda, c)
+    assert status == kda.KDA_OK
+    _check(c, o, lse)
+
+
+def test_default_bound_on_nodes_changes_no_bits(kda):
+    for nodes, G in (([1], 4), ([1, 1, 1], 8), ([4, 1, 3], 4), ([5, 2], 8)):
+        c = _case(nodes, [900, 40, 7][:len(nodes)], G, 2, 128, 128, 16, ref.BF16, True, seed=len(nodes))
+        a, b = _run(kda, c), _run(kda, c, max_nodes=max(nodes))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
