@@ -62,7 +62,8 @@ class HybridModel:
         seq = torch.repeat_interleave(torch.arange(self.N, device="cuda"), (cu[1:] - cu[:-1]).long(), output_size=T)
         positions = (self.ctx_len[seq] + torch.arange(T, device="cuda") - cu[seq]).int()
         qa, ka = kda.kda_rope(qa, ka, positions, self.inv_freq, mscale=self.mscale)
-        a, _ = kda.kda_tree_attn(qa, ka, va, self.k_pages, self.v_pages, self.table, self.ctx_len, cu, return_lse=False)
+        a, _ = kda.kda_tree_attn(qa, ka, va, self.k_pages, self.v_pages, self.table, self.ctx_len, cu, return_lse=False,
+                                 max_nodes=min(T // self.N, kda.KDA_MAX_TREE_NODES))
         x = x + a.view(T, -1) @ self.w_attn_out
         return torch.softmax((x @ self.unembed).float(), -1), (k, v, g, beta), (ka, va)
 

@@ -4,16 +4,18 @@
 //     (a, b) -> m (a cos t - b sin t, a sin t + b cos t),
 // and the gradient is the transposed map, the same with -t.
 //
-// The angle is reduced exactly: w_j / 2 pi is kept as a 64-bit fixed-point fraction of a turn
-// (rounded once, 2^-53 relative), so p times it modulo one turn is the low 64 bits of an integer
-// product, with no error that grows beyond |p| 2^-54 turns.  Its signed top 32 bits then go
-// through sincospif.
+// The angle is reduced without a loss of its own: w_j / 2 pi is kept as a 64-bit fixed-point fraction of a
+// turn (two fp64 roundings, 2^-52 relative, and 2^-64), so p times it modulo one turn is the low 64 bits of an integer product,
+// and the angle is off by |p w_j| 2^-52 radians and |p| 2^-64 turns at most: less than the rounding that follows up to
+// |p w_j| of about 2^27.  Its signed top 32 bits go through sincospif as an fp32 number (2^-24 of a half turn: the
+// products after it are fp32 as well).
 //
 // The bytes of q and k, read and written once, bound it.  A CTA takes up to kTokens tokens at a time: one
 // sine and cosine per (token, pair) into shared memory, used by every head of that token; a thread
 // keeps one 16-byte column of a head (half layout: the two 16-byte halves of its pairs) and
 // walks the (token, head) rows, two in flight.  16,384 tokens of 32 + 8 heads of 128, bf16: 57.5 us, 5.8 TB/s (a persistent grid
-// 62.6 us; four rows in flight, at fewer CTAs per SM, 64.1; eight tokens per CTA 58.4 to 68.5).
+// 62.6 us; four rows in flight, at fewer CTAs per SM, 64.1; eight tokens per CTA 58.4 to 68.5).  Rows or rotated widths that are no
+// multiple of 16 bytes go by single elements: 231 us for the same tokens with 126 rotated channels.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

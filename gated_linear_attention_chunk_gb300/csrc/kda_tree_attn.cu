@@ -14,15 +14,21 @@
 // combine_kernel joins them in part order.  Everything a unit does depends on its own sequence alone,
 // so a sequence's bits do not depend on the batch.
 //
-// Bounded by the bytes of the cache: 128 sequences of 1 to 4 nodes over 1 to 4,096 keys (8 KV heads, bf16) take 204 us, 5.3 TB/s; 16 rows
-// over 131,072 keys 188 us, 5.7 TB/s.  The four warps of a CTA take a quarter of a tile's 64 keys each (half, on two row
+// Bounded by the bytes of the cache: 128 sequences of 1 to 4 nodes over 1 to 4,096 keys (8 KV heads, bf16) take 209 us, 5.2 TB/s; 16 rows
+// over 131,072 keys 187 us, 5.7 TB/s.  The four warps of a CTA take a quarter of a tile's 64 keys each (half, on two row
 // groups) and are joined through shared memory at the end of a part; three CTAs of two stages per SM cover one another's part ends
 // (two CTAs of three stages: 224 us).  From 33 rows on (bf16) the tcgen05 kernel takes over: mma.sync falls behind the
-// loads there (40 rows over 131,072 keys: 358 us, there 250).  fp32 is bound by the rate of mma.sync in tf32: 40 us for seven
-// sequences of 1 to 13 nodes over 1 to 4,099 keys.
+// loads there (40 rows over 131,072 keys: 358 us, there 232).  fp32: 41 us for seven sequences of 1 to 13 nodes over 1 to 4,099 keys,
+// neither at the bytes (4.4 us) nor at the tensor rate (the pipe is busy 9.5% of the time): a part has a few tiles, two warps
+// share a scheduler, and what they wait for is their own chain of copies, splits, products and the join.
 //
-// plan_kernel, one launch before: checks the lengths, lists the sequences with their first unit, and
-// turns the parents into ancestor masks (one 64-bit word per node, by pointer doubling).
+// bf16 weights meet the values as bf16 (half a step, 2^-9 of a weight): a tensor-core product takes both operands in one type, and a
+// second product with the remainders would double the work on the values.  Sums and maxima are fp32, of the weights before
+// that rounding.
+//
+// plan_kernel, one launch before: checks the lengths, lists the sequences with their first unit and their place among the partial
+// results, turns the parents into ancestor masks (one 64-bit word per node, by pointer doubling), and copies the drafted values
+// without infinities and NaN, which combine_kernel adds to the rows that see them (2.5 of the 209 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -306,7 +312,7 @@ struct Ring {
     static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;
     static constexpr int kThreads = 128;
     static constexpr int kStages = sizeof(T) == 2 ? 2 : 3;
-    static constexpr int kPerSm = sizeof(T) == 2 ? 3 : 2;  // CTAs (bf16 with three stages and two CTAs: 224 us for 204)
+    static constexpr int kPerSm = sizeof(T) == 2 ? 3 : 2;  // CTAs (bf16 with three stages and two CTAs: 224 us for 204, before drafted values were copied)
     static constexpr int kUnitsK = DK * static_cast<int>(sizeof(T)) / 16, kUnitsV = DV * static_cast<int>(sizeof(T)) / 16;
     static constexpr int kBytesK = kKeys * kUnitsK * 16, kBytesV = kKeys * kUnitsV * 16;
     static constexpr int kStage = kBytesK + kBytesV;

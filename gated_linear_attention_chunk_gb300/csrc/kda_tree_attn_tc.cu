@@ -1,4 +1,4 @@
-// Tree attention on the tcgen05 tensor cores, for sequences of more than 64 query rows per KV head (bf16).
+// Tree attention on the tcgen05 tensor cores, for sequences of more than 32 query rows per KV head (bf16).
 //
 // The same one-pass softmax as the register kernels.  With R rows per KV head a key costs 2 (dk + dv) R operations against
 // 2 (dk + dv) bytes, so from about 280 rows on the tensor cores bound it, and mma.sync reaches less than half of
@@ -9,7 +9,9 @@
 // Per step of a stream S = Q K^T (128 x 128, fp32, TMEM), the softmax warps turn S into weights P (bf16, written over S in
 // TMEM), O += P V (P from TMEM, V as an MN-major operand).  While one stream's softmax runs, the tensor cores work
 // for the other.  The running maximum a row's weights refer to is raised only when the true one has grown by more than
-// 2^8 beyond it, so O is seldom rescaled (fp32 and bf16 have the range for weights up to 2^8).
+// 2^8 beyond it, so O is seldom rescaled (fp32 and bf16 have the range for weights up to 2^8).  P is bf16 because both
+// operands of a product have one type and V is bf16; that rounds a weight by at most 2^-9 of it (a second product with the
+// remainders would add half of the tensor work).  The row's sum is fp32, of the weights before that rounding.
 //
 // Warps:  0-3 and 4-7 softmax of stream 0 and 1 (a thread per row), 8-11 fill the ring, 12 issues the MMAs.
 // TMEM:   S0 0..127, S1 128..255, O0 256.., O1 384.. (512 columns).
@@ -18,9 +20,11 @@
 // filled with zeros.  The ring holds the tiles in the order in which they are consumed:
 // K_0 .. K_{L-1}, V_0, K_L, V_1, K_{L+1}, .. with L = 1 for a pair and 2 for a tile alone.
 //
-// Four sequences of 32 nodes over 131,072 keys (8 heads on each of 4 KV heads: a pair of tiles): 273 us, 1.0 PFLOP/s.  A pair's
+// Four sequences of 32 nodes over 131,072 keys (8 heads on each of 4 KV heads: a pair of tiles): 275 us, 1.0 PFLOP/s.  A pair's
 // step of 2 x 128 x 128 scores takes 3.4k clocks, the chain of one stream: maximum 0.6k, exponentials 1.0k (16 per clock and
-// SM), PV 0.45k, QK 0.5k and the hand-offs.  A tile alone is bound by the loads: 250 us, 4.3 TB/s.
+// SM), PV 0.45k, QK 0.5k and the hand-offs.  A tile alone is bound by the loads, of which
+// the ring keeps two or so in flight: 64 rows 235 us, 4.6 TB/s; 128 rows 247.  The compiler, which is held to 128 registers for all
+// warps, spills 200 (dk = 64) to 260 bytes a thread.
 //
 // Every wait is bounded (2 s): a role that gives up raises the abort flag, which ends all the others' waits; the MMAs
 // issued so far are drained and the TMEM is freed.

@@ -13,9 +13,10 @@
 // the row into segments of kSegUnit elements (or a multiple), two per warp at a time, and leaves the segments' sums in shared memory,
 // where every CTA of the cluster reads them all in the same order; the draw then needs only the one segment that
 // holds its point again.  So a sequence costs about one reading of one row (two with draft rows),
-// which bounds it: the rest is the latency of the walk's dependent loads.  128 chains of 4 nodes over 131,072 tokens, fp32: 44 us,
-// of them 21.7 in the pass (6.2 TB/s); one tree of 6 nodes over 32,001: 12.3 us a call,
-// 16.4 where a sibling is tried after a refusal (a pass more).  Four CTAs of 256 threads per SM keep all sequences
+// which bounds it: the rest is the latency of the walk's dependent loads.  128 chains of 4 nodes over 131,072 tokens, fp32: 43 us,
+// of them 21.7 in the pass (6.2 TB/s) and about 12 in the steps before and after it (the rest is not accounted for); one tree of 6
+// nodes over 32,001: 12 to 18 us a call, by how many siblings are tried after a refusal (a pass more for each).  With draft rows
+// the 64 registers that four CTAs per SM leave a thread spill 140 bytes (fp32) or 308 (bf16).  Four CTAs of 256 threads per SM keep all sequences
 // resident (one of 512 took 100 us, eight per sequence in two rounds 54, two per sequence 48.5).
 //
 // Precision: the answers are whole numbers, so a rounding shows only next to a border, where a flat

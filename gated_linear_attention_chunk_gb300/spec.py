@@ -7,7 +7,7 @@
 
 ``rope_frequencies`` makes the frequency table of ``kda_rope`` (plain, or scaled for long contexts).
 The accepted nodes go on to ``kda_replay`` for the recurrent states: ``cu_accept`` is its argument, and
-``rows`` picks the tokens' k, v, g and beta.  Like the rest of the package the functions check their
+``rows`` picks the tokens' k, v, g and beta (their number, ``cu_accept[-1]``, has to be read on the host for that).  Like the rest of the package the functions check their
 tensors, allocate what was not passed and call the C entry point of the same name on a stream; the checks and the
 call are in ``_lib/_spec.so`` (``csrc/spec_binding.cpp``), since on small inputs they would take longer than the kernels.
 """
@@ -116,7 +116,8 @@ def kda_tree_attn(q, k, v, k_pages, v_pages, block_table, ctx_len, cu_nodes, par
     [pages, page_size, Hkv, dk], v_pages [.., dv] (any axis order with contiguous channels); block_table [N, max_pages],
     ctx_len [N], cu_nodes [N+1], parent [T] int32 (None: chains).  A node attends to its sequence's first ctx_len cache
     rows, its ancestors and itself; one-node trees are the plain decode step.  ``scale`` defaults to dk ** -0.5;
-    ``max_nodes`` bounds the trees of the batch."""
+    ``max_nodes`` bounds the trees of the batch; pass the real bound where it is known (it sizes the workspace, and above
+    32 rows per KV head adds two launches)."""
     args = (q, k, v, k_pages, v_pages, block_table, ctx_len, cu_nodes, parent, scale, max_nodes, o, lse, return_lse, workspace)
     return _spec.tree_attn(*args) if stream is None else _on(stream, _spec.tree_attn, *args)
 
@@ -126,7 +127,8 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, ctx_len, cu, rows=None
     """Rows j in [cu[n], cu[n+1]) go to the positions after ctx_len[n] of sequence n.  Returns the new lengths [N].
 
     Row j is row ``rows[j]`` of k [T, Hkv, dk] and v [T, Hkv, dv], or row j itself; ``kda_draft_verify``'s cu_accept and
-    rows append the accepted nodes.  Rows from cu[N] on are not read.  The pools are written in place."""
+    rows append the accepted nodes.  Rows from cu[N] on are not read.  The pools are written in place.  After BAD_SLOT, or
+    BAD_PAGE of a row, a new length covers a row that was not written."""
     args = (k, v, k_pages, v_pages, block_table, ctx_len, cu, rows, new_len, workspace)
     return _spec.cache_append(*args) if stream is None else _on(stream, _spec.cache_append, *args)
 

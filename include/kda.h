@@ -391,7 +391,9 @@ kda_status kda_replay_conv(float *state_pool, int64_t num_slots, const int32_t *
  *   positions   [T] int32 (any value)      inv_freq [rot/2] fp64, radians per position
  *   q_out,k_out as q, k with their own strides; may be q and k themselves (same stride).
  * d: a multiple of 8, at most 1024; rot even, 0 <= rot <= d.  Angles are reduced in
- * 64-bit fixed point, so far positions lose nothing; the rest is fp32, rounded once.
+ * 64-bit fixed point and are off by at most |p inv_freq| 2^-52 radians (about what
+ * rounding inv_freq to fp64 costs); sines, cosines and products are fp32, the result is
+ * rounded to dtype once.
  * Pointers are element-aligned; 16-byte aligned rows (and rot / 2, or interleaved rot,
  * a multiple of 16 bytes) take the vector path.  Nothing to report from the device,
  * so no workspace.
@@ -432,10 +434,12 @@ typedef struct kda_paged_kv {
  *   k, v   [T, Hkv, dk], [T, Hkv, dv]: the nodes' own keys and values, not in the cache
  *   o      [T, Hq, dv] dtype, packed;  lse [T, Hq] fp32 or NULL: log sum exp(scale q.k)
  *   max_nodes  the largest tree of the batch (1..KDA_MAX_TREE_NODES); a larger one is
- *          reported as KDA_ERR_BAD_SEQLENS.  T <= N * max_nodes; packed nodes from
+ *          reported as KDA_ERR_BAD_SEQLENS.  A bound far above the trees costs workspace
+ *          and, where it allows more than 32 rows per KV head in bf16, two launches.  T <= N * max_nodes; packed nodes from
  *          cu_nodes[N] on are not read, and their outputs not written.
  * dk, dv each 64 or 128; page_size * max_pages < 2^31.  Scores, softmax and sums are fp32; for bf16 the weights are
- * rounded to bf16 before they meet the values (fp32 inputs: products in three tf32 terms, about 22 bits).
+ * rounded to bf16 (by at most 2^-9 of each) before they meet the values, as the tensor cores take both operands in one
+ * type (fp32 inputs: products in three tf32 terms, about 22 bits).
  * A node's infinities and NaN reach the rows that see the node, and no others.
  * Long contexts are cut into parts that run concurrently and are joined in a fixed
  * order; the cut goes by a sequence's own length and tree, so its bits do not depend
@@ -463,7 +467,8 @@ kda_status kda_tree_attn(const void *q, const void *k, const void *v, kda_dtype 
  * table: such a sequence keeps its length and writes nothing.  BAD_PAGE for a row whose
  * page is outside the pool and BAD_SLOT for rows[j] outside [0, T_src): that row is not
  * written, but the others are and new_len counts it, so after these two errors the
- * length covers a row that was never stored.  Two rows must not name the same place.  workspace: >= KDA_WS_HEADER_BYTES.
+ * length covers a row that was never stored.  Two rows must not name the same place.
+ * workspace: >= KDA_WS_HEADER_BYTES.
  */
 kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const kda_paged_kv *cache,
                             const int32_t *cu, const int32_t *rows, int N, int64_t A_total, int64_t T_src, int Hkv,
@@ -492,10 +497,12 @@ kda_status kda_cache_append(const void *k, const void *v, kda_dtype dtype, const
  * Outputs: cu_accept [N+1] int32: sequence n accepts cu_accept[n+1] - cu_accept[n] nodes,
  * the root among them; rows [T] int32: their packed indices in order, -1 from
  * cu_accept[N] on; next_token [N] int32.  (cu_accept and the rows' k, v, g, beta are what
- * kda_replay takes.)  An empty tree, or one with a device error (BAD_SEQLENS, BAD_TREE),
+ * kda_replay takes; it wants exactly cu_accept[N] tokens, so the caller reads that count on
+ * the host before it gathers them.  kda_cache_append takes cu_accept and rows as they are.)
+ * An empty tree, or one with a device error (BAD_SEQLENS, BAD_TREE),
  * accepts nothing and gives token -1.
- * p - A q and its sums are carried to about 1e-13 (pairs of fp32, fp64 across threads),
- * so a decision stands unless a number lies that close to a border.
+ * p - A q and its sums are carried to about 1e-13 (pairs of fp32; fp64 for the walk's
+ * scalars), so a decision stands unless a number lies that close to a border.
  * V: at most 2^24.  workspace: >= kda_draft_verify_workspace_size(N).
  */
 size_t kda_draft_verify_workspace_size(int N);
