@@ -95,7 +95,8 @@ inline bool smem_opt_in(int bytes) {
     return true;
 }
 
-// A launch that may begin before the one ahead of it in the stream has ended: the kernel's first act is grid_wait().
+// A launch that may begin before the one ahead of it in the stream has ended: the kernel calls grid_wait() before it touches what
+// that one writes, and in any case before it ends.
 template <typename... P, typename... A>
 inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg{};
