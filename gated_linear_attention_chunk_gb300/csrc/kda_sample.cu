@@ -769,7 +769,18 @@ struct Sampler {
         }
     }
 
-    // The distribution: tokens up to the limit have mass / total, the others none.  Element by element, so that a warp's stores
+    // A token's e below c.cut, where a mass ends, times a factor of at most 1.  x = (l - M) log2(e) / t as a pair: l - M is rounded, and what that
+    // leaves out is exact.  Below half of fp32's smallest number it is 0, as for a masked token.
+    __device__ __forceinline__ float faint(float l, float factor) const {
+        const float d = __fsub_rn(l, c.top), v = __fsub_rn(d, l), d_lo = __fsub_rn(__fsub_rn(l, __fsub_rn(d, v)), __fadd_rn(c.top, v));
+        const float h = __fmul_rn(d, c.c_hi);
+        if (!(h > -151.f)) return 0.f;
+        const float lo = fmaf(d, c.c_hi, -h) + fmaf(d, c.c_lo, d_lo * c.c_hi), n = rintf(h);
+        // the power of two in two steps: fp32's smallest numbers are rounded to once
+        const float scale = __int_as_float((static_cast<int>(n) + 64 + 127) << 23);
+        return exp2f((h - n) + lo) * factor * 5.42101086e-20f * scale;
+    }
+    // The distribution: tokens up to the limit have e / total, the others none.  Element by element, so that a warp's stores
     // are consecutive whatever the row's alignment.
     __device__ void write(int64_t row_at, uint64_t limit, float inv_total) {
         const int64_t first = static_cast<int64_t>(col0) * W - shift;
@@ -785,7 +796,7 @@ struct Sampler {
             if (inf_top) l = l == INFINITY ? 0.f : -INFINITY;
             float x = 0.f;
             if (l > -INFINITY && !(l < least_kept) && (l != least_kept || static_cast<uint32_t>(i) <= last_kept))
-                x = both(exp2_parts(l, l, c, shared().table).value).x * inv_total;
+                x = l - c.sub < c.cut ? faint(l, inv_total) : both(exp2_parts(l, l, c, shared().table).value).x * inv_total;
             if (p.wide_probs) wide[i] = x;
             else narrow[i] = __float2bfloat16_rn(x);
         }
