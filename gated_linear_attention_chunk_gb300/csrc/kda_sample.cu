@@ -52,6 +52,7 @@ constexpr float kSpan = 20.f;      // the bins cover distances from M of up to 2
 // With top-k they cover 40 at least: likely tokens at low temperatures leave the k-th far behind them.  (128 rows of 131,072 whose other tokens lie 20 t and
 // more below three: 184 us the general way, 75 so.)
 constexpr float kRankSpan = 40.f;
+constexpr float kHottest = 1e30f;  // higher temperatures count as this one
 static_assert(3 * kBins >= kCoarse && 3 * kBins * 4 >= kList * 8, "all lie over the bins");
 
 // 2^(i / 256) as th (1 + tl), the exponential's series in fp64.  th's bits come without i << 15: see weigh2.
@@ -923,7 +924,8 @@ struct Sampler {
         unit = __int_as_float((127 + 44 - p.extra) << 23);
         for (int i = threadIdx.x; i < 256; i += kThreads) shared().table[i] = make_uint2(kExp2.th[i], __float_as_uint(kExp2.tl[i]));
         grid_wait();
-        const float t = p.temperature ? p.temperature[at] : 1.f;
+        // (c.cut, 47 halvings below M, is then always within fp32's range: hotter than 3e36 it was not, and what is -inf had a mass)
+        const float asked = p.temperature ? p.temperature[at] : 1.f, t = asked > kHottest ? kHottest : asked;
         const bool greedy = !(t > 1e-30f);
         const float min_p = p.min_p ? p.min_p[at] : 0.f;
         const bool floor_on = min_p > 0.f && !greedy;
@@ -964,17 +966,16 @@ struct Sampler {
         c.cut = -3.4e38f;
         if (!greedy && top > -INFINITY) {
             // log2(e) / t and M log2(e) / t as pairs of fp32
-            const float warm = fminf(t, 7e36f);
-            c.c_hi = __fdiv_rn(1.44269504f, warm);
-            c.c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c.c_hi, warm, 1.44269504f), 1.92596299e-8f), warm);
+            c.c_hi = __fdiv_rn(1.44269504f, t);
+            c.c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-c.c_hi, t, 1.44269504f), 1.92596299e-8f), t);
             const float h = __fmul_rn(top, c.c_hi);
             const bool far = !(fabsf(h) < 128.f);
             c.sub = far ? top : 0.f;
             c.a_hi = far ? 0.f : rintf(h * 65536.f) * (1.f / 65536.f);
             c.a_lo = far ? 0.f : __fadd_rn(__fsub_rn(h, c.a_hi), __fmaf_rn(top, c.c_lo, __fmaf_rn(top, c.c_hi, -h)));
-            c.cut = fmaxf((far ? 0.f : top) - 47.f / c.c_hi, -3.4e38f);
+            c.cut = (far ? 0.f : top) - 47.f / c.c_hi;
             // (a rank's place has nothing to do with the temperature, but does with the logits' scale)
-            c.bin_scale = kCoarse / (rank_on ? fmaxf(kSpan * warm, kRankSpan) : kSpan * warm);
+            c.bin_scale = kCoarse / (rank_on ? fmaxf(kSpan * t, kRankSpan) : kSpan * t);
             // the lowest logit whose e is at least min_p
             if (floor_on) c.low = __double2float_ru(static_cast<double>(top) + shared().min_shift);
         }

@@ -69,7 +69,7 @@ def kda_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
                stream=None):
     """Tokens drawn from logits [N, V] (bf16 or fp32; rows may be strided) by given uniforms u [N] fp32.
 
-    Per row, each [N] or None: ``temperature`` fp32 (0: the largest logit), ``top_k`` int32 (0: off), ``top_p`` fp32 (1: off),
+    Per row, each [N] or None: ``temperature`` fp32 (0: the largest logit; at most 1e30), ``top_k`` int32 (0: off), ``top_p`` fp32 (1: off),
     ``min_p`` fp32 (0: off), applied in this order; ties go to the lower index, and the token is the lowest kept index whose
     running mass exceeds u of the whole.  Returns token [N] int32 (-1 for a row without a finite logit), or ``(token, probs)``
     with ``return_probs`` or an output ``probs`` [N, V] (fp32, or the given tensor's bf16): the distribution that the token was

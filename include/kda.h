@@ -587,7 +587,7 @@ kda_status kda_prefix_attn(const void *q, kda_dtype dtype, const kda_paged_kv *p
  * token[n] is the lowest kept index i with sum_{kept j <= i} e_j > u[n] sum_{kept} e_j, and
  * probs[n] the kept e_i over their sum, zero elsewhere (and where fp32 has nothing so small): what
  * kda_draft_verify takes as target_probs or draft_probs.  A temperature that is not above 1e-30 (0, negative, NaN) takes the lowest index of
- * the largest logit.  -inf and NaN are never drawn; +inf counts as one value above all others.  A row
+ * the largest logit; one above 1e30 counts as 1e30.  -inf and NaN are never drawn; +inf counts as one value above all others.  A row
  * without any other logit gives token -1 and a distribution of zeros.  u is taken into [0, 1).
  *   logits  [N, V] dtype, row stride logits_stride elements (0: V)
  *   u       [N] fp32 (may be NULL without token)

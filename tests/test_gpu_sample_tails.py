@@ -73,3 +73,29 @@ def test_extreme_temperatures(kda):
                           torch.tensor([3e38, -3e38, 2.9e38, 0.0, -float("inf")]), torch.tensor([1e-30, 0.0, -1e-30, 2e-30, -5e-29])])
     for t in (1e-29, 1e-6, 1.0, 1e30):
         _probs(kda, logits, torch.float32, temperature=torch.full((4,), t))
+
+
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+def test_temperatures_without_bound(kda, dtype):
+    """Above 1e30 as at 1e30: ordinary logits are all alike, masked ones stay masked, whatever the row's largest is."""
+    low, inf, V = torch.finfo(dtype).min, float("inf"), 3001
+    gen = torch.Generator().manual_seed(3)
+    logits = torch.randn(6, V, generator=gen)
+    logits[1, 1::2] = low
+    logits[2] = low                     # all of them masked alike
+    logits[3] = low
+    logits[3, ::3] = -inf
+    logits[4] = -1e38
+    logits[4, ::2] = -inf
+    logits[5] *= 1e30
+    logits, u = logits.to(dtype), torch.linspace(0.053, 0.951, 6)
+    for t in (1e30, 3e36, 3e38, inf):
+        temperature = torch.full((6,), t)
+        for filters in ({}, dict(top_k=torch.full((6,), 500, dtype=torch.int32)), dict(top_p=torch.full((6,), 0.4)), dict(min_p=torch.full((6,), 0.5))):
+            counts = dict(filters, temperature=temperature.clamp(max=1e30))
+            want, p, margin = roll.sample(logits, u, **counts)
+            kw = {k: v.cuda() for k, v in filters.items()}
+            token, probs = kda.kda_sample(logits.cuda(), u.cuda(), temperature=temperature.cuda(), return_probs=True, **kw)
+            assert np.array_equal(token.cpu().numpy(), want) and margin.min() > 1e-9
+            assert np.all(np.abs(ref.np64(probs) - p) <= p * 8 * 2.0 ** -24 + 2.0 ** -149)
+    _probs(kda, logits, torch.bfloat16, temperature=torch.full((6,), 1e30))
