@@ -17,8 +17,10 @@
 //
 // Precision: the answers are whole numbers, so a rounding shows only next to a border, where a flat distribution over 10^5
 // tokens has one every 10^-5.  Masses are 64-bit integers in units of 2^-44 of the largest (2^-(63 - b) for 2^b tokens where b > 19):
-// their sums are exact, whatever the order, so that neither atomics nor the cluster's size change a result.  A mass itself is
-// 2^x, x = (l - M) log2(e) / t to about 2^-33, from a table of 2^(i/256) and a cubic: off by about 2e-10 of itself.
+// their sums are exact, whatever the order, so that neither atomics nor the cluster's size change a result.  What a mass is made
+// of is 2^x, x = (l - M) log2(e) / t to about 2^-33, from a table of 2^(i/256) and a cubic: off by about 2e-10 of itself.  Then it is
+// rounded to a unit, by 2^-45 of the largest up to 2^19 tokens: of a flat tail of V tokens that far down all may go the same
+// way, 2^-26 of the largest together at 2^19 and 2^-16 at 2^24 (64-bit sums have no room for finer units).
 //
 // The arithmetic of the masses bounds a call without top-k (30 operations per token, two tokens at a time where there are such instructions):
 // 512 rows of 131,072 in bf16 by temperature alone take 113 us (issue 57% busy, 1.2 TB/s).  With filters it is the steps between the passes as

@@ -586,17 +586,20 @@ kda_status kda_prefix_attn(const void *q, kda_dtype dtype, const kda_paged_kv *p
  *   min_p   of these, the e_i >= min_p (<= 0 or NaN: all; 1 or more: the largest only).
  * token[n] is the lowest kept index i with sum_{kept j <= i} e_j > u[n] sum_{kept} e_j, and
  * probs[n] the kept e_i over their sum, zero elsewhere (and where fp32 has nothing so small): what
- * kda_draft_verify takes as target_probs or draft_probs.  A temperature that is not above 1e-30 (0, negative, NaN) takes the lowest index of
- * the largest logit; one above 1e30 counts as 1e30.  -inf and NaN are never drawn; +inf counts as one value above all others.  A row
- * without any other logit gives token -1 and a distribution of zeros.  u is taken into [0, 1).
+ * kda_draft_verify takes as target_probs or draft_probs.  A temperature that is not above 1e-30 (0,
+ * negative, NaN) takes the lowest index of the largest logit; one above 1e30 counts as 1e30.  -inf
+ * and NaN are never drawn; +inf counts as one value above all others.  A row without any other
+ * logit gives token -1 and a distribution of zeros.  u is taken into [0, 1).
  *   logits  [N, V] dtype, row stride logits_stride elements (0: V)
  *   u       [N] fp32 (may be NULL without token)
  *   temperature, top_p, min_p [N] fp32, top_k [N] int32, each or NULL: 1, and no filter
  *   token   [N] int32 or NULL;  probs [N, V] of probs_dtype, row stride probs_stride (0: V), or NULL; one of
  *           them is given
- * Masses are carried to about 2e-10 of each token's and summed exactly, so a decision stands unless a number
- * lies that close to a border; tokens of less than 2^-45 of the largest have none.  The result does not depend
- * on the batch.  V: at most 2^24.
+ * The borders and the draw go by masses: whole numbers of 2^-44 of the largest for up to 2^19 tokens,
+ * of twice as much whenever V is twice as large.  Each is good to 2e-10 of itself and half a unit, and
+ * they are summed exactly.  So a decision stands unless a number lies within 2e-10 and V half units of
+ * a border (2^-26 of the largest at 2^19 tokens, 2^-16 at 2^24), and a token of less than half a unit
+ * is never drawn, though probs has its e.  The result does not depend on the batch.  V: at most 2^24.
  * Nothing to report from the device, so no workspace.
  */
 kda_status kda_sample(const void *logits, kda_dtype dtype, const float *u, const float *temperature,

@@ -1,4 +1,4 @@
-"""Probabilities of unlikely and masked tokens.
+"""Probabilities of unlikely and masked tokens, and what the integer masses leave of long tails.
 
 A probability is off by the roundings of its exponential (exp2f: two units in the last place, 4 half steps of fp32; what goes into it: a
 quarter), of the total and its inverse (2) and of their product (1), with 2e-10 and half a unit per token for the total (a quarter): 8 half
@@ -99,3 +99,22 @@ def test_temperatures_without_bound(kda, dtype):
             assert np.array_equal(token.cpu().numpy(), want) and margin.min() > 1e-9
             assert np.all(np.abs(ref.np64(probs) - p) <= p * 8 * 2.0 ** -24 + 2.0 ** -149)
     _probs(kda, logits, torch.bfloat16, temperature=torch.full((6,), 1e30))
+
+
+@pytest.mark.parametrize("V, depth", [((1 << 21) + 5, 25.0), ((1 << 21) + 5, 28.5), (1 << 19, 30.0), (1 << 24, 22.0)])
+def test_long_tails(kda, V, depth):
+    """One likely token and an equal tail far below it: a mass is good to 2e-10 of itself and half a unit, 2^-45 of the largest up to
+    2^19 tokens and twice as much whenever there are twice as many, and so is what the draws go by."""
+    half_unit = 2.0 ** -45 * 2.0 ** max(0, (V - 1).bit_length() - 19)
+    logits = torch.full((1, V), -depth)
+    logits[0, V // 3] = 0.0
+    e = np.full(V, np.exp(-depth))
+    e[V // 3] = 1.0
+    upto = np.cumsum(e)
+    slack = (2e-10 * upto[-1] + V * half_unit) * 2  # of the point and of the running mass
+    dev = logits.cuda()
+    for u in (1e-7, 3e-6, 0.5, 1 - 2.0 ** -16, 1 - 2.0 ** -20, 1 - 2.0 ** -24):
+        token, probs = kda.kda_sample(dev, torch.tensor([u], device="cuda"), return_probs=True)
+        i, point = int(token), float(np.float32(u)) * upto[-1]
+        assert upto[i] > point - slack and (upto[i - 1] if i else 0.0) <= point + slack
+    assert abs(float(probs.double().sum()) - 1) <= 8 * 2.0 ** -24 + slack
