@@ -22,6 +22,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_spec.cuh"
 
 namespace kda {
@@ -51,6 +53,7 @@ struct NormParams {
     bool wide_w, vec_w, vec_rows; // weights are fp32; weights, rows are 16-byte aligned
     float mscale, eps;
     float *part;                  // gradient: [CTA][d] sums of dw
+    int fold_at;                  // gradient: a thread's pairs of sums in shared memory, in floats (0: none, its rows are few)
 };
 
 // p w_j modulo one turn is exact in 64-bit fixed point; as in kda_rope.cu.
@@ -157,7 +160,23 @@ __device__ __forceinline__ uint4 load16(const T *row, int at, bool there) {
 
 extern __shared__ __align__(16) char norm_smem[];
 
-template <typename T, bool kInterleaved, bool kBwd>
+// A sum of fp32 numbers that keeps what its roundings leave out.
+struct Pair {
+    float high, low;
+    __device__ __forceinline__ void add(float x) {
+        const float s = __fadd_rn(high, x), b = __fsub_rn(s, high);
+        low = __fadd_rn(low, __fadd_rn(__fsub_rn(high, __fsub_rn(s, b)), __fsub_rn(x, b)));
+        high = s;
+    }
+};
+// Sums of dw: a thread adds up kChain rows or so plainly, then those sums as pairs, which lie in shared memory.  So their
+// error does not grow with the rows of a call; rows that are all alike, as a padded batch has them, took plain sums of some
+// thousand off by 400 to 730 units of 2^-24.  A call with fewer rows per thread has no pairs (16,384 tokens of 32 + 8 heads of
+// 128 make 72); 131,072 such tokens take 811 us with them and 793 without.
+constexpr int kChain = 128;
+
+// kFold: a gradient whose threads have more than kChain rows (as a variable in the same kernel it took the others from 111 to 114 us).
+template <typename T, bool kInterleaved, bool kBwd, bool kFold>
 __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm) norm_rope_kernel(const NormParams p) {
     constexpr int V = Elem<T>::kVec;
     const int half = p.rot / 2, pitch = table_pitch(p.rot);
@@ -205,6 +224,22 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm) no
     weights_at<V>(wa, p.w[which], p, c.a, c.has_a);
     weights_at<V>(wb, p.w[which], p, c.b, c.has_b);
     float da[V] = {}, db[V] = {};  // sums of dw
+    int chain = 0;                 // rows in them
+    // [2 V] pairs of this thread
+    auto folded = [&](int j) { return reinterpret_cast<Pair *>(reinterpret_cast<float *>(norm_smem) + p.fold_at) + j * kNormThreads + threadIdx.x; };
+    auto fold = [&] {
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) {
+            Pair s = *folded(j);
+            s.add(j < V ? da[j] : db[j - V]);
+            *folded(j) = s;
+            (j < V ? da[j] : db[j - V]) = 0.f;
+        }
+        chain = 0;
+    };
+    if constexpr (kFold) {
+        for (int j = 0; j < 2 * V; ++j) *folded(j) = Pair{0.f, 0.f};
+    }
     const float inv_d = 1.f / static_cast<float>(p.d);
     const int rounds = (H + share - 1) / share;  // heads of a group, the same for all lanes of a warp: the shuffles below are of whole warps
     __syncthreads();
@@ -265,6 +300,10 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm) no
                 y += step;
             }
             left -= kUnroll;
+            if constexpr (kFold) {
+                chain += kUnroll;
+                if (chain >= kChain) fold();
+            }
         }
         __syncthreads();
         t0 += blocks * tokens;
@@ -276,6 +315,14 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm) no
         // the groups' sums joined: groups of a warp by shuffles, warps through shared memory, in a fixed order
         float *sums = reinterpret_cast<float *>(norm_smem);  // [warps][d]
         const int warp = threadIdx.x >> 5;
+        if constexpr (kFold) {
+            fold();
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                da[j] = folded(j)->high + folded(j)->low;
+                db[j] = folded(V + j)->high + folded(V + j)->low;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j)
             for (int o = p.lanes; o < 32; o <<= 1) {
@@ -301,7 +348,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm) no
 // Any rotated width and alignment: a row staged in shared memory as fp32, its pairs shared out among its lanes.
 // Floats of a group of lanes in shared memory: rows, and as much as puts the groups of a warp next to one another in the banks (gradient of the
 // same 314 -> 278 us; fp32 heads of 64, 73 -> 55 and 171 -> 106).
-__host__ __device__ __forceinline__ int staged_span(bool bwd, int d, int lanes) { return (bwd ? 3 : 1) * d + (lanes & 31); }
+__host__ __device__ __forceinline__ int staged_span(bool bwd, bool fold, int d, int lanes) { return (!bwd ? 1 : fold ? 5 : 3) * d + (lanes & 31); }
 
 template <typename T, bool kInterleaved, bool kBwd>
 __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const NormParams p) {
@@ -314,14 +361,26 @@ __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const 
     uint64_t *turn = reinterpret_cast<uint64_t *>(norm_smem);
     float *cs = reinterpret_cast<float *>(turn + ((half + 1) & ~1)), *sn = cs + tokens * pitch;
     float *w = sn + tokens * pitch;                          // [d]
-    const int span = staged_span(kBwd, d, p.lanes);
-    float *mine = w + d + group * span;                      // the group's rows: x, g, sums of dw
-    float *mine_g = mine + d, *dw = mine + 2 * d;
+    const bool pairs = kBwd && p.fold_at;
+    const int span = staged_span(kBwd, pairs, d, p.lanes);
+    float *mine = w + d + group * span;                      // the group's rows: x, g, sums of dw, [d] pairs of such sums
+    float *mine_g = mine + d, *dw = mine + 2 * d, *folded = dw + d;
+    int chain = 0;                                           // rows in dw
+    auto fold = [&] {
+        for (int i = lane; i < d; i += p.lanes) {
+            Pair s{folded[i], folded[d + i]};
+            s.add(dw[i]);
+            folded[i] = s.high;
+            folded[d + i] = s.low;
+            dw[i] = 0.f;
+        }
+        chain = 0;
+    };
     grid_wait();
     make_turns(turn, p, kStagedThreads);
     for (int i = threadIdx.x; i < d; i += kStagedThreads) w[i] = weight_at(p.w[which], p.wide_w, i);
     if constexpr (kBwd)
-        for (int i = lane; i < d; i += p.lanes) dw[i] = 0.f;
+        for (int i = lane; i < (pairs ? 3 : 1) * d; i += p.lanes) dw[i] = 0.f;
     const float inv_d = 1.f / static_cast<float>(d);
     const T *x = static_cast<const T *>(p.x[which]), *g = static_cast<const T *>(p.g[which]);
     T *y = static_cast<T *>(p.y[which]);
@@ -428,7 +487,12 @@ __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const 
                     for (int i = lane; i < d; i += p.lanes) row[i] = Elem<T>::from_f(mine[i]);
                 }
             }
+            if (pairs && ++chain >= kChain) fold();  // (a lane has the same channels throughout)
             __syncwarp();
+        }
+        if (pairs && t0 + blocks * tokens >= p.T) {
+            fold();
+            for (int i = lane; i < d; i += p.lanes) dw[i] = folded[i] + folded[d + i];
         }
         __syncthreads();
     }
@@ -444,14 +508,6 @@ __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const 
 
 // dw from the CTAs' sums: 32 channels of q or k per CTA, 32 warps that take every 32nd sum (eight: 1 us longer).  Sums are pairs
 // of fp32: chains of some hundred plain additions lost as much as the threads' own (fp64 took 6 us longer).
-struct Pair {
-    float high, low;
-    __device__ __forceinline__ void add(float x) {
-        const float s = __fadd_rn(high, x), b = __fsub_rn(s, high);
-        low = __fadd_rn(low, __fadd_rn(__fsub_rn(high, __fsub_rn(s, b)), __fsub_rn(x, b)));
-        high = s;
-    }
-};
 constexpr int kWeightWarps = 32;
 __global__ void __launch_bounds__(32 * kWeightWarps) norm_weights_kernel(const float *part, int64_t blocks_q, int64_t blocks_k, int d, float *dq, float *dk) {
     __shared__ Pair share[kWeightWarps][33];
@@ -499,6 +555,7 @@ kda_status launch(NormParams p, bool columns, float *dwq, float *dwk, cudaStream
     const int heads = static_cast<int>(part < 1 ? 1 : part > kRounds ? kRounds : part);
     const int64_t most_tokens = p.rot > 0 ? 8192 / p.rot : 64;     // 32 KB of sines and cosines
     int tokens = 1;
+    bool fold = false;
     for (int i = 0; i < 2; ++i) {
         p.share[i] = 1;
         if (p.H[i] == 0) {
@@ -520,6 +577,9 @@ kda_status launch(NormParams p, bool columns, float *dwq, float *dwk, cudaStream
             int64_t share_i = most_ctas(sms, columns) * p.H[i] / (p.H[0] + p.H[1]);
             share_i = share_i < 1 ? 1 : share_i;
             p.blocks[i] = p.blocks[i] < share_i ? p.blocks[i] : share_i;
+            // rows of a group of lanes
+            const int64_t rounds = groups_of(groups_of(p.T, p.tokens[i]), static_cast<int>(p.blocks[i]));
+            fold |= rounds * (columns ? groups_of(p.H[i], p.share[i]) : groups_of(static_cast<int64_t>(p.tokens[i]) * p.H[i], groups)) > kChain;
         }
     }
     if (p.blocks[0] + p.blocks[1] > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
@@ -529,11 +589,19 @@ kda_status launch(NormParams p, bool columns, float *dwq, float *dwk, cudaStream
     if (columns) {
         const size_t sums = kBwd ? static_cast<size_t>(kNormThreads / 32) * p.d * 4 : 0;
         smem = smem > sums ? smem : sums;
-        if (!smem_opt_in<norm_rope_kernel<T, kInterleaved, kBwd>>(64 * 1024)) return KDA_ERR_CUDA;
-        if (launch_after(norm_rope_kernel<T, kInterleaved, kBwd>, dim3(grid), kNormThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
+        if (fold) {
+            p.fold_at = static_cast<int>(smem / 4);
+            smem += 2 * V * kNormThreads * sizeof(Pair);
+        }
+        auto go = [&](auto folds) {
+            constexpr auto kernel = norm_rope_kernel<T, kInterleaved, kBwd, decltype(folds)::value>;
+            return smem_opt_in<kernel>(64 * 1024) && launch_after(kernel, dim3(grid), kNormThreads, smem, s, p) == cudaSuccess;
+        };
+        if (!(fold ? go(std::bool_constant<kBwd>{}) : go(std::false_type{}))) return KDA_ERR_CUDA;
     } else {
-        smem += (static_cast<size_t>(p.d) + static_cast<size_t>(groups) * staged_span(kBwd, p.d, p.lanes)) * 4;
-        if (!smem_opt_in<norm_rope_staged_kernel<T, kInterleaved, kBwd>>(112 * 1024)) return KDA_ERR_CUDA;
+        p.fold_at = fold ? 1 : 0;
+        smem += (static_cast<size_t>(p.d) + static_cast<size_t>(groups) * staged_span(kBwd, fold, p.d, p.lanes)) * 4;
+        if (!smem_opt_in<norm_rope_staged_kernel<T, kInterleaved, kBwd>>(128 * 1024)) return KDA_ERR_CUDA;
         if (launch_after(norm_rope_staged_kernel<T, kInterleaved, kBwd>, dim3(grid), kStagedThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
     }
     if (kBwd && (dwq || dwk)) {

@@ -530,7 +530,8 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
  *
  * kda_norm_rope_bwd is the gradient: from q, k (the inputs of the forward) and the gradients
  * of its outputs to d_q, d_k and, where not NULL, d_q_weight, d_k_weight [d] fp32 (sums over
- * all tokens and heads, in a fixed order; always fp32, as a sum of T * H terms needs them).
+ * all tokens and heads, in a fixed order; always fp32, as a sum of T * H terms needs them, and
+ * with an error that does not grow with T * H).
  * d_q may be d_q_out or q itself (same stride), d_k likewise.
  * workspace: >= kda_norm_rope_bwd_workspace_size(d) bytes, 16-byte aligned; nothing to report
  * from the device.

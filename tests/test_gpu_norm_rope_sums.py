@@ -1,0 +1,80 @@
+"""The gradient of the norms' weights: every row counts, and its error does not grow with the number of rows.
+
+A term is off by 40 half steps u = 2^-24 of fp32 (test_gpu_norm_rope.py).  A thread adds up at most 130 of them plainly, in whatever direction
+their roundings go; a CTA's threads make 20 additions more, and joining those sums is exact to a few u: 200 u of the sum of magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _rollout_reference as roll
+from tests import _spec_reference as ref
+from tests._helpers import ensure_built
+
+pytestmark = pytest.mark.gpu
+U = roll.U
+
+
+@pytest.fixture(scope="module")
+def kda():
+    ensure_built()
+    import gated_linear_attention_chunk_gb300 as m
+    return m
+
+
+# few tokens of many heads, and many tokens of few: long sums of one thread (60 of 64 channels turned, or 126 of 128: rows through shared memory)
+LONG = [(2, 65536, 0, 64, 64), (2, 40000, 20000, 64, 60), (300000, 4, 1, 64, 64), (250001, 2, 2, 64, 60), (3, 9000, 0, 1024, 1010)]
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,rot", LONG)
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+def test_long_sums_of_equal_rows(kda, T, Hq, Hk, d, rot, dtype):
+    """Rows that are all alike, so that a plain sum's roundings all go one way."""
+    gen = torch.Generator().manual_seed(T + d)
+    freq, m = kda.rope_frequencies(rot)
+    pos = torch.full((1,), 77, dtype=torch.int32)
+    row, g = torch.randn(1, 1, d, generator=gen).to(dtype), torch.randn(1, 1, d, generator=gen).to(dtype)
+    w = (1 + 0.3 * torch.randn(d, generator=gen)).to(dtype)
+    _, dw, _, size = roll.norm_rope_bwd(row, w, g, pos.numpy(), freq.cpu().numpy(), 1e-6, False, m)
+    heads = lambda x, H: x.cuda().expand(T, H, d).contiguous() if H else None  # noqa: E731
+    wk = w.cuda() if Hk else None
+    got = kda.kda_norm_rope_bwd(heads(row, Hq), heads(row, Hk), heads(g, Hq), heads(g, Hk), pos.cuda().expand(T).contiguous(), freq, w.cuda(), wk)
+    for out, H in ((got[2], Hq), (got[3], Hk)):
+        if H:
+            off = np.abs(ref.np64(out) - T * H * dw) / (T * H * size)
+            assert off.max() <= 200 * U, float(off.max() / U)
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,rot", [(2500, 12, 4, 64, 32), (2501, 7, 3, 128, 128), (1217, 5, 2, 128, 126), (4099, 1, 1, 256, 64), (70001, 2, 1, 64, 60)])
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+def test_every_token_counts(kda, T, Hq, Hk, d, rot, dtype):
+    """One token alone has a gradient, the last one or one in between: dw is what that token alone gives."""
+    gen = torch.Generator().manual_seed(T)
+    x = [torch.randn(T, h, d, generator=gen).to(dtype) for h in (Hq, Hk)]
+    pos = torch.randint(0, 5000, (T,), generator=gen, dtype=torch.int32)
+    w = (1 + 0.3 * torch.randn(d, generator=gen)).to(dtype)
+    freq, m = kda.rope_frequencies(rot)
+    dev = [t.cuda() for t in x]
+    for t in (T - 1, T - 2, T // 2 + 1, T // 3, 0):
+        g = [torch.zeros(T, h, d, dtype=dtype) for h in (Hq, Hk)]
+        for y in g:
+            y[t] = torch.randn(y.shape[1], d, generator=gen).to(dtype)
+        got = kda.kda_norm_rope_bwd(*dev, g[0].cuda(), g[1].cuda(), pos.cuda(), freq, w.cuda(), w.cuda())
+        for i in range(2):
+            dx, dw, _, size = roll.norm_rope_bwd(x[i][t:t + 1], w, g[i][t:t + 1], pos[t:t + 1].numpy(), freq.cpu().numpy(), 1e-6, False, m)
+            assert np.all(np.abs(ref.np64(got[2 + i]) - dw) <= 200 * U * size)
+            assert not bool(got[i][:t].any()) and not bool(got[i][t + 1:].any()) and bool(got[i][t].any())
+
+
+def test_random_rows_by_the_norm_of_the_gradient(kda):
+    """A thread's sums over 30,000 random rows: errors of random sign, 8 u of the root of the sum of squares per channel with room to spare; a
+    row left out would be 2^16 u of it."""
+    T, Hq, Hk, d = 2500, 12, 4, 64
+    gen = torch.Generator().manual_seed(5)
+    x, g = ([torch.randn(T, h, d, generator=gen) for h in (Hq, Hk)] for _ in "xg")
+    pos = torch.randint(0, 5000, (T,), generator=gen, dtype=torch.int32)
+    w = 1 + 0.3 * torch.randn(d, generator=gen)
+    freq, m = kda.rope_frequencies(32)
+    got = kda.kda_norm_rope_bwd(*(t.cuda() for t in (*x, *g)), pos.cuda(), freq, w.cuda(), w.cuda(), interleaved=True)
+    for i in range(2):
+        _, dw, _, _ = roll.norm_rope_bwd(x[i], w, g[i], pos.numpy(), freq.cpu().numpy(), 1e-6, True, m)
+        assert np.linalg.norm(ref.np64(got[2 + i]) - dw) <= 1e-6 * np.linalg.norm(dw)
