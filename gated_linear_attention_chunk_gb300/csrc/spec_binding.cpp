@@ -338,6 +338,7 @@ PyObject *norm_rope(PyObject *const *a) {
     const int64_t qs = token_stride(q, "q", q.scalar_type(), T, Hq, d);
     const bool backward = !absent(a[2]), has_k = !absent(a[1]);
     if (has_k != !absent(a[3]) && backward) value_error("k and d_k_out go together");
+    if (!has_k && (!absent(a[12]) || !absent(a[14]))) value_error("an output for k without k");
     const c10::cuda::CUDAGuard guard(q.device());
     Rows k, gq, gk, yq, yk;
     int64_t Hk = 0;

@@ -1,4 +1,4 @@
-"""The gradient of the norms' weights: every row counts, and its error does not grow with the number of rows.
+"""The gradient of the norms' weights: every row counts, its error does not grow with the number of rows, and none is left unwritten.
 
 A term is off by 40 half steps u = 2^-24 of fp32 (test_gpu_norm_rope.py).  A thread adds up at most 130 of them plainly, in whatever direction
 their roundings go; a CTA's threads make 20 additions more, and joining those sums is exact to a few u: 200 u of the sum of magnitudes."""
@@ -78,3 +78,15 @@ def test_random_rows_by_the_norm_of_the_gradient(kda):
     for i in range(2):
         _, dw, _, _ = roll.norm_rope_bwd(x[i], w, g[i], pos.numpy(), freq.cpu().numpy(), 1e-6, True, m)
         assert np.linalg.norm(ref.np64(got[2 + i]) - dw) <= 1e-6 * np.linalg.norm(dw)
+
+
+def test_outputs_for_an_absent_k_are_refused(kda):
+    """Without k there is nothing to write into them: they would stay as they were."""
+    q, pos = torch.randn(4, 2, 64, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda")
+    freq, _ = kda.rope_frequencies(64)
+    held = torch.full((4, 2, 64), 7.0, device="cuda")
+    with pytest.raises(ValueError):
+        kda.kda_norm_rope(q, None, pos, freq, k_out=held)
+    for bad in (dict(d_k=held), dict(d_k_weight=held[0, 0].contiguous())):
+        with pytest.raises(ValueError):
+            kda.kda_norm_rope_bwd(q, None, q, None, pos, freq, **bad)
