@@ -103,8 +103,19 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control &c)
     }
     return true;
 }
+// By a converged warp, whose lanes stay together also where it gives up: instructions and searches of whole warps follow.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Control &c) {
-    return __all_sync(0xffffffffu, wait(bar, parity, c));
+    long long t0 = 0;
+    for (uint32_t spins = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++spins) {
+        if (spins & 63u) continue;
+        const long long now = clock64();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&c.abort) || now - t0 > kPatience)) {
+            *reinterpret_cast<volatile int *>(&c.abort) = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // 32 columns of this thread's TMEM lane.  The registers are not to be touched before landed32.
@@ -548,7 +559,7 @@ __device__ void softmax(const TcParams &a, SegmentWalk w, Control &c, uint32_t t
 #pragma unroll
                 for (int i = 0; i < 4; ++i) bits[i] = __ballot_sync(0xffffffffu, place[i] < keys);
             }
-            if (!wait(&c.s_full[s], s_uses++ & 1, c)) return;
+            if (!wait_warp(&c.s_full[s], s_uses++ & 1, c)) return;
             tc_fence_after();
             uint32_t pk[2][32];
             Step st;
@@ -602,10 +613,10 @@ __device__ void softmax(const TcParams &a, SegmentWalk w, Control &c, uint32_t t
         float f0 = 1.f, f1 = 0.f;
         if (!pair) {
             // (every thread is done with the segment before, whose values lie there)
-            if (segment > 0 && !wait(&c.o_empty, (segment - 1) & 1, c)) return;
+            if (segment > 0 && !wait_warp(&c.o_empty, (segment - 1) & 1, c)) return;
             c.x[s][row] = make_float2(ref, first < nt ? sum : 0.f);
             mbar_arrive(&c.x_full);
-            if (!wait(&c.x_full, x_uses++ & 1, c)) return;
+            if (!wait_warp(&c.x_full, x_uses++ & 1, c)) return;
             const float2 x0 = c.x[0][row], x1 = c.x[1][row];
             ref = x1.y != 0.f && (x0.y == 0.f || x1.x > x0.x) ? x1.x : x0.x;
             f0 = x0.y != 0.f ? ex2(x0.x - ref) : 0.f;
@@ -616,10 +627,10 @@ __device__ void softmax(const TcParams &a, SegmentWalk w, Control &c, uint32_t t
         }
         const int cols = pair ? DV : DV / 2;
         if (pair) {
-            if (!wait(&c.o_full[s], o_uses[s]++ & 1, c)) return;
+            if (!wait_warp(&c.o_full[s], o_uses[s]++ & 1, c)) return;
         } else {
-            if (!wait(&c.o_full[0], o_uses[0]++ & 1, c)) return;
-            if (nt > 1 && !wait(&c.o_full[1], o_uses[1]++ & 1, c)) return;
+            if (!wait_warp(&c.o_full[0], o_uses[0]++ & 1, c)) return;
+            if (nt > 1 && !wait_warp(&c.o_full[1], o_uses[1]++ & 1, c)) return;
         }
         if (pair) ++o_uses[s ^ 1];
         tc_fence_after();
@@ -671,10 +682,10 @@ __device__ void softmax(const TcParams &a, SegmentWalk w, Control &c, uint32_t t
         tc_fence_before();
         mbar_arrive(&c.o_empty);
         if (live && !w.whole && c0 == 0) p.part_ml[slot] = make_float2(ref, err ? -1.f : sum);
-        if (live && w.whole && p.lse && c0 == 0) {
+        if (w.whole && p.lse && c0 == 0) {
             // in a small block two threads read lse_tail, which may be lse
-            if (!pair && !wait(&c.o_empty, segment & 1, c)) return;
-            p.lse[out] = j.lse;
+            if (!pair && !wait_warp(&c.o_empty, segment & 1, c)) return;
+            if (live) p.lse[out] = j.lse;
         }
     }
 }
