@@ -736,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (has_holes(a)) {  // rows between pages stay as they are: zeros
         for (int i = threadIdx.x; i < S::kSlots * S::kSlot / 16; i += kThreads)
             reinterpret_cast<uint4 *>(raw + 2 * S::kQ)[i] = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
     }
+    fence_proxy_async_smem();  // these zeros, and the plan's scratch, lie where copies will write
     if (warp == kSoftmaxWarps + 1) {
         tmem_alloc(&c.tmem, 512);
         tmem_relinquish();
