@@ -86,17 +86,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// A wait that ends after about 2 s (4e9 clocks, counted from the 64th look), or once another role has given up.
+// A wait that ends after about 2 s (4e9 clocks, counted from the 64th look), or once another role has given up.  By a converged
+// warp, whose lanes stay together also where it gives up: instructions of whole warps follow.
 constexpr long long kPatience = 4000000000ll;
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Control &c, uint32_t *status) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Control &c, uint32_t *status) {
     long long t0 = 0;
-    for (uint32_t spins = 1; !mbar_try_wait(bar, parity); ++spins) {
+    for (uint32_t spins = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++spins) {
         if (spins & 63u) continue;
-        if (*reinterpret_cast<volatile int *>(&c.abort)) return false;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&c.abort))) return false;
         const long long now = clock64();
         if (t0 == 0) t0 = now;
-        if (now - t0 > kPatience) {
+        if (__any_sync(0xffffffffu, now - t0 > kPatience)) {
             *reinterpret_cast<volatile int *>(&c.abort) = 1;
             atomicOr(status, static_cast<uint32_t>(DEV_ERR_TIMEOUT));
             return false;
@@ -232,7 +232,7 @@ __device__ void fill(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t 
         // the query rows
         for (int s = 0; s < (w.pair ? 2 : 1); ++s) {
             const int b = w.pair ? s : (alone & 1);
-            if (!wait(&c.q_empty[b], (q_uses[b] & 1) ^ 1, c, p.status)) return;
+            if (!wait_warp(&c.q_empty[b], (q_uses[b] & 1) ^ 1, c, p.status)) return;
             ++q_uses[b];
             const int r = (2 * w.group + s) * kTcRows + mine;
             uint64_t a = 0;
@@ -271,14 +271,14 @@ __device__ void fill(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t 
             // V of tile t - lead, then K of tile t
             if (t >= lead) {
                 const uint32_t slot = item % S::kSlots;
-                if (!wait(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1, c, p.status)) return;
+                if (!wait_warp(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1, c, p.status)) return;
                 copy_rows<DV>(ring + slot * S::kSlot, lead == 1 ? v_wait[0] : v_wait[1], warp, lane, p.q);
                 arrive_landed(&c.full[slot]);
                 ++item;
             }
             if (t < w.ntiles) {
                 const uint32_t slot = item % S::kSlots;
-                if (!wait(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1, c, p.status)) return;
+                if (!wait_warp(&c.empty[slot], ((item / S::kSlots) & 1) ^ 1, c, p.status)) return;
                 copy_rows<DK>(ring + slot * S::kSlot, k_row, warp, lane, p.q);
                 arrive_landed(&c.full[slot]);
                 ++item;
@@ -301,9 +301,6 @@ __device__ __forceinline__ void mma_bf16_ss_warp(uint32_t d_tmem, uint64_t adesc
         "setp.ne.b32 p, %4, 0;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Control &c, uint32_t *status) {
-    return __all_sync(0xffffffffu, wait(bar, parity, c, status));
 }
 template <int DK, int DV>
 __device__ void issue(const AttnParams &p, Control &c, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
@@ -435,7 +432,7 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
             const bool ragged = drafted || count < kTcKeys;
             uint64_t sees = ~0ull;
             if (drafted) sees = __ldg(p.sees + w.t0 + node);
-            if (!wait(&c.s_full[s], s_uses++ & 1, c, p.status)) return;
+            if (!wait_warp(&c.s_full[s], s_uses++ & 1, c, p.status)) return;
             tc_fence_after();
             // the row's scores, all in registers
             uint32_t v[kTcKeys];
@@ -512,7 +509,7 @@ __device__ void softmax(const AttnParams &p, Control &c, uint32_t tmem) {
         }
         const bool any = t_first < w.ntiles;
         if (any) {
-            if (!wait(&c.o_full[s], o_uses++ & 1, c, p.status)) return;
+            if (!wait_warp(&c.o_full[s], o_uses++ & 1, c, p.status)) return;
             tc_fence_after();
         }
         uint32_t err = flag;

@@ -18,7 +18,7 @@ def _body(text, head):
             return text[at:i]
 
 
-@pytest.mark.parametrize("name, role", [("kda_prefix_attn_tc.cu", "softmax"), ("kda_prefix_attn_tc.cu", "fill")])
+@pytest.mark.parametrize("name, role", [(name, role) for name in ("kda_prefix_attn_tc.cu", "kda_tree_attn_tc.cu") for role in ("softmax", "fill")])
 def test_no_lane_leaves_alone(name, role):
     with open(os.path.join(CSRC, name)) as f:
         body = _body(f.read(), r"__device__ \w+ " + role + r"\(")
