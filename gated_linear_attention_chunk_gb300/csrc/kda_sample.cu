@@ -772,7 +772,7 @@ struct Sampler {
         }
     }
 
-    // A token's e below c.cut, where a mass ends, times a factor of at most 1.  x = (l - M) log2(e) / t as a pair: l - M is rounded, and what that
+    // A token's e times a factor of at most 1, wherever the token lies: x = (l - M) log2(e) / t as a pair, of which l - M is rounded, and what that
     // leaves out is exact.  Below half of fp32's smallest number it is 0, as for a masked token.
     __device__ __forceinline__ float faint(float l, float factor) const {
         const float d = __fsub_rn(l, c.top), v = __fsub_rn(d, l), d_lo = __fsub_rn(__fsub_rn(l, __fsub_rn(d, v)), __fadd_rn(c.top, v));
@@ -784,7 +784,8 @@ struct Sampler {
         return exp2f((h - n) + lo) * factor * 5.42101086e-20f * scale;
     }
     // The distribution: tokens up to the limit have e / total, the others none.  Element by element, so that a warp's stores
-    // are consecutive whatever the row's alignment.
+    // are consecutive whatever the row's alignment; two at a time, as there are such instructions.  The last step: c.cut goes down to where the
+    // exponentials end (125 halvings below M, or 63 where l - sub is exact no further); what lies below is faint.
     __device__ void write(int64_t row_at, uint64_t limit, float inv_total) {
         const int64_t first = static_cast<int64_t>(col0) * W - shift;
         const int from = static_cast<int>(first < 0 ? 0 : first);
@@ -794,14 +795,35 @@ struct Sampler {
         __nv_bfloat16 *narrow = static_cast<__nv_bfloat16 *>(p.probs) + row_at * p.ps;
         const float least_kept = logit_of(limit);  // (a NaN where there is no limit: every logit is then kept)
         const uint32_t last_kept = static_cast<uint32_t>(limit);
-        for (int i = from + threadIdx.x; i < to; i += kThreads) {
-            float l = Elem<T>::to_f(row[i]);
-            if (inf_top) l = l == INFINITY ? 0.f : -INFINITY;
-            float x = 0.f;
-            if (l > -INFINITY && !(l < least_kept) && (l != least_kept || static_cast<uint32_t>(i) <= last_kept))
-                x = l - c.sub < c.cut ? faint(l, inv_total) : both(exp2_parts(l, l, c, shared().table).value).x * inv_total;
-            if (p.wide_probs) wide[i] = x;
-            else narrow[i] = __float2bfloat16_rn(x);
+        c.cut = c.sub != 0.f ? -63.f / c.c_hi : c.top - 125.f / c.c_hi;
+        for (int i0 = from + threadIdx.x; i0 < to; i0 += 2 * kThreads) {
+            float l[2], x[2];
+            bool kept[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = i0 + j * kThreads;
+                l[j] = i < to ? Elem<T>::to_f(row[i]) : -INFINITY;
+                if (inf_top) l[j] = l[j] == INFINITY ? 0.f : -INFINITY;
+                kept[j] = l[j] > -INFINITY && !(l[j] < least_kept) && (l[j] != least_kept || static_cast<uint32_t>(i) <= last_kept);
+            }
+            x[0] = x[1] = 0.f;
+            if (kept[0] || kept[1]) {
+                const float2 e = both(exp2_parts(l[0], l[1], c, shared().table).value);
+                x[0] = e.x * inv_total;
+                x[1] = e.y * inv_total;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!kept[j]) x[j] = 0.f;
+                    else if (l[j] - c.sub < c.cut) x[j] = faint(l[j], inv_total);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = i0 + j * kThreads;
+                if (i >= to) break;
+                if (p.wide_probs) wide[i] = x[j];
+                else narrow[i] = __float2bfloat16_rn(x[j]);
+            }
         }
     }
 
