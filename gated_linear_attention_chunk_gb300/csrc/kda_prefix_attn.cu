@@ -30,7 +30,7 @@ constexpr int kSmsAtMost = 160;  // what the workspace allows for
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefixParams p) {
     __shared__ PlanScratch scratch;
     grid_go();
-    make_plan(p, scratch, nullptr);
+    make_plan(p, scratch);
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -68,14 +68,13 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const PrefixParams 
     static_assert(sizeof(PlanScratch) <= L::kFloats * 4, "the plan's scratch lies over the tiles");
     grid_wait();
     grid_go();
-    __shared__ GroupInfo near[kNearGroups + 1];
-    const GroupInfo *info = p.planned ? p.info : make_plan(p, *reinterpret_cast<PlanScratch *>(smem), near);
+    if (!p.planned) make_plan(p, *reinterpret_cast<PlanScratch *>(smem));
     uint32_t met = 0;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const float c2 = p.scale * kLog2e;
     const T *kbase = reinterpret_cast<const T *>(p.c.k), *vbase = reinterpret_cast<const T *>(p.c.v), *base = static_cast<const T *>(p.q);
     SegmentWalk w;
-    for (w.start(p, info); w.live(); w.next(p)) {
+    for (w.start(p); w.live(); w.next(p)) {
         const int64_t rows = static_cast<int64_t>(w.tokens) * p.G, r0 = static_cast<int64_t>(w.block) * kRows;
         // A tile's rows are looked up while the one before is worked on, and its keys, and values where they have a place, copied ahead.  (16 prompts of up
         // to 4,096, 16 samples each, 32 / 8 heads of 64: 192 us where they are waited for one after the other, 153 so; of 128, 332 and 256.)

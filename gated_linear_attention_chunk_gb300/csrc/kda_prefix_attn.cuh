@@ -66,8 +66,10 @@ __host__ __device__ inline int tiles_of_len(const PrefixParams &p, int len) {
 // Work is cut into parts where blocks share so many tiles of keys (64 KB each) that L2 does not keep them from one block to the next.
 constexpr int64_t kShared = 1024;
 constexpr int kPartCost = 4, kUnitCost = 4;  // tiles
-constexpr int kPlanGroups = 256;  // up to so many groups the kernels plan themselves, which spares a launch
-constexpr int kNearGroups = 16;   // up to so many the plan is read in shared memory: three reads from L2 come before a segment's first copy otherwise
+// Up to so many groups the kernels plan themselves, which spares a launch: 65,536 keys of 8 heads, eight tokens per group, in 2 to 16 groups 63 to 65
+// us and 69 with the launch, in 64 groups 90 and 94, in 256 173 and 191 (256 groups of two tokens and 128 keys 116 and 108, of four and 1,000 296 and 290).
+// Reading the plan from L2 is as fast as from shared memory (one group of 2,048 keys 22.4 us either way, 16 of 4,096 64.6).
+constexpr int kPlanGroups = 256;
 
 // What the plan of a CTA of whole warps, kPlanGroups threads at least, needs in shared memory.
 struct PlanScratch {
@@ -81,16 +83,10 @@ struct PlanScratch {
     int tiles[kPlanGroups], blocks[kPlanGroups];
 };
 
-// Checks the lengths, numbers the steps and chooses the cut; by all threads of a CTA.  Up to kNearGroups groups each CTA writes its own `near`
-// [kNearGroups + 1], and the first one p.info; otherwise p.info alone is written, each entry once, by every CTA with the same.  Returns where this CTA
-// finds it.
-__device__ inline const GroupInfo *make_plan(const PrefixParams &p, PlanScratch &s, GroupInfo *near) {
+// Checks the lengths, numbers the steps and chooses the cut; by all threads of a CTA.  Each entry of p.info is written once, by every CTA that plans
+// with the same.
+__device__ inline void make_plan(const PrefixParams &p, PlanScratch &s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
-    if (p.N > kNearGroups) near = nullptr;
-    auto put = [&](int g, const GroupInfo &x) {
-        if (near) near[g] = x;
-        if (!near || blockIdx.x == 0) p.info[g] = x;
-    };
     if (threadIdx.x == 0) {
         s.base = s.shared_tiles = s.all_tiles = 0;
         s.errors = 0;
@@ -167,7 +163,7 @@ __device__ inline const GroupInfo *make_plan(const PrefixParams &p, PlanScratch 
         for (int w = 0; w < warp; ++w) off += s.warp_sum[w];
         if (g < p.N) {
             x.step0 = off + upto - steps;
-            put(g, x);
+            p.info[g] = x;
         }
         __syncthreads();
         if (threadIdx.x == threads - 1) s.base = off + upto;
@@ -179,10 +175,9 @@ __device__ inline const GroupInfo *make_plan(const PrefixParams &p, PlanScratch 
         x.step0 = s.base;
         x.parts = by_parts ? 1 : 0;
         x.blocks = lead;
-        put(p.N, x);
+        p.info[p.N] = x;
     }
     __syncthreads();
-    return near ? near : p.info;
 }
 
 // The steps of a CTA begin at first_step(c); cta_of is the CTA that has a step.
@@ -191,7 +186,6 @@ __device__ __forceinline__ int cta_of(int64_t total, int64_t step, int ctas) { r
 
 // A CTA's walk over its segments: runs of steps within one unit, those with keys.
 struct SegmentWalk {
-    const GroupInfo *info;
     int64_t next_step, end, begin;
     int lead;                    // steps without keys at the beginning of a unit
     bool by_parts, is_live;
@@ -201,9 +195,8 @@ struct SegmentWalk {
     int slot;
 
     // Every lane of a converged warp.
-    __device__ __forceinline__ void start(const PrefixParams &p, const GroupInfo *plan) {
-        info = plan;
-        const GroupInfo all = info[p.N];
+    __device__ __forceinline__ void start(const PrefixParams &p) {
+        const GroupInfo all = p.info[p.N];
         by_parts = all.parts != 0;
         lead = all.blocks;
         begin = next_step = by_parts ? blockIdx.x : first_step(all.step0, blockIdx.x, p.ctas);
@@ -221,8 +214,8 @@ struct SegmentWalk {
     __device__ __forceinline__ void enter(const PrefixParams &p) {
         const int64_t at = next_step;
         // (groups without steps begin where the next one does: the last of them has it)
-        g = warp_find([&](int i) { return info[i].step0; }, p.N, at);
-        const GroupInfo s = info[g];
+        g = warp_find([&](int i) { return p.info[i].step0; }, p.N, at);
+        const GroupInfo s = p.info[g];
         t0 = s.t0; tokens = s.tokens; len = s.len; tiles = s.tiles;
         if (by_parts) {
             const int off = static_cast<int>(at - s.step0), rest = off / s.blocks;

@@ -24,7 +24,7 @@
 //
 // Of 112k clocks of a CTA of the rollout case (16 prompts, 68 us) 23k go by before its first scores: 9k until lengths are read and the plan is
 // made, the rest the first walk, copies and products, code that no cache has yet as much as data.  So the launch may begin before the one ahead
-// of it has ended (26 -> 21 us for one prompt together with the next two), the plan is read in shared memory, and the first segment is looked up
+// of it has ended (26 -> 21 us for one prompt together with the next), and the first segment is looked up
 // once for all warps.  A step of two streams takes 3,050 clocks, of which the tensor cores work 1,800; issuing from two warps was slower (the
 // streams fell into step).
 //
@@ -60,7 +60,6 @@ struct Control {
     int abort, bad_seen;         // a role gave up; a page was out of range
     uint32_t bad_segment[8];     // [n % 8]: n + 1, if segment n has such a page (the filling side is less than eight segments ahead)
     float2 x[2][kRow];           // a small block: both streams' references and sums
-    GroupInfo near[kNearGroups + 1];
 };
 
 template <int DK, int DV>
@@ -707,9 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     grid_wait();
     grid_go();
-    const GroupInfo *info = p.planned ? p.info : make_plan(p, *reinterpret_cast<PlanScratch *>(raw), c.near);
+    if (!p.planned) make_plan(p, *reinterpret_cast<PlanScratch *>(raw));
     SegmentWalk w;  // here, and not by each role for itself: that is code that none of them finds in a cache
-    w.start(p, info);
+    w.start(p);
     if (!w.live()) {
         if (threadIdx.x == 0) p.errors[blockIdx.x] = 0;
         return;
