@@ -35,7 +35,11 @@ constexpr int kNormThreads = 128;    // (256: 71.5 us forward, 119 gradient, whe
 constexpr int kStagedThreads = 128;  // of the path through shared memory
 constexpr int kUnroll = 2;           // rows in flight per thread
 constexpr int kRounds = 8;           // heads for which a thread keeps a token's sines
-constexpr int kFwdPerSm = 7, kBwdPerSm = 4, kStagedPerSm = 6;  // CTAs; of the gradient each has its own sums of dw
+constexpr int kBwdPerSm = 4, kStagedPerSm = 6;  // CTAs; of the gradient each has its own sums of dw
+// Forward: seven leave 72 registers, of which bf16 spills 56 to 76 bytes, six 80 (16 to 24 bytes).  bf16, 16,384 tokens of 32 + 8 heads of 128: 64.0 us with
+// seven, 62.4 with six; fp32, which spills neither way, 101.2 and 105.4.
+template <typename T>
+constexpr int kFwdPerSm = sizeof(T) == 2 ? 6 : 7;
 
 struct NormParams {
     // [0]: q, [1]: k
@@ -177,7 +181,7 @@ constexpr int kChain = 128;
 
 // kFold: a gradient whose threads have more than kChain rows (as a variable in the same kernel it took the others from 111 to 114 us).
 template <typename T, bool kInterleaved, bool kBwd, bool kFold>
-__global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm) norm_rope_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>) norm_rope_kernel(const NormParams p) {
     constexpr int V = Elem<T>::kVec;
     const int half = p.rot / 2, pitch = table_pitch(p.rot);
     const int which = blockIdx.x < p.blocks[0] ? 0 : 1;
