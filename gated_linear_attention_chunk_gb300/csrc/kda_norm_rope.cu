@@ -1,23 +1,23 @@
 // RMS norms of q and k per head with learned weights, then rotary positions, in one pass; and the gradient.
 //
-// A head's row x of d channels, with n = r x, r = (mean x_i^2 + eps)^-1/2, becomes R(p) (w * n): R turns pair j by the
-// angle p w_j and scales it by m, as kda_rope does.  With g the output's gradient and b = R^T g (the turn by the opposite
-// angle),
+// A head's row x of d channels, with n = r x, r = (mean x_i^2 + eps)^-1/2, becomes R(p) (w * n): R turns pair j by the angle p
+// w_j and scales it by m, as kda_rope does.  With g the output's gradient and b = R^T g (the turn by the opposite angle),
 //     dw = sum over rows of b * n,      e = w * b,      dx = r (e - n mean(e * n)),
 // and mean(e * n) = r sum(e * x) / d, so that sum(x^2) and sum(e x) are all that a row's lanes have to share.  The gradient
 // reads x again in the place of a stored r: it needs n anyway.
 //
-// The bytes of the rows, read and written once, bound it.  A CTA has rows of q or of k (so that a thread keeps its
-// channels' weights, and in the gradient its channels' sums of dw, in registers) of a few tokens; sines and cosines are
-// computed once per (token, pair) into shared memory from the exactly reduced angle (kda_rope.cu).  A row
-// belongs to a group of lanes, each with two 16-byte columns: the two halves of its pairs, or two neighbours.  A group takes several heads of
-// one token, for which it holds the sines in registers.  Rows that are not 16-byte aligned, and halves that do not split into
-// such columns, go through shared memory.
+// The bytes of the rows, read and written once, bound it.  A CTA has rows of q or of k (so that a thread keeps its channels'
+// weights, and in the gradient its channels' sums of dw, in registers) of a few tokens; sines and cosines are computed once per
+// (token, pair) into shared memory from the exactly reduced angle (kda_rope.cu).  A row belongs to a group of lanes, each with
+// two 16-byte columns: the two halves of its pairs, or two neighbours.  A group takes several heads of one token, for which it
+// holds the sines in registers.  Rows that are not 16-byte aligned, and halves that do not split into such columns, go through
+// shared memory.
 //
-// 16,384 tokens of 32 + 8 heads of 128, bf16: forward 64 us (5.2 TB/s, 77% of the copy rate; issue 65% busy), gradient 111 (4.5 TB/s, 68%: 16
-// warps per SM, whose sums of dw take the registers), its weights' sums 3 of them.  8,191 tokens of 32 heads of 64, fp32: gradient 67 us (6.0
-// TB/s, 89%).  Through shared memory (126 of 128 channels turned, in halves): 139 and 278 us (neighbours: 62 and 103 for 20 of 128).  A decoding
-// step's 512 tokens: 6 to 7 us, of which the launch is half.
+// 16,384 tokens of 32 + 8 heads of 128, bf16: forward 62.5 us (5.4 TB/s, 80% of the copy rate; issue 64% busy), gradient 111
+// (4.5 TB/s, 68%: 16 warps per SM, whose sums of dw take the registers), its weights' sums 3 of them; fp32 forward 101 (6.6
+// TB/s).  8,191 tokens of 32 + 32 heads of 64, fp32: forward 44 us (6.2 TB/s), gradient 67 (6.0 TB/s, 90%).  Through shared
+// memory (126 of 128 channels turned, in halves): 139 and 278 us (neighbours: 62 and 103 for 20 of 128).  A decoding step's 512
+// tokens: 6 to 9 us, of which the launch is half.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -36,8 +36,8 @@ constexpr int kStagedThreads = 128;  // of the path through shared memory
 constexpr int kUnroll = 2;           // rows in flight per thread
 constexpr int kRounds = 8;           // heads for which a thread keeps a token's sines
 constexpr int kBwdPerSm = 4, kStagedPerSm = 6;  // CTAs; of the gradient each has its own sums of dw
-// Forward: seven leave 72 registers, of which bf16 spills 56 to 76 bytes, six 80 (16 to 24 bytes).  bf16, 16,384 tokens of 32 + 8 heads of 128: 64.0 us with
-// seven, 62.4 with six; fp32, which spills neither way, 101.2 and 105.4.
+// Forward: seven leave 72 registers, of which bf16 spills 56 to 76 bytes, six 80 (16 to 24 bytes).  bf16, 16,384 tokens of 32 +
+// 8 heads of 128: 64.0 us with seven, 62.4 with six; fp32, which spills neither way, 101.2 and 105.4.
 template <typename T>
 constexpr int kFwdPerSm = sizeof(T) == 2 ? 6 : 7;
 
@@ -73,7 +73,8 @@ __device__ __forceinline__ void make_table(float *cs, float *sn, const uint64_t 
     for (int e = threadIdx.x; e < nt * half; e += threads) {
         const int t = e / half, j = e - t * half;
         const uint64_t a = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + t])) * turn[j];
-        // the nearest quarter turn, and what is left as an fp32 number of half turns (at most 1/4: 2^-27 off, as against 2^-25 without)
+        // the nearest quarter turn, and what is left as an fp32 number of half turns (at most 1/4: 2^-27 off, as against 2^-25
+        // without)
         const uint32_t turns = static_cast<uint32_t>(a >> 32), quarter = (turns + 0x20000000u) >> 30;
         const float h = static_cast<float>(static_cast<int32_t>(turns - (quarter << 30))) * 4.656612873077392578e-10f;
         float s, c;
@@ -97,7 +98,8 @@ __device__ __forceinline__ void weights_at(float (&f)[V], const void *w, const N
         for (int j = 0; j < V; ++j) f[j] = there ? weight_at(w, p.wide_w, i + j) : 0.f;
     } else if (p.wide_w) {
 #pragma unroll
-        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(f + j) = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + i + j);
+        for (int j = 0; j < V; j += 4)
+            *reinterpret_cast<float4 *>(f + j) = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + i + j);
     } else {
         const __nv_bfloat162 *from = reinterpret_cast<const __nv_bfloat162 *>(static_cast<const __nv_bfloat16 *>(w) + i);
 #pragma unroll
@@ -144,13 +146,14 @@ __device__ __forceinline__ Columns columns_of(int lane, int d, int rot) {
     return c;
 }
 
-// The columns' pairs turned by the angle, or by its opposite (kBack).  co, si: of the pairs (a_i, b_i), or of a's and then b's pairs of
-// neighbours.
+// The columns' pairs turned by the angle, or by its opposite (kBack).  co, si: of the pairs (a_i, b_i), or of a's and then b's
+// pairs of neighbours.
 template <int V, bool kInterleaved, bool kBack>
 __device__ __forceinline__ void turn_columns(float (&a)[V], float (&b)[V], const float (&co)[V], const float (&si)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        float &x = kInterleaved ? (i < V / 2 ? a[2 * i] : b[2 * i - V]) : a[i], &y = kInterleaved ? (i < V / 2 ? a[2 * i + 1] : b[2 * i - V + 1]) : b[i];
+        float &x = kInterleaved ? (i < V / 2 ? a[2 * i] : b[2 * i - V]) : a[i];
+        float &y = kInterleaved ? (i < V / 2 ? a[2 * i + 1] : b[2 * i - V + 1]) : b[i];
         const float u = x, v = y;
         x = kBack ? fmaf(u, co[i], v * si[i]) : fmaf(u, co[i], -(v * si[i]));
         y = kBack ? fmaf(v, co[i], -(u * si[i])) : fmaf(u, si[i], v * co[i]);
@@ -179,7 +182,8 @@ struct Pair {
 // 128 make 72); 131,072 such tokens take 811 us with them and 793 without.
 constexpr int kChain = 128;
 
-// kFold: a gradient whose threads have more than kChain rows (as a variable in the same kernel it took the others from 111 to 114 us).
+// kFold: a gradient whose threads have more than kChain rows (as a variable in the same kernel it took the others from 111 to
+// 114 us).
 template <typename T, bool kInterleaved, bool kBwd, bool kFold>
 __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>) norm_rope_kernel(const NormParams p) {
     constexpr int V = Elem<T>::kVec;
@@ -230,7 +234,9 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>)
     float da[V] = {}, db[V] = {};  // sums of dw
     int chain = 0;                 // rows in them
     // [2 V] pairs of this thread
-    auto folded = [&](int j) { return reinterpret_cast<Pair *>(reinterpret_cast<float *>(norm_smem) + p.fold_at) + j * kNormThreads + threadIdx.x; };
+    auto folded = [&](int j) {
+        return reinterpret_cast<Pair *>(reinterpret_cast<float *>(norm_smem) + p.fold_at) + j * kNormThreads + threadIdx.x;
+    };
     auto fold = [&] {
 #pragma unroll
         for (int j = 0; j < 2 * V; ++j) {
@@ -350,9 +356,12 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>)
 }
 
 // Any rotated width and alignment: a row staged in shared memory as fp32, its pairs shared out among its lanes.
-// Floats of a group of lanes in shared memory: rows, and as much as puts the groups of a warp next to one another in the banks (gradient of the
-// same 314 -> 278 us; fp32 heads of 64, 73 -> 55 and 171 -> 106).
-__host__ __device__ __forceinline__ int staged_span(bool bwd, bool fold, int d, int lanes) { return (!bwd ? 1 : fold ? 5 : 3) * d + (lanes & 31); }
+//
+// Floats of a group of lanes in shared memory: rows, and as much as puts the groups of a warp next to one another in the banks
+// (gradient of the same 314 -> 278 us; fp32 heads of 64, 73 -> 55 and 171 -> 106).
+__host__ __device__ __forceinline__ int staged_span(bool bwd, bool fold, int d, int lanes) {
+    return (!bwd ? 1 : fold ? 5 : 3) * d + (lanes & 31);
+}
 
 template <typename T, bool kInterleaved, bool kBwd>
 __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const NormParams p) {
@@ -401,8 +410,8 @@ __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const 
             for (int i = lane; i < d; i += p.lanes) to[i] = Elem<T>::to_f(row[i]);
         }
     };
-    // The group's next row on its way while this one is worked on, where a lane has no more than two columns of it (126 of 128 channels turned:
-    // 190 us without, 141 with; gradient 380, 314).
+    // The group's next row on its way while this one is worked on, where a lane has no more than two columns of it (126 of 128
+    // channels turned: 190 us without, 141 with; gradient 380, 314).
     const bool ahead = p.vec_rows && d / V <= 2 * p.lanes;
     uint4 nx[2], ng[2];
     auto load_ahead = [&](int64_t t, int h) {
@@ -513,7 +522,8 @@ __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const 
 // dw from the CTAs' sums: 32 channels of q or k per CTA, 32 warps that take every 32nd sum (eight: 1 us longer).  Sums are pairs
 // of fp32: chains of some hundred plain additions lost as much as the threads' own (fp64 took 6 us longer).
 constexpr int kWeightWarps = 32;
-__global__ void __launch_bounds__(32 * kWeightWarps) norm_weights_kernel(const float *part, int64_t blocks_q, int64_t blocks_k, int d, float *dq, float *dk) {
+__global__ void __launch_bounds__(32 * kWeightWarps) norm_weights_kernel(const float *part, int64_t blocks_q, int64_t blocks_k, int d,
+                                                                        float *dq, float *dk) {
     __shared__ Pair share[kWeightWarps][33];
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x * 32;
@@ -583,7 +593,8 @@ kda_status launch(NormParams p, bool columns, float *dwq, float *dwk, cudaStream
             p.blocks[i] = p.blocks[i] < share_i ? p.blocks[i] : share_i;
             // rows of a group of lanes
             const int64_t rounds = groups_of(groups_of(p.T, p.tokens[i]), static_cast<int>(p.blocks[i]));
-            fold |= rounds * (columns ? groups_of(p.H[i], p.share[i]) : groups_of(static_cast<int64_t>(p.tokens[i]) * p.H[i], groups)) > kChain;
+            const int64_t each = columns ? groups_of(p.H[i], p.share[i]) : groups_of(static_cast<int64_t>(p.tokens[i]) * p.H[i], groups);
+            fold |= rounds * each > kChain;
         }
     }
     if (p.blocks[0] + p.blocks[1] > 0x7fffffffLL) return KDA_ERR_INVALID_ARGUMENT;
@@ -606,11 +617,13 @@ kda_status launch(NormParams p, bool columns, float *dwq, float *dwk, cudaStream
         p.fold_at = fold ? 1 : 0;
         smem += (static_cast<size_t>(p.d) + static_cast<size_t>(groups) * staged_span(kBwd, fold, p.d, p.lanes)) * 4;
         if (!smem_opt_in<norm_rope_staged_kernel<T, kInterleaved, kBwd>>(128 * 1024)) return KDA_ERR_CUDA;
-        if (launch_after(norm_rope_staged_kernel<T, kInterleaved, kBwd>, dim3(grid), kStagedThreads, smem, s, p) != cudaSuccess) return KDA_ERR_CUDA;
+        if (launch_after(norm_rope_staged_kernel<T, kInterleaved, kBwd>, dim3(grid), kStagedThreads, smem, s, p) != cudaSuccess)
+            return KDA_ERR_CUDA;
     }
     if (kBwd && (dwq || dwk)) {
         const dim3 g(static_cast<unsigned>((p.d + 31) / 32), 2);
-        if (launch_after(norm_weights_kernel, g, 32 * kWeightWarps, 0, s, static_cast<const float *>(p.part), p.blocks[0], p.blocks[1], p.d, dwq, dwk) != cudaSuccess)
+        const float *part = p.part;
+        if (launch_after(norm_weights_kernel, g, 32 * kWeightWarps, 0, s, part, p.blocks[0], p.blocks[1], p.d, dwq, dwk) != cudaSuccess)
             return KDA_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -639,7 +652,8 @@ kda_status norm_rope(const NormArgs &a, void *stream) {
     if (!dtype_ok(a.dtype) || !dtype_ok(a.wdtype)) return KDA_ERR_UNSUPPORTED;
     const int d = a.d;
     if (d <= 0 || d % 8 != 0 || d > 1024) return KDA_ERR_UNSUPPORTED;
-    if (a.rot < 0 || a.rot > d || a.rot % 2 != 0 || a.T < 0 || a.Hq <= 0 || a.Hk < 0 || a.Hq > 65536 || a.Hk > 65536) return KDA_ERR_INVALID_ARGUMENT;
+    if (a.rot < 0 || a.rot > d || a.rot % 2 != 0 || a.T < 0 || a.Hq <= 0 || a.Hk < 0 || a.Hq > 65536 || a.Hk > 65536)
+        return KDA_ERR_INVALID_ARGUMENT;
     if (!(a.eps >= 0.f && a.eps < 3.0e38f)) return KDA_ERR_INVALID_ARGUMENT;
     const int Hk = a.k || a.T == 0 ? a.Hk : 0;  // (an empty tensor may have no address)
     const size_t es = elem_size(a.dtype), ws = elem_size(a.wdtype);
@@ -653,10 +667,12 @@ kda_status norm_rope(const NormArgs &a, void *stream) {
         return H == 0 || (*out >= width && aligned_to(ptr, es) && (a.T == 0 || ptr));
     };
     NormParams p{};
-    if (!rows(a.q, a.qs, a.Hq, &p.xs[0]) || !rows(a.k, a.ks, Hk, &p.xs[1]) || !rows(a.yq, a.yqs, a.Hq, &p.ys[0]) || !rows(a.yk, a.yks, Hk, &p.ys[1]))
+    if (!rows(a.q, a.qs, a.Hq, &p.xs[0]) || !rows(a.k, a.ks, Hk, &p.xs[1]) || !rows(a.yq, a.yqs, a.Hq, &p.ys[0]) ||
+        !rows(a.yk, a.yks, Hk, &p.ys[1]))
         return KDA_ERR_INVALID_ARGUMENT;
     if (a.backward && (!rows(a.gq, a.gqs, a.Hq, &p.gs[0]) || !rows(a.gk, a.gks, Hk, &p.gs[1]))) return KDA_ERR_INVALID_ARGUMENT;
-    if (!aligned_to(a.wq, ws) || !aligned_to(a.wk, ws) || !aligned_to(a.dwq, 4) || !aligned_to(a.dwk, 4) || (a.dwk && !Hk)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(a.wq, ws) || !aligned_to(a.wk, ws) || !aligned_to(a.dwq, 4) || !aligned_to(a.dwk, 4) || (a.dwk && !Hk))
+        return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned_to(a.positions, 4) || !aligned_to(a.inv_freq, 8) || (a.T > 0 && (!a.positions || (a.rot > 0 && !a.inv_freq))))
         return KDA_ERR_INVALID_ARGUMENT;
     if (a.backward && (!a.workspace || !aligned_to(a.workspace, 16) || a.ws_bytes < bwd_workspace(d))) return KDA_ERR_WORKSPACE;

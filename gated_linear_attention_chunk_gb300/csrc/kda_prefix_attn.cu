@@ -1,18 +1,18 @@
 // Attention of groups of sequences over the prefix that each group shares, joined with what the rows have from their own keys.
 //
-// The tokens of a group and the G = Hq / Hkv query heads of a KV head are the rows of one matrix product per KV head, so
-// that the prefix's keys and values are read once for all of them.  One pass with a running maximum and sum per row (base-2 exponentials
-// of scale log2(e) q.k).  The work is cut evenly (kda_prefix_attn.cuh).  A unit (group, KV head, block of rows) that lies within one CTA is
-// finished there; the parts of the others leave their sums, maximum and weight sum in the workspace, and join_kernel adds them in order.  So a
-// result's bits depend on the batch's sizes, but not on chance.
+// The tokens of a group and the G = Hq / Hkv query heads of a KV head are the rows of one matrix product per KV head, so that
+// the prefix's keys and values are read once for all of them.  One pass with a running maximum and sum per row (base-2
+// exponentials of scale log2(e) q.k).  The work is cut evenly (kda_prefix_attn.cuh).  A unit (group, KV head, block of rows)
+// that lies within one CTA is finished there; the parts of the others leave their sums, maximum and weight sum in the
+// workspace, and join_kernel adds them in order.  So a result's bits depend on the batch's sizes, but not on chance.
 //
-// The keys' bytes bound it up to about 280 rows per KV head, the tensor cores beyond (bf16), the fp32 units (fp32).  Measured, 32 / 8 heads of
-// 128, bf16: 16 prompts of up to 8,192 tokens with eight samples each 68 us (272 MB: 4.0 TB/s, 60% of the copy rate); one prompt of 131,072 with
-// 512 tokens 845 us (1.3 PFLOP/s, 68% of measured); one prompt of 2,048 with eight 21 us (latency).  fp32, 3 prompts of up to 4,099, 45 tokens,
-// 12 / 4 heads of 64: 36 us (latency).
+// The keys' bytes bound it up to about 280 rows per KV head, the tensor cores beyond (bf16), the fp32 units (fp32).  Measured,
+// 32 / 8 heads of 128, bf16: 16 prompts of up to 8,192 tokens with eight samples each 68 us (272 MB: 4.0 TB/s, 60% of the copy
+// rate); one prompt of 131,072 with 512 tokens 845 us (1.3 PFLOP/s, 68% of measured); one prompt of 2,048 with eight 21 us
+// (latency).  fp32, 3 prompts of up to 4,099, 45 tokens, 12 / 4 heads of 64: 36 us (latency).
 //
-// The plan checks the lengths and numbers the steps.  With more than kPlanGroups groups it is a launch of its own, otherwise every CTA makes it
-// for itself.
+// The plan checks the lengths and numbers the steps.  With more than kPlanGroups groups it is a launch of its own, otherwise
+// every CTA makes it for itself.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,8 +34,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefixParams p
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// fp32: blocks of 64 rows against tiles of 64 keys on the fp32 units: a thread has 4 x 4 scores, then 4 rows of dv / 16 columns.  A tile's products are summed apart and
-// then added to what there is, which keeps long sums as exact as short ones.
+// fp32 (16 to 60 bytes of spills at two CTAs per SM): blocks of 64 rows against tiles of 64 keys on the fp32 units: a thread
+// has 4 x 4 scores, then 4 rows of dv / 16 columns.  A tile's products are summed apart and then added to what there is, which
+// keeps long sums as exact as short ones.
 // ---------------------------------------------------------------------------------------------------------------
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
 
@@ -50,8 +51,8 @@ struct Tile {
 
 // 16 bytes into shared memory, zeros where there is nothing to read.
 __device__ __forceinline__ void copy16(float *to, const float *from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from), "r"(there ? 16 : 0)
-                 : "memory");
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -76,8 +77,9 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const PrefixParams 
     SegmentWalk w;
     for (w.start(p); w.live(); w.next(p)) {
         const int64_t rows = static_cast<int64_t>(w.tokens) * p.G, r0 = static_cast<int64_t>(w.block) * kRows;
-        // A tile's rows are looked up while the one before is worked on, and its keys, and values where they have a place, copied ahead.  (16 prompts of up
-        // to 4,096, 16 samples each, 32 / 8 heads of 64: 192 us where they are waited for one after the other, 153 so; of 128, 332 and 256.)
+        // A tile's rows are looked up while the one before is worked on, and its keys, and values where they have a place,
+        // copied ahead.  (16 prompts of up to 4,096, 16 samples each, 32 / 8 heads of 64: 192 us where they are waited for one
+        // after the other, 153 so; of 128, 332 and 256.)
         auto look_up = [&](int t) {
             if (threadIdx.x >= kKeys || t >= w.k1) return false;
             const uint32_t j = static_cast<uint32_t>(t) * kKeys + threadIdx.x;
@@ -194,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const PrefixParams 
                 for (int x = 0; x < 4; ++x) {
                     float v[C];
 #pragma unroll
-                    for (int j = 0; j < C; j += 4) *reinterpret_cast<float4 *>(v + j) = *reinterpret_cast<const float4 *>(vs + (k + x) * DV + j * 16 + tx * 4);
+                    for (int j = 0; j < C; j += 4)
+                        *reinterpret_cast<float4 *>(v + j) = *reinterpret_cast<const float4 *>(vs + (k + x) * DV + j * 16 + tx * 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float e = x == 0 ? a[i].x : x == 1 ? a[i].y : x == 2 ? a[i].z : a[i].w;
@@ -241,8 +244,11 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const PrefixParams 
     if (threadIdx.x == 0) p.errors[blockIdx.x] = met;
 }
 
-// The rows that no CTA has finished: a warp per (token, query head), the parts added in order.  What it reads of the call's inputs it reads before it
-// waits for the kernel ahead, which itself waited for everything before the call.
+// The rows that no CTA has finished: a warp per (token, query head), the parts added in order.  What it reads of the call's
+// inputs it reads before it waits for the kernel ahead.  That is safe because the kernel ahead lets it begin (grid_go) only
+// after its own grid_wait, when everything before the call has ended; and because what it may read while that kernel writes,
+// o_tail and lse_tail where they are o and lse, is of rows that kernel finishes itself (n == 1 below), and is dropped.  A row
+// that is joined here is written here alone.
 template <typename T, int DV>
 __global__ void __launch_bounds__(128) join_kernel(const PrefixParams p) {
     constexpr int VL = DV / 32;
@@ -363,7 +369,8 @@ Layout layout_of(int N, int64_t T, int Hq, int Hkv, int dv) {
     auto take = [&](size_t bytes) { const size_t at = off; off = align256(off + bytes); return at; };
     l.info = take((static_cast<size_t>(N) + 1) * sizeof(GroupInfo));
     l.errors = take(2 * kSmsAtMost * 4);
-    // bf16: one CTA per SM, two slots each, or up to kMostRounds parts where there is more than one block; fp32: two CTAs, smaller blocks
+    // bf16: one CTA per SM, two slots each, or up to kMostRounds parts where there is more than one block; fp32: two CTAs,
+    // smaller blocks
     const int64_t rows = T * (Hq / Hkv), a = (rows > kTcBlock ? kMostRounds : 2) * pitch_of(rows, kTcBlock), b = 4 * pitch_of(rows, kRows);
     const size_t slots = static_cast<size_t>(kSmsAtMost) * (a > b ? a : b);
     l.part_ml = take(slots * sizeof(float2));

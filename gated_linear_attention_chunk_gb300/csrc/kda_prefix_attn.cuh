@@ -63,12 +63,14 @@ __host__ __device__ inline int tiles_of_len(const PrefixParams &p, int len) {
     return static_cast<int>((n + keys - 1) / keys);
 }
 
-// Work is cut into parts where blocks share so many tiles of keys (64 KB each) that L2 does not keep them from one block to the next.
+// Work is cut into parts where blocks share so many tiles of keys (64 KB each) that L2 does not keep them from one block to the
+// next.
 constexpr int64_t kShared = 1024;
 constexpr int kPartCost = 4, kUnitCost = 4;  // tiles
-// Up to so many groups the kernels plan themselves, which spares a launch: 65,536 keys of 8 heads, eight tokens per group, in 2 to 16 groups 63 to 65
-// us and 69 with the launch, in 64 groups 90 and 94, in 256 173 and 191 (256 groups of two tokens and 128 keys 116 and 108, of four and 1,000 296 and 290).
-// Reading the plan from L2 is as fast as from shared memory (one group of 2,048 keys 22.4 us either way, 16 of 4,096 64.6).
+// Up to so many groups the kernels plan themselves, which spares a launch: 65,536 keys of 8 heads, eight tokens per group, in 2
+// to 16 groups 63 to 65 us and 69 with the launch, in 64 groups 90 and 94, in 256 173 and 191 (256 groups of two tokens and 128
+// keys 116 and 108, of four and 1,000 296 and 290). Reading the plan from L2 is as fast as from shared memory (one group of
+// 2,048 keys 22.4 us either way, 16 of 4,096 64.6).
 constexpr int kPlanGroups = 256;
 
 // What the plan of a CTA of whole warps, kPlanGroups threads at least, needs in shared memory.
@@ -83,8 +85,8 @@ struct PlanScratch {
     int tiles[kPlanGroups], blocks[kPlanGroups];
 };
 
-// Checks the lengths, numbers the steps and chooses the cut; by all threads of a CTA.  Each entry of p.info is written once, by every CTA that plans
-// with the same.
+// Checks the lengths, numbers the steps and chooses the cut; by all threads of a CTA.  Each entry of p.info is written once, by
+// every CTA that plans with the same.
 __device__ inline void make_plan(const PrefixParams &p, PlanScratch &s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
     if (threadIdx.x == 0) {
@@ -131,7 +133,8 @@ __device__ inline void make_plan(const PrefixParams &p, PlanScratch &s) {
             lead = by_parts ? 0 : static_cast<int>(share < kUnitCost ? share : kUnitCost);
             if (x.tiles > 0) steps += static_cast<int64_t>(p.Hkv) * x.blocks * lead;
             if (by_parts) {
-                // Parts of at most `size` tiles: of 32 sizes the one whose rounds take least, a part costing kPartCost tiles beside its own.
+                // Parts of at most `size` tiles: of 32 sizes the one whose rounds take least, a part costing kPartCost tiles
+                // beside its own.
                 auto parts_of = [](int tiles, int size) { return tiles > 0 ? (tiles + size - 1) / size : 0; };
                 // (a lane has a size, a warp some of the groups)
                 const int size = (s.longest + lane) / (lane + 1);
@@ -182,7 +185,9 @@ __device__ inline void make_plan(const PrefixParams &p, PlanScratch &s) {
 
 // The steps of a CTA begin at first_step(c); cta_of is the CTA that has a step.
 __device__ __forceinline__ int64_t first_step(int64_t total, int c, int ctas) { return total * c / ctas; }
-__device__ __forceinline__ int cta_of(int64_t total, int64_t step, int ctas) { return static_cast<int>(((step + 1) * ctas + total - 1) / total) - 1; }
+__device__ __forceinline__ int cta_of(int64_t total, int64_t step, int ctas) {
+    return static_cast<int>(((step + 1) * ctas + total - 1) / total) - 1;
+}
 
 // A CTA's walk over its segments: runs of steps within one unit, those with keys.
 struct SegmentWalk {

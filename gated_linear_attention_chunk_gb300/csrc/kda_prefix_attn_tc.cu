@@ -4,32 +4,35 @@
 // about 280 rows and the tensor cores beyond.  One CTA per SM works on two streams of 128 rows x 128 keys:
 //   a block of more than 128 rows: stream s has rows 128 s .. of it, both take every key tile;
 //   a smaller block:               both streams have its rows, stream s takes the key tiles of parity s.
-// Per step of a stream S = Q K^T (128 x 128, fp32, TMEM), its softmax warps turn S into weights P (bf16, over S in
-// TMEM), O += P V (P from TMEM, V as an MN-major operand).  While one stream's softmax runs, the tensor cores work for the other.
+// Per step of a stream S = Q K^T (128 x 128, fp32, TMEM), its softmax warps turn S into weights P (bf16, over S in TMEM),
+// O += P V (P from TMEM, V as an MN-major operand).  While one stream's softmax runs, the tensor cores work for the other.
 //
-// The softmax of a step is one pass: weights are taken against the reference that the row has, while the maximum is
-// looked for beside them.  Only where the maximum lies more than 2^8 above the reference (or, before there is any weight, 2^60 below it)
-// does the reference move there; the step's scores, which are still in TMEM, are then read again and O is rescaled.  (fp32 and bf16
-// have the range for weights up to 2^8.)  So the maximum is not waited for, and the exponentials start with the
-// first scores.  P is bf16 because both operands of a product have one type and V is bf16; that rounds a weight by at most 2^-9 of it.
-// The row's sum is fp32, of the weights before that rounding.
+// The softmax of a step is one pass: weights are taken against the reference that the row has, while the maximum is looked for
+// beside them.  Only where the maximum lies more than 2^8 above the reference (or, before there is any weight, 2^60 below it)
+// does the reference move there; the step's scores, which are still in TMEM, are then read again and O is rescaled.  (fp32 and
+// bf16 have the range for weights up to 2^8.)  So the maximum is not waited for, and the exponentials start with the first
+// scores.  P is bf16 because both operands of a product have one type and V is bf16; that rounds a weight by at most 2^-8 of
+// it. The row's sum is fp32, of the weights before that rounding.
 //
 // Warps:  0-3 and 4-7 softmax of stream 0 and 1 (a thread per row), 8 fills the ring, 9 issues the MMAs.
 // TMEM:   S0 0..127, S1 128..255, O0 256.., O1 384.. (512 columns).
 // Shared memory: two Q tiles and a ring of 128-row K or V tiles, all with the 128-byte swizzle (two 64-channel halves).  A tile of
 // keys is a page's part of 128 rows, or as many whole pages as fit, each from a row that is a multiple of eight (page_size 20: five
-// pages at rows 0, 24, ..); TMA copies one page's rows at a time.  What lies between the pages, and in the last tile behind the
-// prefix, is masked in S and zero in V.  The ring holds the tiles in the order in which they are consumed:
-// K_0 .. K_{L-1}, V_0, K_L, V_1, K_{L+1}, .. with L = 1 for two row tiles and 2 for one.
+// pages at rows 0, 24, ..); TMA copies one page's rows at a time.  (A page of 136 rows is two tiles, of 128 keys and of 8: 16
+// prompts of 4,080 82 us, where pages of 64, 128 or 256 take 65 to 66, of 264 71, of 200 68 and of 24 66.)  What lies between the
+// pages, and in the last tile behind the prefix, is masked in S and zero in V.  The ring holds the tiles in the order in which
+// they are consumed: K_0 .. K_{L-1}, V_0, K_L, V_1, K_{L+1}, .. with L = 1 for two row tiles and 2 for one.
 //
-// Of 112k clocks of a CTA of the rollout case (16 prompts, 68 us) 23k go by before its first scores: 9k until lengths are read and the plan is
-// made, the rest the first walk, copies and products, code that no cache has yet as much as data.  So the launch may begin before the one ahead
-// of it has ended (26 -> 21 us for one prompt together with the next), and the first segment is looked up
-// once for all warps.  A step of two streams takes 3,050 clocks, of which the tensor cores work 1,800; issuing from two warps was slower (the
-// streams fell into step).
+// 20 to 32 bytes of spills remain at 168 registers.
 //
-// Every wait is bounded (2 s): a role that gives up raises the abort flag, which ends all the others' waits; the MMAs
-// issued so far are drained and the TMEM is freed.
+// Of 112k clocks of a CTA of the rollout case (16 prompts, 68 us) 23k go by before its first scores: 9k until lengths are read
+// and the plan is made, the rest the first walk, copies and products, code that no cache has yet as much as data.  So the
+// launch may begin before the one ahead of it has ended (26 -> 21 us for one prompt together with the next), and the first
+// segment is looked up once for all warps.  A step of two streams takes 3,050 clocks, of which the tensor cores work 1,800;
+// issuing from two warps was slower (the streams fell into step).
+//
+// Every wait is bounded (2 s): a role that gives up raises the abort flag, which ends all the others' waits; the MMAs issued so
+// far are drained and the TMEM is freed.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -196,9 +199,9 @@ struct BlockRows {
     }
 };
 
-// Returns the number of ring tiles issued.  The query rows come with the first keys; rows of a tile beyond them have what was there or rows of others
-// (their results go nowhere).  Where G divides a tile the rows of whole tokens are a box: 32 lanes copying 256 rows each by itself took 10k clocks, as long as
-// three steps, boxes of eight rows 9k.
+// Returns the number of ring tiles issued.  The query rows come with the first keys; rows of a tile beyond them have what was
+// there or rows of others (their results go nowhere).  Where G divides a tile the rows of whole tokens are a box: 32 lanes
+// copying 256 rows each by itself took 10k clocks, as long as three steps, boxes of eight rows 9k.
 template <int DK, int DV>
 __device__ uint32_t fill(const TcParams &a, SegmentWalk w, const CUtensorMap *q_map, const CUtensorMap *k_map, const CUtensorMap *v_map, Control &c,
                          uint32_t q_smem, uint32_t ring, uint32_t (&q_uses)[2]) {
@@ -296,10 +299,10 @@ __device__ uint32_t fill(const TcParams &a, SegmentWalk w, const CUtensorMap *q_
 }
 
 // ---- issuing side (one warp) --------------------------------------------------------------------------------------
-// The two streams' steps follow one another through this one warp, so every instruction of it counts: it shares its scheduler with two
-// softmax warps, and at one election, descriptor and vote per MMA and wait, with all it waited for long there, it took 3.4k
-// clocks for a step of two streams, of which the tensor cores worked 1.8k.  So a product's MMAs are one block with one election, ring
-// places and parities are counted along, and a wait looks once before anything else.
+// The two streams' steps follow one another through this one warp, so every instruction of it counts: it shares its scheduler
+// with two softmax warps, and at one election, descriptor and vote per MMA and wait, with all it waited for long there, it took
+// 3.4k clocks for a step of two streams, of which the tensor cores worked 1.8k.  So a product's MMAs are one block with one
+// election, ring places and parities are counted along, and a wait looks once before anything else.
 __device__ __forceinline__ uint32_t same(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }  // known to be the same in all lanes
 
 // S = Q K^T: 128 x 128, 4 or 8 steps of 16 channels; halves of 64 channels are 16 KB apart.
@@ -375,8 +378,8 @@ __device__ void issue(const TcParams &a, SegmentWalk w, Control &c, char *smem, 
         return wait(bar, parity, c);
     };
     auto scores = [&](int s, int b, uint32_t slot) {
-        scores_mma<DK / 16>(tmem + s * 128, q_desc + static_cast<uint64_t>(b * (S::kQ >> 4)), k_desc + static_cast<uint64_t>(slot * (S::kSlot >> 4)), id_s,
-                            &c.s_full[s]);
+        scores_mma<DK / 16>(tmem + s * 128, q_desc + static_cast<uint64_t>(b * (S::kQ >> 4)),
+                            k_desc + static_cast<uint64_t>(slot * (S::kSlot >> 4)), id_s, &c.s_full[s]);
     };
     auto values = [&](int s, uint32_t slot, bool first) {
         values_mma(tmem + 256 + s * 128, tmem + s * 128, v_desc + static_cast<uint64_t>(slot * (S::kSlot >> 4)), id_o, first ? 0u : 1u);
@@ -535,7 +538,7 @@ __device__ void softmax(const TcParams &a, SegmentWalk w, Control &c, uint32_t t
         const BlockRows rows(p, w);
         const bool pair = rows.left > kRow;
         const int nt = w.k1 - w.k0, step = pair ? 1 : 2, first = pair ? 0 : s;
-        // where this thread's row goes, and its tail, on its way to L2 meanwhile
+        // where this thread's row goes, and its tail, on its way to the cache meanwhile
         const int in_block = (pair ? s * kRow : 0) + row;
         const bool there = in_block < rows.left;
         const int row_tok = (rows.rem0 + in_block) / p.G;

@@ -1,12 +1,12 @@
 // Tokens drawn from logits by given uniform numbers, after temperature, top-k, top-p and min-p, and the filtered distributions.
 //
-// With M the row's largest logit and e_i = exp((l_i - M) / t), the tokens are put in the order of K_i = (l_i descending,
-// i ascending).  Every filter keeps a first run of that order: top-k its first k, top-p the shortest run of those with a mass of
-// p of theirs, min-p the e_i >= min_p.  So the filters come down to one limit K*, and the token is the lowest i with
-// sum_{j <= i, K_j <= K*} e_j > u sum_{K_j <= K*} e_j.
+// With M the row's largest logit and e_i = exp((l_i - M) / t), the tokens are put in the order of K_i = (l_i descending, i
+// ascending).  Every filter keeps a first run of that order: top-k its first k, top-p the shortest run of those with a mass of
+// p of theirs, min-p the e_i >= min_p.  So the filters come down to one limit K*, and the token is the lowest i
+// with sum_{j <= i, K_j <= K*} e_j > u sum_{K_j <= K*} e_j.
 //
-// One cluster of CTAs per row; the row's bytes, read once, are the floor (the later passes over it find it in L2).  To find K* the
-// tokens are counted in 4096 bins by distance from M.
+// One cluster of CTAs per row; the row's bytes, read once, are the floor (the later passes over it find it in L2).  To find K*
+// the tokens are counted in 4096 bins by distance from M.
 //   top-k: the counts tell the bin of the k-th token.  The tokens up to it, if they are at most 2048, are sorted by one CTA,
 //          which takes all further steps on them.
 //   top-p: a bin's count and the sum of its tokens' places in it estimate its mass to about 10^-3, which brackets the bins that
@@ -16,19 +16,21 @@
 //          that the rank or the mass falls into is cut into 2048 bins of K again until 2048 tokens are left.
 //
 // Precision: the answers are whole numbers, so a rounding shows only next to a border, where a flat distribution over 10^5
-// tokens has one every 10^-5.  Masses are 64-bit integers in units of 2^-44 of the largest (2^-(63 - b) for 2^b tokens where b > 19):
-// their sums are exact, whatever the order, so that neither atomics nor the cluster's size change a result.  What a mass is made
-// of is 2^x, x = (l - M) log2(e) / t to about 2^-33, from a table of 2^(i/256) and a cubic: off by about 2e-10 of itself.  Then it is
-// rounded to a unit, by 2^-45 of the largest up to 2^19 tokens: of a flat tail of V tokens that far down all may go the same
-// way, 2^-26 of the largest together at 2^19 and 2^-16 at 2^24 (64-bit sums have no room for finer units).
+// tokens has one every 10^-5.  Masses are 64-bit integers in units of 2^-44 of the largest (2^-(63 - b) for 2^b tokens where
+// b > 19): their sums are exact, whatever the order, so that neither atomics nor the cluster's size change a result.  What a mass
+// is made of is 2^x, x = (l - M) log2(e) / t to about 2^-33, from a table of 2^(i/256) and a cubic: off by about 2e-10 of
+// itself.  Then it is rounded to a unit, by 2^-45 of the largest up to 2^19 tokens: of a flat tail of V tokens that far down
+// all may go the same way, 2^-26 of the largest together at 2^19 and 2^-16 at 2^24 (64-bit sums have no room for finer units).
 //
-// The arithmetic of the masses bounds a call without top-k (30 operations per token, two tokens at a time where there are such instructions):
-// 512 rows of 131,072 in bf16 by temperature alone take 113 us (issue 57% busy, 1.2 TB/s).  With filters it is the steps between the passes as
-// well: a CTA has 64 tokens per thread of such a row, and spends about as many instructions on sums over warps and cluster.  128 rows of
-// 131,072, fp32: 112 us with top-p, 73 with top-k below 200; 256 rows of 100,003 in bf16 with all distributions written 185; one row of 32,001
-// 13 to 20 (cluster barriers). Tried and not kept: rows through a ring of asynchronous copies (slower: the passes do not wait for memory), two
-// to four columns ahead in registers (109 to 116 us for 112, spills), counting threads' maxima before tokens for top-k (top-k 73 -> 64 us, but
-// top-p 112 -> 119: the registers), a cluster's size by waves (see launch_sample).
+// The arithmetic of the masses bounds a call without top-k (30 operations per token, two tokens at a time where there are such
+// instructions): 512 rows of 131,072 in bf16 by temperature alone take 113 us (issue 57% busy, 1.2 TB/s; 38 to 42 bytes of
+// spills at 64 registers).  With filters it is the steps between the passes as well: a CTA has 64 tokens per thread of such a
+// row, and spends about as many instructions on sums over warps and cluster.  128 rows of 131,072, fp32: 112 us with top-p, 73
+// with top-k below 200, 30 greedy; 256 rows of 100,003 in bf16 with all distributions written 172 to 183 with filters and 113
+// without (54 of them the draw); one row of 32,001 11 to 18 (cluster barriers). Tried and not kept: rows through a ring of
+// asynchronous copies (slower: the passes do not wait for memory), two to four columns ahead in registers (109 to 116 us for
+// 112, spills), counting threads' maxima before tokens for top-k (top-k 73 -> 64 us, but top-p 112 -> 119: the registers), a
+// cluster's size by waves (see launch_sample).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,8 +53,8 @@ constexpr int kList = 2048;        // tokens that are put in order by sorting
 constexpr int kPer = kList / kThreads;
 constexpr int kMaxCluster = 8;
 constexpr float kSpan = 20.f;      // the bins cover distances from M of up to 20 t, the last one has the rest
-// With top-k they cover 40 at least: likely tokens at low temperatures leave the k-th far behind them.  (128 rows of 131,072 whose other tokens lie 20 t and
-// more below three: 184 us the general way, 75 so.)
+// With top-k they cover 40 at least: likely tokens at low temperatures leave the k-th far behind them.  (128 rows of 131,072
+// whose other tokens lie 20 t and more below three: 184 us the general way, 75 so.)
 constexpr float kRankSpan = 40.f;
 constexpr float kHottest = 1e30f;  // higher temperatures count as this one
 static_assert(3 * kBins >= kCoarse && 3 * kBins * 4 >= kList * 8, "all lie over the bins");
@@ -207,7 +209,8 @@ struct Sampler {
     cg::cluster_group cluster;
     int C, rank, warp, lane;
     // Shared memory.
-    static __device__ __forceinline__ uint32_t *count() { return reinterpret_cast<uint32_t *>(sample_smem); }  // [kBins] each; together the kCoarse counts
+    // [kBins] each; together the kCoarse counts
+    static __device__ __forceinline__ uint32_t *count() { return reinterpret_cast<uint32_t *>(sample_smem); }
     static __device__ __forceinline__ uint32_t *mass_lo() { return count() + kBins; }
     static __device__ __forceinline__ uint32_t *mass_hi() { return count() + 2 * kBins; }
     // [kList]: tokens of this CTA, or of all in the first one; the second list lies over the bins
@@ -341,8 +344,9 @@ struct Sampler {
         const float places = static_cast<float>(1 << p.place_bits), most = static_cast<float>((kCoarse << p.place_bits) - 1);
         const float scale = c.bin_scale * places;  // (exact: bins and places are cut at the same points as by distance())
         const uint32_t mask = (1u << p.place_bits) - 1u, one = 1u << p.count_shift;
-        // Tokens beyond the last place are counted by each thread for itself: they would all meet at one word.  (128 rows of 131,072, top-p: 120 us where
-        // they are counted like the others, 112 so; where all but three tokens lie there 150 and 89.)
+        // Tokens beyond the last place are counted by each thread for itself: they would all meet at one word.  (128 rows of
+        // 131,072, top-p: 120 us where they are counted like the others, 112 so; where all but three tokens lie there 150 and
+        // 89.)
         uint32_t far = 0;
         columns([&](int, const float (&x)[W]) {
 #pragma unroll
@@ -511,7 +515,8 @@ struct Sampler {
             if (threadIdx.x + y * kThreads < size) keys[threadIdx.x + y * kThreads] = v[y];
         __syncthreads();
     }
-    // Running sums over at most kList values, kPer neighbours per thread: m becomes the sum up to and with each.  For the whole CTA.
+    // Running sums over at most kList values, kPer neighbours per thread: m becomes the sum up to and with each.  For the whole
+    // CTA.
     __device__ uint64_t scan(uint64_t (&m)[kPer]) {
         uint64_t own = 0;
 #pragma unroll
@@ -772,8 +777,8 @@ struct Sampler {
         }
     }
 
-    // A token's e times a factor of at most 1, wherever the token lies: x = (l - M) log2(e) / t as a pair, of which l - M is rounded, and what that
-    // leaves out is exact.  Below half of fp32's smallest number it is 0, as for a masked token.
+    // A token's e times a factor of at most 1, wherever the token lies: x = (l - M) log2(e) / t as a pair, of which l - M is
+    // rounded, and what that leaves out is exact.  Below half of fp32's smallest number it is 0, as for a masked token.
     __device__ __forceinline__ float faint(float l, float factor) const {
         const float d = __fsub_rn(l, c.top), v = __fsub_rn(d, l), d_lo = __fsub_rn(__fsub_rn(l, __fsub_rn(d, v)), __fadd_rn(c.top, v));
         const float h = __fmul_rn(d, c.c_hi);
@@ -784,8 +789,9 @@ struct Sampler {
         return exp2f((h - n) + lo) * factor * 5.42101086e-20f * scale;
     }
     // The distribution: tokens up to the limit have e / total, the others none.  Element by element, so that a warp's stores
-    // are consecutive whatever the row's alignment; two at a time, as there are such instructions.  The last step: c.cut goes down to where the
-    // exponentials end (125 halvings below M, or 63 where l - sub is exact no further); what lies below is faint.
+    // are consecutive whatever the row's alignment; two at a time, as there are such instructions.  The last step: c.cut goes
+    // down to where the exponentials end (125 halvings below M, or 63 where l - sub is exact no further); what lies below is
+    // faint.
     __device__ void write(int64_t row_at, uint64_t limit, float inv_total) {
         const int64_t first = static_cast<int64_t>(col0) * W - shift;
         const int from = static_cast<int>(first < 0 ? 0 : first);
@@ -827,8 +833,8 @@ struct Sampler {
         }
     }
 
-    // The token at a point of the kept mass, by the CTA that holds it; shared().warp_mass: the kept masses of its warps' tokens.  The tokens of the one
-    // warp that has it are shared out among all threads, a few neighbours each, round by round.
+    // The token at a point of the kept mass, by the CTA that holds it; shared().warp_mass: the kept masses of its warps'
+    // tokens.  The tokens of the one warp that has it are shared out among all threads, a few neighbours each, round by round.
     __device__ void draw(int64_t at, uint64_t limit, uint64_t before, uint64_t point) {
         const uint64_t own = lane < kWarps ? shared().warp_mass[lane] : 0;
         uint64_t start = own;
@@ -948,7 +954,8 @@ struct Sampler {
         unit = __int_as_float((127 + 44 - p.extra) << 23);
         for (int i = threadIdx.x; i < 256; i += kThreads) shared().table[i] = make_uint2(kExp2.th[i], __float_as_uint(kExp2.tl[i]));
         grid_wait();
-        // (c.cut, 47 halvings below M, is then always within fp32's range: hotter than 3e36 it was not, and what is -inf had a mass)
+        // (c.cut, 47 halvings below M, is then always within fp32's range: hotter than 3e36 it was not, and what is -inf had a
+        // mass)
         const float asked = p.temperature ? p.temperature[at] : 1.f, t = asked > kHottest ? kHottest : asked;
         const bool greedy = !(t > 1e-30f);
         const float min_p = p.min_p ? p.min_p[at] : 0.f;
@@ -956,7 +963,8 @@ struct Sampler {
         const float top_p = p.top_p ? p.top_p[at] : 1.f;
         const int k = top_p <= 0.f ? 1 : p.top_k ? p.top_k[at] : 0;  // (no mass asked for: the first token)
         bool rank_on = k > 0 && k < p.V;
-        if (threadIdx.x == kThreads - 1 && floor_on) shared().min_shift = min_p < 1.f ? static_cast<double>(t) * log(static_cast<double>(min_p)) : 0.0;
+        if (threadIdx.x == kThreads - 1 && floor_on)
+            shared().min_shift = min_p < 1.f ? static_cast<double>(t) * log(static_cast<double>(min_p)) : 0.0;
         // the row, and its largest logit
         float top = -INFINITY;
         const int end = min(cols, (warp + 1) * span);
@@ -1197,10 +1205,10 @@ kda_status launch_sample(SampleParams p, int N, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return KDA_ERR_CUDA;
     const int cols = static_cast<int>((static_cast<int64_t>(p.V) + 2 * W - 2) / W);  // at any alignment of the row
-    // Two CTAs are resident on an SM.  A CTA alone has no cluster to wait for, but rows in fewer CTAs than that leave SMs idle: clusters just
-    // large enough to fill them (128 rows of 131,072, fp32 with top-p: 183 us with one, 137 with two, 116 with four, 142 with eight), as long as every
-    // thread has a column.  (Rows with top-k alone would like fewer, 128 of them 58 us with two and 73 with four, but not where others are among them: 107
-    // to 111 with four, 118 to 127 with two.)
+    // Two CTAs are resident on an SM.  A CTA alone has no cluster to wait for, but rows in fewer CTAs than that leave SMs idle:
+    // clusters just large enough to fill them (128 rows of 131,072, fp32 with top-p: 183 us with one, 137 with two, 116 with
+    // four, 142 with eight), as long as every thread has a column.  (Rows with top-k alone would like fewer, 128 of them 58 us
+    // with two and 73 with four, but not where others are among them: 107 to 111 with four, 118 to 127 with two.)
     int C = 1;
     while (C < kMaxCluster && static_cast<int64_t>(N) * C < 2 * sms && cols / C >= 2 * kThreads) C *= 2;
     p.slice = (cols + C - 1) / C;
@@ -1244,8 +1252,8 @@ kda_status kda_sample(const void *logits, kda_dtype dtype, const float *u, const
     if (logits_stride < V || probs_stride < V) return KDA_ERR_INVALID_ARGUMENT;
     if (N == 0) return KDA_OK;
     if (!token && !probs) return KDA_ERR_INVALID_ARGUMENT;
-    if (!aligned_to(logits, elem_size(dtype)) || !aligned_to(u, 4) || !aligned_to(temperature, 4) || !aligned_to(top_k, 4) || !aligned_to(top_p, 4) ||
-        !aligned_to(min_p, 4) || !aligned_to(token, 4) || (probs && !aligned_to(probs, elem_size(probs_dtype))))
+    if (!aligned_to(logits, elem_size(dtype)) || !aligned_to(u, 4) || !aligned_to(temperature, 4) || !aligned_to(top_k, 4) ||
+        !aligned_to(top_p, 4) || !aligned_to(min_p, 4) || !aligned_to(token, 4) || (probs && !aligned_to(probs, elem_size(probs_dtype))))
         return KDA_ERR_INVALID_ARGUMENT;
     if (!logits || (token && !u)) return KDA_ERR_INVALID_ARGUMENT;
     kda::SampleParams p{};

@@ -22,7 +22,7 @@
 // neither at the bytes (4.4 us) nor at the tensor rate (the pipe is busy 9.5% of the time): a part has a few tiles, two warps
 // share a scheduler, and what they wait for is their own chain of copies, splits, products and the join.
 //
-// bf16 weights meet the values as bf16 (half a step, 2^-9 of a weight): a tensor-core product takes both operands in one type, and a
+// bf16 weights meet the values as bf16 (half a step, 2^-8 of a weight): a tensor-core product takes both operands in one type, and a
 // second product with the remainders would double the work on the values.  Sums and maxima are fp32, of the weights before
 // that rounding.
 //

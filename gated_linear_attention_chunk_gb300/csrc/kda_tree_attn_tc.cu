@@ -10,7 +10,7 @@
 // TMEM), O += P V (P from TMEM, V as an MN-major operand).  While one stream's softmax runs, the tensor cores work
 // for the other.  The running maximum a row's weights refer to is raised only when the true one has grown by more than
 // 2^8 beyond it, so O is seldom rescaled (fp32 and bf16 have the range for weights up to 2^8).  P is bf16 because both
-// operands of a product have one type and V is bf16; that rounds a weight by at most 2^-9 of it (a second product with the
+// operands of a product have one type and V is bf16; that rounds a weight by at most 2^-8 of it (a second product with the
 // remainders would add half of the tensor work).  The row's sum is fp32, of the weights before that rounding.
 //
 // Warps:  0-3 and 4-7 softmax of stream 0 and 1 (a thread per row), 8-11 fill the ring, 12 issues the MMAs.

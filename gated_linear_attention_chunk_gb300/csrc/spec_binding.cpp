@@ -502,7 +502,8 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef methods[] = {method<rope, 9>("rope"), method<tree_attn, 15>("tree_attn"), method<cache_append, 10>("cache_append"),
-                         method<draft_verify, 11>("draft_verify"), method<norm_rope, 16>("norm_rope"), method<sample, 9>("sample"), method<prefix_attn, 13>("prefix_attn"),
+                         method<draft_verify, 11>("draft_verify"), method<norm_rope, 16>("norm_rope"), method<sample, 9>("sample"),
+                         method<prefix_attn, 13>("prefix_attn"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_spec", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

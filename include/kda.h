@@ -441,7 +441,7 @@ typedef struct kda_paged_kv {
  *          and, where it allows more than 32 rows per KV head in bf16, two launches.  T <= N * max_nodes; packed nodes from
  *          cu_nodes[N] on are not read, and their outputs not written.
  * dk, dv each 64 or 128; page_size * max_pages < 2^31.  Scores, softmax and sums are fp32; for bf16 the weights are
- * rounded to bf16 (by at most 2^-9 of each) before they meet the values, as the tensor cores take both operands in one
+ * rounded to bf16 (by at most 2^-8 of each) before they meet the values, as the tensor cores take both operands in one
  * type (fp32 inputs: products in three tf32 terms, about 22 bits).
  * A node's infinities and NaN reach the rows that see the node, and no others.
  * Long contexts are cut into parts that run concurrently and are joined in a fixed
@@ -566,7 +566,7 @@ kda_status kda_norm_rope_bwd(const void *q, const void *k, const void *d_q_out, 
  * A row without any key has o = 0 and lse = -inf.  Calls can be chained (a prefix of prefixes): a result is the next one's tail.
  * dk, dv each 64 or 128; page_size * max_pages < 2^31.  Packed tokens from cu_tokens[N] on do not matter, and their outputs are not
  * written.  Scores, softmax and sums are fp32 up to the one rounding of o; for bf16 the weights are rounded to bf16 (by at
- * most 2^-9 of each) before they meet the values.  The work is cut by the sizes of the whole batch, so the bits of a result depend on
+ * most 2^-8 of each) before they meet the values.  The work is cut by the sizes of the whole batch, so the bits of a result depend on
  * them, but not on chance.
  * Device errors: BAD_SEQLENS, BAD_PAGE (a page outside the pool, or a prefix longer than its table row); such a group
  * writes nothing.  workspace: >= kda_prefix_attn_workspace_size(N, T, Hq, Hkv, dv) bytes, 16-byte aligned.
