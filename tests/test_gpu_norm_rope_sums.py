@@ -66,8 +66,8 @@ def test_every_token_counts(kda, T, Hq, Hk, d, rot, dtype):
 
 
 def test_random_rows_by_the_norm_of_the_gradient(kda):
-    """A thread's sums over 30,000 random rows: errors of random sign, 8 u of the root of the sum of squares per channel with room to spare; a
-    row left out would be 2^16 u of it."""
+    """30,000 random rows: the terms' errors and the sums' have random signs, a few u of the gradient's norm together (1e-6 is 17 u); one row
+    left out would be about 1 / sqrt(30,000) of it."""
     T, Hq, Hk, d = 2500, 12, 4, 64
     gen = torch.Generator().manual_seed(5)
     x, g = ([torch.randn(T, h, d, generator=gen) for h in (Hq, Hk)] for _ in "xg")
