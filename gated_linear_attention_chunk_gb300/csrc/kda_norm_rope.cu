@@ -120,15 +120,19 @@ __device__ __forceinline__ float lanes_sum(float x, int lanes) {
     return x;
 }
 
+// Which channels are pairs: (j, j + rot / 2); or (2 j, 2 j + 1), all of them or those below rot.  (16,384 tokens of 32 + 8 heads of
+// 128 in bf16, gradient: neighbours 117 us, 120 where their number is looked at; halves are as fast either way.)
+enum Layout { kHalves, kNeighbours, kSomeNeighbours };
 // A thread's two columns of a row: channels a .. a + V and b .. b + V.
 struct Columns {
     int a, b, table;  // table: its first pair (half layout), or a's first pair
     bool has_a, has_b;
     bool turns;       // half layout: its pairs are turned (neighbours: those below rot / 2 are)
 };
-template <int V, bool kInterleaved>
+template <int V, Layout kLayout>
 __device__ __forceinline__ Columns columns_of(int lane, int d, int rot) {
     Columns c{};
+    constexpr bool kInterleaved = kLayout != kHalves;
     const int pairs = kInterleaved ? 0 : rot / 2 / V;  // lanes that hold both halves of their pairs
     if (lane < pairs) {
         c.a = lane * V;
@@ -146,17 +150,22 @@ __device__ __forceinline__ Columns columns_of(int lane, int d, int rot) {
     return c;
 }
 
-// The columns' pairs turned by the angle, or by its opposite (kBack).  co, si: of the pairs (a_i, b_i), or of a's and then b's
-// pairs of neighbours.
-template <int V, bool kInterleaved, bool kBack>
-__device__ __forceinline__ void turn_columns(float (&a)[V], float (&b)[V], const float (&co)[V], const float (&si)[V]) {
+// The columns' first n pairs (of halves all or none) turned by the angle, or by its opposite (kBack).  co, si: of the pairs (a_i, b_i),
+// or of a's and then b's pairs of neighbours, 1 and 0 where there is none: an infinity or a NaN in such a channel is nothing to
+// the other.
+template <int V, Layout kLayout, bool kBack>
+__device__ __forceinline__ void turn_columns(float (&a)[V], float (&b)[V], const float (&co)[V], const float (&si)[V], int n) {
+    constexpr bool kInterleaved = kLayout != kHalves;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float &x = kInterleaved ? (i < V / 2 ? a[2 * i] : b[2 * i - V]) : a[i];
         float &y = kInterleaved ? (i < V / 2 ? a[2 * i + 1] : b[2 * i - V + 1]) : b[i];
-        const float u = x, v = y;
-        x = kBack ? fmaf(u, co[i], v * si[i]) : fmaf(u, co[i], -(v * si[i]));
-        y = kBack ? fmaf(v, co[i], -(u * si[i])) : fmaf(u, si[i], v * co[i]);
+        const float u = kInterleaved || n > 0 ? x : 0.f, v = kInterleaved || n > 0 ? y : 0.f;
+        const float s = kBack ? fmaf(x, co[i], v * si[i]) : fmaf(x, co[i], -(v * si[i]));
+        const float t = kBack ? fmaf(y, co[i], -(u * si[i])) : fmaf(u, si[i], y * co[i]);
+        const bool pair = kLayout != kSomeNeighbours || i < n;
+        x = pair ? s : x;
+        y = pair ? t : y;
     }
 }
 
@@ -184,9 +193,10 @@ constexpr int kChain = 128;
 
 // kFold: a gradient whose threads have more than kChain rows (as a variable in the same kernel it took the others from 111 to
 // 114 us).
-template <typename T, bool kInterleaved, bool kBwd, bool kFold>
+template <typename T, Layout kLayout, bool kBwd, bool kFold>
 __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>) norm_rope_kernel(const NormParams p) {
     constexpr int V = Elem<T>::kVec;
+    constexpr bool kInterleaved = kLayout != kHalves;
     const int half = p.rot / 2, pitch = table_pitch(p.rot);
     const int which = blockIdx.x < p.blocks[0] ? 0 : 1;
     const int64_t block = blockIdx.x - (which ? p.blocks[0] : 0), blocks = p.blocks[which];
@@ -195,7 +205,8 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>)
     float *cs = reinterpret_cast<float *>(turn + ((half + 1) & ~1)), *sn = cs + tokens * pitch;
     const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, share = p.share[which];
     const int slot = group / share, head0 = group - slot * share;  // the group's token in the CTA, its first head
-    const Columns c = columns_of<V, kInterleaved>(lane, p.d, p.rot);
+    const Columns c = columns_of<V, kLayout>(lane, p.d, p.rot);
+    const int turned = kInterleaved ? half - c.table : c.turns ? V : 0;  // pairs of the columns, if that many
     const int64_t step = static_cast<int64_t>(share) * p.d;        // from one of the group's heads to the next
     int64_t t0 = block * tokens;
     const T *x, *g = nullptr;                                      // the group's next head to load, this thread's column a
@@ -257,13 +268,12 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>)
         const int nt = static_cast<int>(p.T - t0 < tokens ? p.T - t0 : tokens);
         make_table(cs, sn, turn, p, t0, nt, kNormThreads);
         __syncthreads();
-        // pairs that are not turned have the angle 0
         float co[V], si[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const bool turned = (kInterleaved ? c.table + i < half : c.turns) && slot < nt;
-            co[i] = turned ? cs[slot * pitch + c.table + i] : 1.f;
-            si[i] = turned ? sn[slot * pitch + c.table + i] : 0.f;
+            const bool there = i < turned && slot < nt;
+            co[i] = there ? cs[slot * pitch + c.table + i] : 1.f;
+            si[i] = there ? sn[slot * pitch + c.table + i] : 0.f;
         }
         for (int r0 = 0; r0 < rounds; r0 += kUnroll) {
             if (r0 > 0) load();
@@ -283,12 +293,12 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>)
                         a[j] = a[j] * rn * wa[j];
                         b[j] = b[j] * rn * wb[j];
                     }
-                    turn_columns<V, kInterleaved, false>(a, b, co, si);
+                    turn_columns<V, kLayout, false>(a, b, co, si, turned);
                 } else {
                     float u[V], v[V];
                     unpack16(ga[i], u);
                     unpack16(gb[i], v);
-                    turn_columns<V, kInterleaved, true>(u, v, co, si);
+                    turn_columns<V, kLayout, true>(u, v, co, si, turned);
                     float ex = 0.f;
 #pragma unroll
                     for (int j = 0; j < V; ++j) ex = fmaf(u[j] * wa[j], a[j], fmaf(v[j] * wb[j], b[j], ex));
@@ -609,8 +619,13 @@ kda_status launch(NormParams p, bool columns, float *dwq, float *dwk, cudaStream
             smem += 2 * V * kNormThreads * sizeof(Pair);
         }
         auto go = [&](auto folds) {
-            constexpr auto kernel = norm_rope_kernel<T, kInterleaved, kBwd, decltype(folds)::value>;
-            return smem_opt_in<kernel>(64 * 1024) && launch_after(kernel, dim3(grid), kNormThreads, smem, s, p) == cudaSuccess;
+            auto run = [&](auto layout) {
+                constexpr auto kernel = norm_rope_kernel<T, decltype(layout)::value, kBwd, decltype(folds)::value>;
+                return smem_opt_in<kernel>(64 * 1024) && launch_after(kernel, dim3(grid), kNormThreads, smem, s, p) == cudaSuccess;
+            };
+            if constexpr (!kInterleaved) return run(std::integral_constant<Layout, kHalves>{});
+            else if (p.rot == p.d) return run(std::integral_constant<Layout, kNeighbours>{});
+            else return run(std::integral_constant<Layout, kSomeNeighbours>{});
         };
         if (!(fold ? go(std::bool_constant<kBwd>{}) : go(std::false_type{}))) return KDA_ERR_CUDA;
     } else {

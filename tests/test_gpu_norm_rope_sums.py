@@ -90,3 +90,27 @@ def test_outputs_for_an_absent_k_are_refused(kda):
     for bad in (dict(d_k=held), dict(d_k_weight=held[0, 0].contiguous())):
         with pytest.raises(ValueError):
             kda.kda_norm_rope_bwd(q, None, q, None, pos, freq, **bad)
+
+
+@pytest.mark.parametrize("d,rot", [(64, 0), (64, 32), (128, 64), (128, 20), (128, 126), (136, 16), (256, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [ref.BF16, ref.F32])
+def test_channels_that_are_not_turned_know_nothing_of_one_another(kda, d, rot, interleaved, dtype):
+    """An infinity among them: its head's other channels become zeros (its norm is infinite), and in the gradient its own weight's sum alone is no
+    number or infinite."""
+    gen = torch.Generator().manual_seed(d + rot)
+    T, H = 6, 3
+    x, g = (torch.randn(T, H, d, generator=gen).to(dtype) for _ in "xg")
+    pos, freq = torch.arange(T, dtype=torch.int32, device="cuda"), torch.rand(rot // 2, generator=gen, dtype=torch.float64).cuda()
+    w = torch.ones(d, device="cuda")
+    for at in range(rot, d, 5):
+        y = x.clone()
+        y[2, 1, at] = float("inf")
+        out = kda.kda_norm_rope(y.cuda(), None, pos, freq, w, interleaved=interleaved)[0][2, 1]
+        rest = torch.arange(d, device="cuda") != at
+        assert bool((out[rest] == 0).all()) and bool(out[at].isnan())
+        z = g.clone()
+        z[2, 1, at] = float("inf")
+        dw = kda.kda_norm_rope_bwd(x.cuda(), None, z.cuda(), None, pos, freq, w, interleaved=interleaved)[2]
+        same = kda.kda_norm_rope_bwd(x.cuda(), None, g.cuda(), None, pos, freq, w, interleaved=interleaved)[2]
+        assert torch.equal(dw[rest], same[rest]) and not bool(dw[at].isfinite())
