@@ -184,6 +184,8 @@ struct Pair {
         low = __fadd_rn(low, __fadd_rn(__fsub_rn(high, __fsub_rn(s, b)), __fsub_rn(x, b)));
         high = s;
     }
+    // (beyond fp32's range `high` is what a plain sum has, and what it leaves out no number)
+    __device__ __forceinline__ float value() const { return fabsf(high) < INFINITY ? high + low : high; }
 };
 // Sums of dw: a thread adds up kChain rows or so plainly, then those sums as pairs, which lie in shared memory.  So their
 // error does not grow with the rows of a call; rows that are all alike, as a padded batch has them, took plain sums of some
@@ -339,8 +341,8 @@ __global__ void __launch_bounds__(kNormThreads, kBwd ? kBwdPerSm : kFwdPerSm<T>)
             fold();
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                da[j] = folded(j)->high + folded(j)->low;
-                db[j] = folded(V + j)->high + folded(V + j)->low;
+                da[j] = folded(j)->value();
+                db[j] = folded(V + j)->value();
             }
         }
 #pragma unroll
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kStagedThreads) norm_rope_staged_kernel(const 
         }
         if (pairs && t0 + blocks * tokens >= p.T) {
             fold();
-            for (int i = lane; i < d; i += p.lanes) dw[i] = folded[i] + folded[d + i];
+            for (int i = lane; i < d; i += p.lanes) dw[i] = Pair{folded[i], folded[d + i]}.value();
         }
         __syncthreads();
     }
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(32 * kWeightWarps) norm_weights_kernel(const f
         s.add(high);
         s.low += low;
     }
-    if (lane == 0 && first + warp < d) to[first + warp] = s.high + s.low;
+    if (lane == 0 && first + warp < d) to[first + warp] = s.value();
 }
 
 // CTAs of the gradient for q and k: as many as are resident, shared out by heads, but no more than there are groups of tokens.

@@ -114,3 +114,24 @@ def test_channels_that_are_not_turned_know_nothing_of_one_another(kda, d, rot, i
         dw = kda.kda_norm_rope_bwd(x.cuda(), None, z.cuda(), None, pos, freq, w, interleaved=interleaved)[2]
         same = kda.kda_norm_rope_bwd(x.cuda(), None, g.cuda(), None, pos, freq, w, interleaved=interleaved)[2]
         assert torch.equal(dw[rest], same[rest]) and not bool(dw[at].isfinite())
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d", [(5, 3, 1, 64), (700, 4, 2, 128), (2, 40000, 2, 64), (3, 9000, 1, 136)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_an_infinite_gradient_stays_infinite(kda, T, Hq, Hk, d, sign):
+    """One infinite entry of the output's gradient: that channel's sum is infinite, of its sign, and no other channel knows of it."""
+    gen = torch.Generator().manual_seed(T)
+    q, k = (torch.randn(T, h, d, generator=gen).abs() + 0.1 for h in (Hq, Hk))
+    gq, gk = (torch.randn(T, h, d, generator=gen) for h in (Hq, Hk))
+    pos, freq = torch.arange(T, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.float64, device="cuda")
+    w = torch.ones(d, device="cuda")
+    call = lambda g: kda.kda_norm_rope_bwd(q.cuda(), k.cuda(), g.cuda(), gk.cuda(), pos, freq, w, w)  # noqa: E731
+    plain, at = call(gq), (T - 1, Hq // 2, 21)
+    gq[at] = sign * float("inf")
+    got = call(gq)
+    assert float(got[2][21]) == sign * float("inf")
+    rest = torch.arange(d) != 21
+    assert torch.equal(got[2][rest], plain[2][rest]) and torch.equal(got[3], plain[3])
+    row = torch.zeros(T, Hq, dtype=torch.bool)
+    row[at[:2]] = True
+    assert bool(got[0][row].isnan().any()) and torch.equal(got[0][~row], plain[0][~row])
