@@ -13,8 +13,8 @@
 // holds the sines in registers.  Rows that are not 16-byte aligned, and halves that do not split into such columns, go through
 // shared memory.
 //
-// 16,384 tokens of 32 + 8 heads of 128, bf16: forward 62.5 us (5.4 TB/s, 80% of the copy rate; issue 64% busy), gradient 111
-// (4.5 TB/s, 68%: 16 warps per SM, whose sums of dw take the registers), its weights' sums 3 of them; fp32 forward 101 (6.6
+// 16,384 tokens of 32 + 8 heads of 128, bf16: forward 63 us (5.3 TB/s, 80% of the copy rate; issue 64% busy), gradient 109
+// (4.6 TB/s, 69%: 16 warps per SM, whose sums of dw take the registers), its weights' sums 3 of them; fp32 forward 101 (6.6
 // TB/s).  8,191 tokens of 32 + 32 heads of 64, fp32: forward 44 us (6.2 TB/s), gradient 67 (6.0 TB/s, 90%).  Through shared
 // memory (126 of 128 channels turned, in halves): 139 and 278 us (neighbours: 62 and 103 for 20 of 128).  A decoding step's 512
 // tokens: 6 to 9 us, of which the launch is half.
@@ -36,7 +36,7 @@ constexpr int kStagedThreads = 128;  // of the path through shared memory
 constexpr int kUnroll = 2;           // rows in flight per thread
 constexpr int kRounds = 8;           // heads for which a thread keeps a token's sines
 constexpr int kBwdPerSm = 4, kStagedPerSm = 6;  // CTAs; of the gradient each has its own sums of dw
-// Forward: seven leave 72 registers, of which bf16 spills 56 to 76 bytes, six 80 (16 to 24 bytes).  bf16, 16,384 tokens of 32 +
+// Forward: seven leave 72 registers, of which bf16 spills 56 to 76 bytes, six 80 (8 to 16 bytes).  bf16, 16,384 tokens of 32 +
 // 8 heads of 128: 64.0 us with seven, 62.4 with six; fp32, which spills neither way, 101.2 and 105.4.
 template <typename T>
 constexpr int kFwdPerSm = sizeof(T) == 2 ? 6 : 7;

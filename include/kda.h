@@ -525,8 +525,9 @@ kda_status kda_draft_verify(const int32_t *tokens, const int32_t *cu_nodes, cons
  * kda_rope, and
  *   q_weight, k_weight  [d] of weight_dtype, or NULL: ones
  *   eps   finite, >= 0
- * Norms, weights, sines and products are fp32; the result is rounded to dtype once.  q_out
- * and k_out may be q and k themselves (same stride).
+ * Norms, weights, sines and products are fp32 (the squares of a head and their mean have to lie
+ * within its range); the result is rounded to dtype once.  q_out and k_out may be q and k
+ * themselves (same stride).
  *
  * kda_norm_rope_bwd is the gradient: from q, k (the inputs of the forward) and the gradients
  * of its outputs to d_q, d_k and, where not NULL, d_q_weight, d_k_weight [d] fp32 (sums over
